@@ -420,6 +420,135 @@ moe_status_t moe_aux_finalize(const moe_cfg_t *cfg, long long n_tokens_total,
                               const double *aux_part, float *out, moe_stream_t stream);
 
 /* ---------------------------------------------------------------------------
+ * The training step: the layer's gradients and the update of its parameters. (The
+ * pages train the layer through their framework's automatic differentiation; these
+ * are its formulas.) Token-choice configurations, except moe_expert_ffn_backward,
+ * which takes both routings. Nothing of a forward call is kept: the gradients
+ * recompute what they need from x, the weights and the routing (the taps of
+ * moe_forward), and need a workspace of moe_backward_workspace_size() bytes, prepared
+ * once with moe_workspace_init() and read with moe_last_device_error() like the
+ * forward's (it serves every entry point below; calls that share it must not overlap).
+ * Gradients of weights have cfg->dtype, of biases fp32; each given output is
+ * overwritten (nothing is accumulated into it). */
+
+/* The parameters' gradients: the shapes of moe_weights_t's members; a NULL member is
+ * not computed. b_router is the gradient of logit_bias as well. */
+typedef struct {
+  void *w_router;   /* [E, d] dtype */
+  float *b_router;  /* [E] */
+  void *w1;         /* [E, F, d] dtype */
+  void *w3;         /* [E, F, d] dtype (SwiGLU experts only) */
+  void *w2;         /* [E, d, F] dtype */
+  float *b1;        /* [E, F] (MLP experts with b1 only) */
+  float *b2;        /* [E, d] (MLP experts with b2 only) */
+  void *ws_gate;    /* [n_shared*F_sh, d] dtype (moe_backward only, like the next two) */
+  void *ws_up;      /* [n_shared*F_sh, d] dtype */
+  void *ws_down;    /* [d, n_shared*F_sh] dtype */
+} moe_grads_t;
+
+/* Bytes of workspace the gradient entry points need for `cfg`. */
+moe_status_t moe_backward_workspace_size(const moe_cfg_t *cfg, size_t *bytes);
+
+/* Gradient of moe_combine with respect to y_perm and topk_gate, from dy [T, d] dtype:
+ *   dy_perm[inv[t,s]] = topk_gate[t,s] * dy[t]   (dtype, rounded once), every kept slot
+ *   dgate[t,s] = <dy[t], y_perm[inv[t,s]]>       ([T, k] fp32), 0 for a dropped slot
+ * Either output may be NULL (topk_gate or y_perm, which only that output reads, may
+ * then be NULL too). Rows of dy_perm that no slot owns are left as they were. inv comes
+ * from moe_permute (no row appears twice). The gradient of shared_y is dy itself. */
+moe_status_t moe_combine_backward(const moe_cfg_t *cfg, const void *dy, const void *y_perm,
+                                  const int32_t *inv, const float *topk_gate, void *dy_perm,
+                                  float *dgate, void *ws, size_t ws_bytes, moe_stream_t stream);
+
+/* Gradient of moe_permute's row gather with respect to x:
+ *   dx[t] = sum_{s: inv[t,s] >= 0} dx_perm[inv[t,s]] (+ dx_add[t])
+ * dx_perm [R, d] and dx [T, d] in dtype, dx_add [T, d] fp32 or NULL (the router's share
+ * of the token's gradient, see moe_route_backward). fp32 sums, rounded once. */
+moe_status_t moe_permute_backward(const moe_cfg_t *cfg, const void *dx_perm, const int32_t *inv,
+                                  const float *dx_add, void *dx, void *ws, size_t ws_bytes,
+                                  moe_stream_t stream);
+
+/* Gradient of moe_route and moe_aux_stats. In: x [T, d] and w->w_router (needed for
+ * grads->w_router and dx), logits [T, E] and topk_idx [T, k] (moe_route's outputs), dgate
+ * [T, k] fp32 or NULL (no gradient through the gates), d_losses [2] fp32 (device) or
+ * NULL: the upstream gradients of aux and z_loss (counts [E], before drops, is read only
+ * with it; f is held fixed). Out, each may be NULL: dlogits [T, E] fp32, dx [T, d] fp32
+ * (dlogits W_r, the addend of moe_permute_backward), grads->w_router, grads->b_router
+ * (grads itself may be NULL). The selection has no gradient. */
+moe_status_t moe_route_backward(const moe_cfg_t *cfg, const moe_weights_t *w, const void *x,
+                                const float *logits, const int32_t *topk_idx,
+                                const int32_t *counts, const float *dgate,
+                                const float *d_losses, float *dlogits, float *dx,
+                                const moe_grads_t *grads, void *ws, size_t ws_bytes,
+                                moe_stream_t stream);
+
+/* Gradient of moe_expert_ffn: x_perm, offsets as there, dy_perm [R, d] dtype the
+ * gradient of its rows. Out: dx_perm [R, d] dtype (NULL: not computed; rows past
+ * offsets[E] are left as they were) and grads->w1, w3, w2, b1, b2 (an expert without
+ * rows gets zeros). The pre-activations are recomputed; they and the activation's
+ * gradient stay in fp32 up to one rounding to dtype. Invalid offsets:
+ * MOE_DEVERR_OFFSETS, no row is read, the gradients are zero. */
+moe_status_t moe_expert_ffn_backward(const moe_cfg_t *cfg, const moe_weights_t *w,
+                                     const void *x_perm, const int32_t *offsets,
+                                     const void *dy_perm, void *dx_perm,
+                                     const moe_grads_t *grads, void *ws, size_t ws_bytes,
+                                     moe_stream_t stream);
+
+/* Gradient of moe_forward: from x, dy [T, d] dtype and the forward's routing (taps:
+ * logits, topk_idx, topk_gate, offsets and inv are required INPUTS, counts too with
+ * d_losses; perm is not used) the gradients of x (dx [T, d] dtype, NULL: not computed)
+ * and of the parameters that `grads` names. d_losses as in moe_route_backward. The
+ * gates' weight is applied to the experts' rows in fp32, and the rows of dx are summed
+ * in fp32 before the one rounding. */
+moe_status_t moe_backward(const moe_cfg_t *cfg, const moe_weights_t *w, const void *x,
+                          const moe_taps_t *taps, const void *dy, const float *d_losses,
+                          void *dx, const moe_grads_t *grads, void *ws, size_t ws_bytes,
+                          moe_stream_t stream);
+
+/* Elements that share one scale of an 8-bit optimizer state. */
+#define MOE_ADAMW_BLOCK 256
+
+/* One tensor of moe_adamw_step (n elements, contiguous; n = 0 is skipped). */
+typedef struct {
+  int64_t n;
+  void *param;              /* [n] param_dtype, updated in place */
+  const void *grad;         /* [n] grad_dtype */
+  void *exp_avg;            /* [n] fp32, or e4m3 codes (state_bits 8) */
+  void *exp_avg_sq;         /* [n] fp32: v; or e4m3 codes of sqrt(v) (state_bits 8) */
+  float *exp_avg_scale;     /* [ceil(n / MOE_ADAMW_BLOCK)] fp32 (state_bits 8), else NULL */
+  float *exp_avg_sq_scale;  /* the same for exp_avg_sq */
+  float *master;            /* [n] fp32 copy of a bf16 param that the step works on (param
+                               gets its rounding), or NULL */
+  int32_t param_dtype;      /* MOE_DTYPE_* */
+  int32_t grad_dtype;       /* MOE_DTYPE_* */
+  int32_t state_bits;       /* 32 or 8 */
+} moe_adamw_tensor_t;
+
+/* Hyperparameters. The four device pointers may be NULL; given, they are read when the
+ * kernel runs, so that a captured step can be replayed with other values. */
+typedef struct {
+  double beta1, beta2;       /* in [0, 1) */
+  float lr, eps, weight_decay;
+  int64_t step;              /* 1 for the first step (ignored with step_dev) */
+  const int64_t *step_dev;   /* the step's number */
+  const float *lr_dev;       /* in place of lr */
+  const float *grad_scale;   /* multiplies every gradient (clipping, loss scaling) */
+  const float *found_inf;    /* nonzero: the whole step is skipped */
+} moe_adamw_t;
+
+/* One AdamW step over n_tensors tensors (decoupled weight decay, bias correction):
+ *   m = b1 m + (1 - b1) g;  v = b2 v + (1 - b2) g^2
+ *   p = p (1 - lr wd) - lr m / (1 - b1^t) / (sqrt(v / (1 - b2^t)) + eps)
+ * in fp32. state_bits 8: m = exp_avg * exp_avg_scale and sqrt(v) = exp_avg_sq *
+ * exp_avg_sq_scale, the scale the block's largest magnitude / 448 (at least 2^-100 /
+ * 448); the parameter's step uses the new m and v before their rounding to e4m3, and a
+ * nonzero sqrt(v) keeps at least the smallest code. A gradient that is not finite
+ * spoils its element (an infinite one with 8-bit states its block): found_inf is there
+ * to skip such a step. `tensors` and `opt` are host memory, read before the call returns.
+ * No workspace. Tensors must not overlap. */
+moe_status_t moe_adamw_step(const moe_adamw_tensor_t *tensors, int32_t n_tensors,
+                            const moe_adamw_t *opt, moe_stream_t stream);
+
+/* ---------------------------------------------------------------------------
  * Test hooks for failure detection (no counterpart on the pages). Every pipeline
  * wait inside the tensor-core kernels is bounded; a wait that runs out records
  * MOE_DEVERR_WAIT_TIMEOUT (info = the wait's site), lets the copies and MMAs the CTA

@@ -32,8 +32,13 @@ EXPORTED = ("moe_workspace_size", "moe_workspace_init", "moe_route", "moe_route_
             "moe_expert_ffn", "moe_combine", "moe_aux_stats", "moe_forward",
             "moe_route_shard", "moe_permute_shard", "moe_forward_shard", "moe_aux_finalize",
             "moe_forward_staged", "moe_noise_draws", "moe_route_noisy_seeded",
-            "moe_forward_noisy_seeded", "moe_test_set_wait_limit", "moe_test_withhold_load",
+            "moe_forward_noisy_seeded", "moe_backward_workspace_size", "moe_combine_backward",
+            "moe_permute_backward", "moe_route_backward", "moe_expert_ffn_backward",
+            "moe_backward", "moe_adamw_step", "moe_test_set_wait_limit", "moe_test_withhold_load",
             "moe_last_device_error", "moe_status_string")
+
+ADAMW_BLOCK = 256  # MOE_ADAMW_BLOCK: elements that share a scale of an 8-bit state
+_ADAMW_DTYPES = {torch.float32: synth.DT_F32, torch.bfloat16: synth.DT_BF16}
 
 # stages of one layer call (MOE_STAGE_*), in launch order
 STAGES = ("route", "scan", "permute", "shared_ffn", "expert_ffn", "combine")
@@ -73,6 +78,27 @@ class MoeShard(ctypes.Structure):
 
 class MoeStageEvents(ctypes.Structure):
     _fields_ = [("ev", ctypes.c_void_p * (len(STAGES) + 1))]
+
+
+class MoeGrads(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in
+                ("w_router", "b_router", "w1", "w3", "w2", "b1", "b2", "ws_gate", "ws_up",
+                 "ws_down")]
+
+
+class MoeAdamWTensor(ctypes.Structure):
+    _fields_ = [("n", ctypes.c_int64)] + [(n, ctypes.c_void_p) for n in
+                ("param", "grad", "exp_avg", "exp_avg_sq", "exp_avg_scale", "exp_avg_sq_scale",
+                 "master")] + [(n, ctypes.c_int32) for n in
+                               ("param_dtype", "grad_dtype", "state_bits")]
+
+
+class MoeAdamW(ctypes.Structure):
+    _fields_ = [("beta1", ctypes.c_double), ("beta2", ctypes.c_double), ("lr", ctypes.c_float),
+                ("eps", ctypes.c_float), ("weight_decay", ctypes.c_float),
+                ("step", ctypes.c_int64), ("step_dev", ctypes.c_void_p),
+                ("lr_dev", ctypes.c_void_p), ("grad_scale", ctypes.c_void_p),
+                ("found_inf", ctypes.c_void_p)]
 
 
 class MoeNoise(ctypes.Structure):
@@ -118,6 +144,16 @@ def load() -> ctypes.CDLL:
                                    P],
         "moe_forward_noisy_seeded": [cfgp, wp, P, ctypes.c_uint64, ctypes.c_uint64, P, P,
                                      ctypes.POINTER(MoeTaps), P, S, P],
+        "moe_backward_workspace_size": [cfgp, ctypes.POINTER(ctypes.c_size_t)],
+        "moe_combine_backward": [cfgp, P, P, P, P, P, P, P, S, P],
+        "moe_permute_backward": [cfgp, P, P, P, P, P, S, P],
+        "moe_route_backward": [cfgp, wp, P, P, P, P, P, P, P, P, ctypes.POINTER(MoeGrads), P, S,
+                               P],
+        "moe_expert_ffn_backward": [cfgp, wp, P, P, P, P, ctypes.POINTER(MoeGrads), P, S, P],
+        "moe_backward": [cfgp, wp, P, ctypes.POINTER(MoeTaps), P, P, P,
+                         ctypes.POINTER(MoeGrads), P, S, P],
+        "moe_adamw_step": [ctypes.POINTER(MoeAdamWTensor), ctypes.c_int32,
+                           ctypes.POINTER(MoeAdamW), P],
         "moe_test_set_wait_limit": [ctypes.c_uint64],
         "moe_test_withhold_load": [ctypes.c_int32],
         "moe_last_device_error": [P, ctypes.POINTER(ctypes.c_int32),
@@ -166,6 +202,21 @@ def check_rows(t: Optional[torch.Tensor], rows: int, cols: int, name: str):
                          f"not {tuple(t.shape)}")
 
 
+def check_tensor(t: Optional[torch.Tensor], shape, dtype: torch.dtype, name: str, device,
+                 optional: bool = False):
+    """A tensor handed to the training entry points: contiguous, of this shape and dtype,
+    on `device` (the C ABI sees none of these)."""
+    if t is None:
+        if optional:
+            return
+        raise ValueError(f"{name} is missing")
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {tuple(shape)} {dtype} tensor, not "
+                         f"{tuple(t.shape)} {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not on {device}")
+
+
 def _stream():
     return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
 
@@ -204,8 +255,16 @@ def workspace_size(cfg: MoeCfg) -> int:
     return n.value
 
 
-def new_workspace(cfg: MoeCfg, device="cuda") -> torch.Tensor:
-    nbytes = workspace_size(cfg)
+def backward_workspace_size(cfg: MoeCfg) -> int:
+    n = ctypes.c_size_t(0)
+    _check(load().moe_backward_workspace_size(ctypes.byref(cfg), ctypes.byref(n)),
+           "moe_backward_workspace_size")
+    return n.value
+
+
+def new_workspace(cfg: MoeCfg, device="cuda", backward: bool = False) -> torch.Tensor:
+    """A prepared workspace of the forward entry points, or (backward) of the gradients'."""
+    nbytes = backward_workspace_size(cfg) if backward else workspace_size(cfg)
     ws = torch.empty(nbytes + 256, dtype=torch.uint8, device=device)
     off = (-ws.data_ptr()) % 256
     ws = ws[off:off + nbytes]
@@ -230,6 +289,7 @@ class MoELayer:
         self.weights = MoeWeights(**{k: _ptr(self.p.get(k)) for k, _ in MoeWeights._fields_})
         self.ws = new_workspace(self.cfg, self.device)
         self.lib = load()
+        self._bws = None
 
     # -------------------------------------------------------------- whole layer
     def forward(self, x: torch.Tensor, y: Optional[torch.Tensor] = None,
@@ -395,9 +455,156 @@ class MoELayer:
                "moe_aux_finalize")
         return out
 
+    # ------------------------------------------------------------ the training step
+    @property
+    def bws(self) -> torch.Tensor:
+        """The workspace of the gradients, made at the first use (so make that use before
+        a capture). Calls that share it must not overlap."""
+        if self._bws is None:
+            with torch.cuda.device(self.ws.device):
+                self._bws = new_workspace(self.cfg, self.ws.device, backward=True)
+        return self._bws
+
+    def _call(self, name: str, *args):
+        """lib.name(cfg, *args, workspace, its size, stream) on this layer's device, on
+        that device's current stream."""
+        bws = self.bws
+        with torch.cuda.device(bws.device):
+            _check(getattr(self.lib, name)(ctypes.byref(self.cfg), *args, _ptr(bws),
+                                           bws.numel(), _stream()), name)
+
+    def _want(self, t, shape, name, dtype=None, optional=False):
+        check_tensor(t, shape, dtype or self.w.torch_dtype, name, self.ws.device, optional)
+
+    def grad_shapes(self) -> dict:
+        """name -> (shape, dtype) of every parameter's gradient: the parameters this layer
+        has (b_router also stands for logit_bias)."""
+        w, dt, f32 = self.w, self.w.torch_dtype, torch.float32
+        E, d, F, Fs = w.n_experts, w.d_model, w.d_ff, w.n_shared * w.d_ff_shared
+        shapes = {"w_router": ((E, d), dt), "b_router": ((E,), f32), "w1": ((E, F, d), dt),
+                  "w3": ((E, F, d), dt), "w2": ((E, d, F), dt), "b1": ((E, F), f32),
+                  "b2": ((E, d), f32), "ws_gate": ((Fs, d), dt), "ws_up": ((Fs, d), dt),
+                  "ws_down": ((d, Fs), dt)}
+        has = {n for n in shapes if self.p.get(n) is not None}
+        if self.p.get("w_router") is not None:
+            has.add("b_router")
+        return {n: s for n, s in shapes.items() if n in has}
+
+    def new_grads(self) -> dict:
+        """Buffers for the gradients of this layer's parameters."""
+        return {n: torch.empty(s, dtype=dt, device=self.ws.device)
+                for n, (s, dt) in self.grad_shapes().items()}
+
+    def _grads(self, grads: Optional[dict], names) -> MoeGrads:
+        shapes, out = self.grad_shapes(), MoeGrads()
+        for n, t in (grads or {}).items():
+            if t is None or n not in names:
+                continue
+            if n not in shapes:
+                raise ValueError(f"this layer has no {n}")
+            self._want(t, shapes[n][0], f"grads[{n!r}]", shapes[n][1])
+            setattr(out, n, t.data_ptr())
+        return out
+
+    def combine_backward(self, dy: torch.Tensor, y_perm: Optional[torch.Tensor],
+                         inv: torch.Tensor, topk_gate: Optional[torch.Tensor],
+                         dy_perm: Optional[torch.Tensor], dgate: Optional[torch.Tensor]):
+        """Gradient of combine: dy [T, d] -> dy_perm [R, d] and dgate [T, k] (each may be
+        None; y_perm is read for dgate, topk_gate for dy_perm)."""
+        T, d, k, i32, f32 = self.w.T, self.w.d_model, self.w.top_k, torch.int32, torch.float32
+        self._want(dy, (T, d), "dy")
+        self._want(y_perm, (T * k, d), "y_perm", optional=dgate is None)
+        self._want(inv, (T * k,), "inv", i32)
+        self._want(topk_gate, (T, k), "topk_gate", f32, optional=dy_perm is None)
+        self._want(dy_perm, (T * k, d), "dy_perm", optional=True)
+        self._want(dgate, (T, k), "dgate", f32, optional=True)
+        self._call("moe_combine_backward", _ptr(dy), _ptr(y_perm), _ptr(inv), _ptr(topk_gate),
+                   _ptr(dy_perm), _ptr(dgate))
+
+    def permute_backward(self, dx_perm: torch.Tensor, inv: torch.Tensor,
+                         dx_add: Optional[torch.Tensor], dx: torch.Tensor):
+        """Gradient of permute: dx_perm [R, d] -> dx [T, d] (plus dx_add [T, d] fp32)."""
+        T, d, k = self.w.T, self.w.d_model, self.w.top_k
+        self._want(dx_perm, (T * k, d), "dx_perm")
+        self._want(inv, (T * k,), "inv", torch.int32)
+        self._want(dx_add, (T, d), "dx_add", torch.float32, optional=True)
+        self._want(dx, (T, d), "dx")
+        self._call("moe_permute_backward", _ptr(dx_perm), _ptr(inv), _ptr(dx_add), _ptr(dx))
+
+    def route_backward(self, x: Optional[torch.Tensor], logits: torch.Tensor,
+                       topk_idx: torch.Tensor, counts: Optional[torch.Tensor],
+                       dgate: Optional[torch.Tensor], d_losses: Optional[torch.Tensor],
+                       dlogits: Optional[torch.Tensor], dx: Optional[torch.Tensor],
+                       grads: Optional[dict] = None):
+        """Gradient of route and aux_stats: from dgate [T, k] and d_losses [2] (the upstream
+        gradients of aux and z_loss, with counts) the gradients of the logits [T, E] fp32,
+        of x ([T, d] fp32) and grads["w_router"], grads["b_router"]."""
+        T, d, E, k = self.w.T, self.w.d_model, self.w.n_experts, self.w.top_k
+        i32, f32 = torch.int32, torch.float32
+        g = self._grads(grads, ("w_router", "b_router"))
+        self._want(x, (T, d), "x", optional=not g.w_router)
+        self._want(logits, (T, E), "logits", f32)
+        self._want(topk_idx, (T, k), "topk_idx", i32)
+        self._want(counts, (E,), "counts", i32, optional=d_losses is None)
+        self._want(dgate, (T, k), "dgate", f32, optional=True)
+        self._want(d_losses, (2,), "d_losses", f32, optional=True)
+        self._want(dlogits, (T, E), "dlogits", f32, optional=True)
+        self._want(dx, (T, d), "dx", f32, optional=True)
+        self._call("moe_route_backward", ctypes.byref(self.weights), _ptr(x), _ptr(logits),
+                   _ptr(topk_idx), _ptr(counts), _ptr(dgate), _ptr(d_losses), _ptr(dlogits),
+                   _ptr(dx), ctypes.byref(g))
+
+    def expert_ffn_backward(self, x_perm: torch.Tensor, offsets: torch.Tensor,
+                            dy_perm: torch.Tensor, dx_perm: Optional[torch.Tensor],
+                            grads: Optional[dict] = None):
+        """Gradient of expert_ffn: dx_perm [R, d] and grads["w1"], ["w3"], ["w2"], ["b1"],
+        ["b2"] (those that `grads` names)."""
+        R, d = expert_rows(self.cfg), self.w.d_model
+        self._want(x_perm, (R, d), "x_perm")
+        self._want(offsets, (self.w.n_experts + 1,), "offsets", torch.int32)
+        self._want(dy_perm, (R, d), "dy_perm")
+        self._want(dx_perm, (R, d), "dx_perm", optional=True)
+        g = self._grads(grads, ("w1", "w3", "w2", "b1", "b2"))
+        self._call("moe_expert_ffn_backward", ctypes.byref(self.weights), _ptr(x_perm),
+                   _ptr(offsets), _ptr(dy_perm), _ptr(dx_perm), ctypes.byref(g))
+
+    def backward(self, x: torch.Tensor, dy: torch.Tensor, taps: dict,
+                 dx: Optional[torch.Tensor] = None, grads: Optional[dict] = None,
+                 d_losses: Optional[torch.Tensor] = None):
+        """Gradient of forward: `taps` as the forward filled them (new_taps); returns (dx,
+        grads), into the buffers given or new ones (a dict without some names: those
+        gradients are not computed)."""
+        T, d, E, k = self.w.T, self.w.d_model, self.w.n_experts, self.w.top_k
+        i32, f32 = torch.int32, torch.float32
+        self._want(x, (T, d), "x")
+        self._want(dy, (T, d), "dy")
+        for n, s, t in (("logits", (T, E), f32), ("topk_idx", (T, k), i32),
+                        ("topk_gate", (T, k), f32), ("offsets", (E + 1,), i32),
+                        ("inv", (T * k,), i32)):
+            self._want(taps.get(n), s, f"taps[{n!r}]", t)
+        self._want(taps.get("counts"), (E,), "taps['counts']", i32, optional=d_losses is None)
+        self._want(d_losses, (2,), "d_losses", f32, optional=True)
+        if dx is None:
+            dx = torch.empty_like(x)
+        self._want(dx, (T, d), "dx")
+        if grads is None:
+            grads = self.new_grads()
+        g = self._grads(grads, tuple(self.grad_shapes()) + tuple(grads))
+        tp = _taps(taps)
+        self._call("moe_backward", ctypes.byref(self.weights), _ptr(x), ctypes.byref(tp),
+                   _ptr(dy), _ptr(d_losses), _ptr(dx), ctypes.byref(g))
+        return dx, grads
+
+    def last_backward_error(self):
+        """(code, info) of the gradients' workspace, cleared (see last_device_error)."""
+        return self._device_error(self.bws)
+
     def last_device_error(self):
+        return self._device_error(self.ws)
+
+    def _device_error(self, ws):
         code, info = ctypes.c_int32(0), ctypes.c_int32(0)
-        st = self.lib.moe_last_device_error(_ptr(self.ws), ctypes.byref(code), ctypes.byref(info),
+        st = self.lib.moe_last_device_error(_ptr(ws), ctypes.byref(code), ctypes.byref(info),
                                             _stream())
         if st not in (MOE_OK, 6):
             raise MoeError(st, "moe_last_device_error")
@@ -410,6 +617,117 @@ def noise_draws(n_tokens: int, n_experts: int, seed: int, offset: int, eps: torc
     (the uint32 bit patterns), both on the current device and stream."""
     _check(load().moe_noise_draws(n_tokens, n_experts, seed, offset, _ptr(eps), _ptr(raw),
                                   _stream()), "moe_noise_draws")
+
+
+class AdamW:
+    """AdamW over a list of CUDA tensors on one device (moe_adamw_step), updated in place.
+
+    ``state_bits``: 32, or 8 (e4m3 with one fp32 scale for each ADAMW_BLOCK elements).
+    ``master``: keep fp32 copies of the bf16 parameters, which the step works on.
+    ``state`` continues a former run: a dict of ``step`` and lists ``exp_avg``,
+    ``exp_avg_sq``, with 8 bits ``exp_avg_scale`` and ``exp_avg_sq_scale``, and optionally
+    ``master`` (None where a parameter has none), used as they are; `state_dict` gives one.
+    With 8 bits exp_avg_sq holds the root of the second moment.
+    """
+
+    def __init__(self, params, lr: float = 1e-3, betas=(0.9, 0.999), eps: float = 1e-8,
+                 weight_decay: float = 1e-2, state_bits: int = 32, master: bool = False,
+                 state: Optional[dict] = None):
+        self.params = list(params.values() if isinstance(params, dict) else params)
+        self.lr, self.betas, self.eps, self.weight_decay = lr, betas, eps, weight_decay
+        if not self.params:
+            raise ValueError("no parameters")
+        self.device = self.params[0].device
+        if self.device.type != "cuda":
+            raise ValueError("the parameters must be CUDA tensors")
+        if state is None:
+            if state_bits not in (8, 32):
+                raise ValueError("state_bits must be 32 or 8")
+            self.bits, self.t = state_bits, 0
+            dt = torch.float32 if state_bits == 32 else torch.float8_e4m3fn
+            new = lambda p: torch.zeros(p.shape, dtype=dt, device=p.device)  # noqa: E731
+            self.exp_avg = [new(p) for p in self.params]
+            self.exp_avg_sq = [new(p) for p in self.params]
+            self.exp_avg_scale = self.exp_avg_sq_scale = None
+            if state_bits == 8:
+                scale = lambda p: torch.zeros(-(-p.numel() // ADAMW_BLOCK), device=p.device)  # noqa: E731
+                self.exp_avg_scale = [scale(p) for p in self.params]
+                self.exp_avg_sq_scale = [scale(p) for p in self.params]
+            self.master = [p.float() if master and p.dtype == torch.bfloat16 else None
+                           for p in self.params]
+        else:
+            self.t = int(state["step"])
+            self.exp_avg, self.exp_avg_sq = list(state["exp_avg"]), list(state["exp_avg_sq"])
+            self.exp_avg_scale = state.get("exp_avg_scale")
+            self.exp_avg_sq_scale = state.get("exp_avg_sq_scale")
+            self.bits = 32 if self.exp_avg_scale is None else 8
+            self.master = list(state.get("master") or [None] * len(self.params))
+        self._lib = load()
+        self._batch = (MoeAdamWTensor * len(self.params))()
+        dt = torch.float32 if self.bits == 32 else torch.float8_e4m3fn
+        lists = [self.exp_avg, self.exp_avg_sq, self.master]
+        if self.bits == 8:
+            lists += [self.exp_avg_scale, self.exp_avg_sq_scale]
+        if any(x is None or len(x) != len(self.params) for x in lists):
+            raise ValueError("the state has not one entry for each parameter")
+        for i, p in enumerate(self.params):
+            if p.dtype not in _ADAMW_DTYPES:
+                raise ValueError(f"parameter {i} is {p.dtype}: fp32 or bf16 are supported")
+            check_tensor(p, p.shape, p.dtype, f"parameter {i}", self.device)
+            check_tensor(self.exp_avg[i], p.shape, dt, f"exp_avg[{i}]", self.device)
+            check_tensor(self.exp_avg_sq[i], p.shape, dt, f"exp_avg_sq[{i}]", self.device)
+            check_tensor(self.master[i], p.shape, torch.float32, f"master[{i}]", self.device,
+                         optional=True)
+            if self.master[i] is not None and p.dtype == torch.float32:
+                raise ValueError(f"master[{i}]: parameter {i} is fp32 already")
+            e = self._batch[i]
+            e.n, e.param, e.exp_avg, e.exp_avg_sq = (p.numel(), p.data_ptr(),
+                                                     self.exp_avg[i].data_ptr(),
+                                                     self.exp_avg_sq[i].data_ptr())
+            e.master = None if self.master[i] is None else self.master[i].data_ptr()
+            if self.bits == 8:
+                n = (-(-p.numel() // ADAMW_BLOCK),)
+                for name, x in (("exp_avg_scale", self.exp_avg_scale[i]),
+                                ("exp_avg_sq_scale", self.exp_avg_sq_scale[i])):
+                    check_tensor(x, n, torch.float32, f"{name}[{i}]", self.device)
+                    setattr(e, name, x.data_ptr())
+            e.param_dtype, e.state_bits = _ADAMW_DTYPES[p.dtype], self.bits
+
+    def step(self, grads, grad_scale: Optional[torch.Tensor] = None,
+             found_inf: Optional[torch.Tensor] = None, step: Optional[torch.Tensor] = None,
+             lr: Optional[torch.Tensor] = None):
+        """One step from ``grads`` (a list in the parameters' order, or a dict's values).
+        Device scalars, read when the kernel runs: ``grad_scale`` multiplies the gradients,
+        ``found_inf`` nonzero skips the update (the step still counts), ``step`` (int64) and
+        ``lr`` (fp32) take the place of the counter and of self.lr (a captured step needs
+        them to move)."""
+        grads = list(grads.values() if isinstance(grads, dict) else grads)
+        if len(grads) != len(self.params):
+            raise ValueError(f"{len(grads)} gradients for {len(self.params)} parameters")
+        for i, (g, p, e) in enumerate(zip(grads, self.params, self._batch)):
+            if g.dtype not in _ADAMW_DTYPES:
+                raise ValueError(f"gradient {i} is {g.dtype}: fp32 or bf16 are supported")
+            check_tensor(g, p.shape, g.dtype, f"gradient {i}", self.device)
+            e.grad, e.grad_dtype = g.data_ptr(), _ADAMW_DTYPES[g.dtype]
+        o = MoeAdamW(beta1=self.betas[0], beta2=self.betas[1], lr=self.lr, eps=self.eps,
+                     weight_decay=self.weight_decay, step=self.t + 1)
+        for name, t, dt in (("grad_scale", grad_scale, torch.float32),
+                            ("found_inf", found_inf, torch.float32),
+                            ("step_dev", step, torch.int64), ("lr_dev", lr, torch.float32)):
+            if t is not None:
+                if t.numel() != 1:
+                    raise ValueError(f"{name} must hold one value")
+                check_tensor(t, t.shape, dt, name, self.device)
+                setattr(o, name, t.data_ptr())
+        with torch.cuda.device(self.device):
+            _check(self._lib.moe_adamw_step(self._batch, len(self.params), ctypes.byref(o),
+                                            _stream()), "moe_adamw_step")
+        self.t += 1
+
+    def state_dict(self) -> dict:
+        return {"step": self.t, "exp_avg": self.exp_avg, "exp_avg_sq": self.exp_avg_sq,
+                "exp_avg_scale": self.exp_avg_scale, "exp_avg_sq_scale": self.exp_avg_sq_scale,
+                "master": self.master}
 
 
 def shared_as_experts(layer: MoELayer):

@@ -8,9 +8,8 @@
 
 #include <nvtx3/nvToolsExt.h>
 
+#include "api.cuh"
 #include "shard.cuh"
-
-#define MOE_API extern "C" __attribute__((visibility("default")))
 
 namespace moe {
 
@@ -29,13 +28,10 @@ struct Layout {
   size_t total;
 };
 
-size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
+}  // namespace
 
-bool expert_choice(const moe_cfg_t &c) { return c.routing == MOE_ROUTING_EXPERT_CHOICE; }
 long long ec_picks(const moe_cfg_t &c);
 
-// rows of the expert-contiguous buffers (x_perm, h, y_perm): T*k (token choice) or
-// E*C (expert choice)
 long long expert_rows(const moe_cfg_t &c) {
   return expert_choice(c) ? (long long)c.n_experts * ec_picks(c)
                           : (long long)c.n_tokens * c.top_k;
@@ -47,6 +43,8 @@ long long ec_picks(const moe_cfg_t &c) {
   const double v = floor((double)c.capacity_factor * (double)c.n_tokens / (double)c.n_experts);
   return v > 1e18 ? (long long)1e18 : (long long)v;
 }
+
+namespace {
 
 Layout layout_for(const moe_cfg_t &c) {
   const size_t T = (size_t)c.n_tokens, E = (size_t)c.n_experts, k = (size_t)c.top_k;
@@ -114,7 +112,7 @@ unsigned *scan_ticket(void *ws, const Layout &L) {
   return reinterpret_cast<unsigned *>(at<int32_t>(ws, L, B_ERR) + 2);
 }
 
-bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+}  // namespace
 
 moe_status_t check_cfg(const moe_cfg_t *c) {
   if (c == nullptr) return MOE_ERR_INVALID_ARG;
@@ -156,6 +154,7 @@ moe_status_t check_cfg(const moe_cfg_t *c) {
   return MOE_OK;
 }
 
+namespace {
 moe_status_t check_ws(const moe_cfg_t *c, const void *ws, size_t ws_bytes) {
   if (ws == nullptr) return MOE_ERR_INVALID_ARG;
   if (!aligned(ws, 256)) return MOE_ERR_MISALIGNED;
@@ -163,7 +162,8 @@ moe_status_t check_ws(const moe_cfg_t *c, const void *ws, size_t ws_bytes) {
   return MOE_OK;
 }
 
-// every pointer in the list: non-null required unless allowed, 16-byte aligned
+}  // namespace
+
 moe_status_t check_ptrs(std::initializer_list<std::pair<const void *, bool>> ps) {
   for (auto &p : ps) {
     if (p.first == nullptr) {
@@ -190,14 +190,7 @@ moe_status_t check_shared_weights(const moe_cfg_t *c, const moe_weights_t *w) {
   return check_ptrs({{w->ws_gate, true}, {w->ws_up, true}, {w->ws_down, true}});
 }
 
-moe_status_t cuda_status(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA; }
-
-#define MOE_TRY(expr)                        \
-  do {                                       \
-    moe_status_t s_ = (expr);                \
-    if (s_ != MOE_OK) return s_;             \
-  } while (0)
-#define MOE_CUDA(expr) MOE_TRY(cuda_status(expr))
+namespace {
 
 // Stage boundaries of one layer call: an event (when the caller gave one) and an
 // NVTX range per stage. Stages are entered in increasing order; skipped stages
@@ -261,12 +254,6 @@ moe_status_t check_shard(const moe_cfg_t &c, const moe_shard_t *sh) {
   if (sh->counts_all == nullptr) return MOE_ERR_INVALID_ARG;
   if (expert_choice(c)) return MOE_ERR_INVALID_ARG;  // picks are per expert over all tokens
   return MOE_OK;
-}
-
-int m_tiles_ub(long long rows, int groups) {
-  long long ub = ceil_div((int)rows, kRowTile) + groups;
-  if (ub > rows) ub = rows;
-  return (int)ub;
 }
 
 // Process-wide test settings of the single-CTA tensor-core GEMM (see

@@ -1,0 +1,302 @@
+// Gradients of the token movement: the gate-weighted combine and the
+// expert-contiguous permutation (and the row gather that the whole layer's
+// gradient starts with).
+//
+//   combine  y[t] = sum_s g[t,s] Y[inv[t,s]]   dY[inv[t,s]] = g[t,s] dy[t]
+//                                              dg[t,s] = <dy[t], Y[inv[t,s]]>
+//   permute  X[inv[t,s]] = x[t]                dx[t] = sum_s dX[inv[t,s]]
+//
+// Both are gathers over (token, slot), like the forward combine: every output is
+// written by one warp (or the warps of one block), so there are no atomics and the
+// result does not depend on the schedule. A dropped slot (inv < 0) reads and writes
+// no row and has a zero gate gradient.
+#include "grad.cuh"
+
+namespace moe {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+
+// the row of pair p, or -1: dropped, or outside [0, R) (recorded)
+__device__ __forceinline__ int checked_row(const int32_t *inv, size_t p, int R, int32_t *err,
+                                           bool report) {
+  int r = inv[p];
+  if (r < -1 || r >= R) {
+    if (report) report_error(err, MOE_DEVERR_ROW_INDEX, (int32_t)p);
+    r = -1;
+  }
+  return r;
+}
+
+// `wpt` warps of a block share a token: warp `sub` of them takes the vectors
+// 32 (sub + wpt i) + lane. NB vectors of dy and of each kept slot's row are requested
+// before any is used.
+template <typename T, int KMAX, int NB>
+__global__ void __launch_bounds__(kThreads) k_combine_bwd(CombineBwdArgs a, int wpt) {
+  constexpr int VE = Elem<T>::kPerVec;
+  __shared__ float red[kWarps][KMAX];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int sub = warp % wpt;
+  const int t = blockIdx.x * (kWarps / wpt) + warp / wpt;
+  pdl_wait();
+  pdl_trigger();
+  const int k = a.k;
+  const bool live = t < a.T;
+  int row[KMAX];
+  float g[KMAX], dot[KMAX];
+#pragma unroll
+  for (int s = 0; s < KMAX; ++s) {
+    row[s] = -1;
+    g[s] = dot[s] = 0.f;
+    if (live && s < k) {
+      row[s] = checked_row(a.inv, (size_t)t * k + s, a.R, a.err, lane == 0 && sub == 0);
+      if (a.dy_perm) g[s] = a.gate[(size_t)t * k + s];
+    }
+  }
+  const int nvec = a.d / VE;
+  const uint4 *dy = reinterpret_cast<const uint4 *>(static_cast<const T *>(a.dy) + (size_t)t * a.d);
+  const T *yp = static_cast<const T *>(a.y_perm);
+  T *out = static_cast<T *>(a.dy_perm);
+  bool any = false;
+#pragma unroll
+  for (int s = 0; s < KMAX; ++s) any |= row[s] >= 0;
+  for (int v0 = sub * 32 + lane; any && v0 < nvec; v0 += 32 * wpt * NB) {
+    uint4 q[NB], u[KMAX][NB];
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      const int v = v0 + 32 * wpt * b;
+      q[b] = v < nvec ? __ldg(dy + v) : make_uint4(0u, 0u, 0u, 0u);
+    }
+    if (a.dgate) {
+#pragma unroll
+      for (int s = 0; s < KMAX; ++s)
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          const int v = v0 + 32 * wpt * b;
+          u[s][b] = (row[s] >= 0 && v < nvec)
+                        ? __ldg(reinterpret_cast<const uint4 *>(yp + (size_t)row[s] * a.d) + v)
+                        : make_uint4(0u, 0u, 0u, 0u);
+        }
+    }
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      const int v = v0 + 32 * wpt * b;
+      if (v >= nvec) break;
+      float f[VE];
+      unpack16(q[b], f);
+#pragma unroll
+      for (int s = 0; s < KMAX; ++s) {
+        if (row[s] < 0) continue;
+        if (a.dgate) {
+          float y[VE];
+          unpack16(u[s][b], y);
+#pragma unroll
+          for (int i = 0; i < VE; ++i) dot[s] = fmaf(f[i], y[i], dot[s]);
+        }
+        if (out) {
+          float o[VE];
+#pragma unroll
+          for (int i = 0; i < VE; ++i) o[i] = g[s] * f[i];
+          reinterpret_cast<uint4 *>(out + (size_t)row[s] * a.d)[v] = pack16(o);
+        }
+      }
+    }
+  }
+  if (a.dgate == nullptr) return;
+#pragma unroll
+  for (int s = 0; s < KMAX; ++s) dot[s] = warp_sum(dot[s]);
+  if (wpt > 1) {
+    if (lane == 0) {
+#pragma unroll
+      for (int s = 0; s < KMAX; ++s) red[warp][s] = dot[s];
+    }
+    __syncthreads();
+    if (sub == 0) {
+#pragma unroll
+      for (int s = 0; s < KMAX; ++s)
+        for (int w = 1; w < wpt; ++w) dot[s] += red[warp + w][s];
+    }
+  }
+  if (live && sub == 0 && lane == 0) {
+#pragma unroll
+    for (int s = 0; s < KMAX; ++s)
+      if (s < k) a.dgate[(size_t)t * k + s] = dot[s];
+  }
+}
+
+// 8 fp32 values (or 4) at a row's vector v: VE of them, from 16-byte loads
+template <int VE>
+__device__ __forceinline__ void load_f32(const float *p, float (&f)[VE]) {
+#pragma unroll
+  for (int i = 0; i < VE; i += 4) {
+    const float4 q = __ldg(reinterpret_cast<const float4 *>(p + i));
+    f[i] = q.x; f[i + 1] = q.y; f[i + 2] = q.z; f[i + 3] = q.w;
+  }
+}
+__device__ __forceinline__ void load_row(const __nv_bfloat16 *p, float (&f)[8]) {
+  unpack16(__ldg(reinterpret_cast<const uint4 *>(p)), f);
+}
+template <int VE>
+__device__ __forceinline__ void load_row(const float *p, float (&f)[VE]) { load_f32(p, f); }
+
+// dx[t] = the kept slots' rows in slot order, then the addends; summed in fp32 and
+// rounded once. TI: the rows' type.
+template <typename T, typename TI, int KMAX, int NB>
+__global__ void __launch_bounds__(kThreads) k_permute_bwd(PermuteBwdArgs a, int wpt) {
+  constexpr int VE = Elem<T>::kPerVec;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int sub = warp % wpt;
+  const int t = blockIdx.x * (kWarps / wpt) + warp / wpt;
+  pdl_wait();
+  pdl_trigger();
+  if (t >= a.T) return;
+  int row[KMAX];
+#pragma unroll
+  for (int s = 0; s < KMAX; ++s)
+    row[s] = s < a.k ? checked_row(a.inv, (size_t)t * a.k + s, a.R, a.err, lane == 0 && sub == 0)
+                     : -1;
+  const TI *xp = static_cast<const TI *>(a.dx_perm);
+  T *dx = static_cast<T *>(a.dx) + (size_t)t * a.d;
+  const int nvec = a.d / VE;
+  for (int v0 = sub * 32 + lane; v0 < nvec; v0 += 32 * wpt * NB) {
+    float f[KMAX][NB][VE], add[2][NB][VE];
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      const int v = v0 + 32 * wpt * b;
+      const bool in = v < nvec;
+#pragma unroll
+      for (int s = 0; s < KMAX; ++s)
+        if (row[s] >= 0 && in) load_row(xp + (size_t)row[s] * a.d + (size_t)v * VE, f[s][b]);
+      if (a.add0 && in) load_f32(a.add0 + (size_t)t * a.d + (size_t)v * VE, add[0][b]);
+      if (a.add1 && in) load_f32(a.add1 + (size_t)t * a.d + (size_t)v * VE, add[1][b]);
+    }
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      const int v = v0 + 32 * wpt * b;
+      if (v >= nvec) break;
+      float o[VE];
+#pragma unroll
+      for (int i = 0; i < VE; ++i) o[i] = 0.f;
+#pragma unroll
+      for (int s = 0; s < KMAX; ++s)
+        if (row[s] >= 0) {
+#pragma unroll
+          for (int i = 0; i < VE; ++i) o[i] += f[s][b][i];
+        }
+      if (a.add0) {
+#pragma unroll
+        for (int i = 0; i < VE; ++i) o[i] += add[0][b][i];
+      }
+      if (a.add1) {
+#pragma unroll
+        for (int i = 0; i < VE; ++i) o[i] += add[1][b][i];
+      }
+      reinterpret_cast<uint4 *>(dx)[v] = pack16(o);
+    }
+  }
+}
+
+__global__ void __launch_bounds__(kThreads) k_gather_rows(GatherRowsArgs a, int wpt) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int sub = warp % wpt;
+  const int t = blockIdx.x * (kWarps / wpt) + warp / wpt;
+  pdl_wait();
+  pdl_trigger();
+  if (t >= a.T) return;
+  int row[kMaxTopK];
+  bool any = false;
+#pragma unroll
+  for (int s = 0; s < kMaxTopK; ++s) {
+    row[s] = -1;
+    if (s < a.k) {
+      const size_t p = (size_t)t * a.k + s;
+      row[s] = checked_row(a.inv, p, a.R, a.err, lane == 0 && sub == 0);
+      if (row[s] >= 0 && lane == 0 && sub == 0) a.row_w[row[s]] = a.gate[p];
+    }
+    any |= row[s] >= 0;
+  }
+  if (!any) return;
+  const int nvec = a.row_bytes / 16;
+  const uint4 *x = reinterpret_cast<const uint4 *>(static_cast<const char *>(a.x) +
+                                                   (size_t)t * a.row_bytes);
+  const uint4 *dy = reinterpret_cast<const uint4 *>(static_cast<const char *>(a.dy) +
+                                                    (size_t)t * a.row_bytes);
+  constexpr int NB = 4;
+  for (int v0 = sub * 32 + lane; v0 < nvec; v0 += 32 * wpt * NB) {
+    uint4 p[NB], q[NB];
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      const int v = v0 + 32 * wpt * b;
+      if (v < nvec) {
+        p[b] = __ldg(x + v);
+        q[b] = __ldg(dy + v);
+      }
+    }
+#pragma unroll
+    for (int s = 0; s < kMaxTopK; ++s) {
+      if (row[s] < 0) continue;
+      uint4 *xo = reinterpret_cast<uint4 *>(static_cast<char *>(a.x_perm) +
+                                            (size_t)row[s] * a.row_bytes);
+      uint4 *yo = reinterpret_cast<uint4 *>(static_cast<char *>(a.dy_perm) +
+                                            (size_t)row[s] * a.row_bytes);
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        const int v = v0 + 32 * wpt * b;
+        if (v < nvec) {
+          xo[v] = p[b];
+          yo[v] = q[b];
+        }
+      }
+    }
+  }
+}
+
+// Warps per token: one while the tokens alone give the GPU its warps, more (up to
+// the block's eight, and no more than the row has 32-vector pieces) when there are
+// few tokens and the rows are long.
+int warps_per_token(int T, int nvec) {
+  int wpt = 1;
+  while (wpt < kWarps && (long long)T * wpt < 148 * 16 && 32 * wpt < nvec) wpt *= 2;
+  return wpt;
+}
+
+template <typename T>
+cudaError_t combine_bwd(const CombineBwdArgs &a, cudaStream_t st) {
+  const int wpt = warps_per_token(a.T, a.d / Elem<T>::kPerVec);
+  const dim3 g(ceil_div(a.T, kWarps / wpt)), b(kThreads);
+  if (a.k <= 2) return launch_pdl(k_combine_bwd<T, 2, 4>, g, b, 0, st, a, wpt);
+  return launch_pdl(k_combine_bwd<T, kMaxTopK, 1>, g, b, 0, st, a, wpt);
+}
+
+template <typename T, typename TI>
+cudaError_t permute_bwd(const PermuteBwdArgs &a, cudaStream_t st) {
+  const int wpt = warps_per_token(a.T, a.d / Elem<T>::kPerVec);
+  const dim3 g(ceil_div(a.T, kWarps / wpt)), b(kThreads);
+  if (a.k <= 2) return launch_pdl(k_permute_bwd<T, TI, 2, 2>, g, b, 0, st, a, wpt);
+  return launch_pdl(k_permute_bwd<T, TI, kMaxTopK, 1>, g, b, 0, st, a, wpt);
+}
+
+}  // namespace
+
+cudaError_t launch_combine_bwd(const CombineBwdArgs &a, int dtype, cudaStream_t st) {
+  if (a.T == 0 || (a.dy_perm == nullptr && a.dgate == nullptr)) return cudaSuccess;
+  return dtype == MOE_DTYPE_F32 ? combine_bwd<float>(a, st) : combine_bwd<__nv_bfloat16>(a, st);
+}
+
+cudaError_t launch_permute_bwd(const PermuteBwdArgs &a, int dtype, cudaStream_t st) {
+  if (a.T == 0) return cudaSuccess;
+  if (dtype == MOE_DTYPE_F32) return permute_bwd<float, float>(a, st);
+  return a.dx_perm_f32 ? permute_bwd<__nv_bfloat16, float>(a, st)
+                       : permute_bwd<__nv_bfloat16, __nv_bfloat16>(a, st);
+}
+
+cudaError_t launch_gather_rows(const GatherRowsArgs &a, cudaStream_t st) {
+  if (a.T == 0) return cudaSuccess;
+  const int wpt = warps_per_token(a.T, a.row_bytes / 16);
+  return launch_pdl(k_gather_rows, dim3(ceil_div(a.T, kWarps / wpt)), dim3(kThreads), 0, st, a,
+                    wpt);
+}
+
+}  // namespace moe
