@@ -1,4 +1,5 @@
-// Gradient of the grouped expert FFN on CUDA cores.
+// Gradient of the grouped expert FFN: the CUDA-core path (fp32 layers), and what both
+// paths share (tables, bias gradients, the weights' row gradient).
 //
 // With x, dy the expert-contiguous rows of an expert and w_r an optional weight of
 // row r's output (1 without), from recomputed pre-activations:
@@ -191,62 +192,65 @@ __global__ void __launch_bounds__(256) k_dact(FfnGradArgs s) {
 
 // w_r-weighted column sums of dy over a 128-row tile -> part [tiles, d]
 template <typename T>
-__global__ void __launch_bounds__(256) k_col_sums(const T *dy, const float *row_w,
-                                                  const int32_t *offsets, const int32_t *mprefix,
-                                                  int G, int d, float *part) {
+__global__ void __launch_bounds__(256) k_col_sums(FfnGradArgs s) {
   __shared__ float red[4][64];
   pdl_wait();
   pdl_trigger();
-  const int g = group_of_tile(mprefix, G, blockIdx.y);
+  const int g = group_of_tile(s.mprefix, s.G, blockIdx.y), d = s.d;
   if (g < 0) return;
-  const int row0 = offsets[g] + ((int)blockIdx.y - mprefix[g]) * BM;
-  const int nrows = min(BM, offsets[g + 1] - row0);
+  const int in = ((int)blockIdx.y - s.mprefix[g]) * BM;
+  const int row0 = s.poff[g] + in;
+  const int nrows = min(BM, s.offsets[g + 1] - s.offsets[g] - in);
   const int n = blockIdx.x * 64 + (threadIdx.x & 63), q = threadIdx.x >> 6;
+  const T *dy = static_cast<const T *>(s.dy);
   float v = 0.f;
   if (n < d) {
 #pragma unroll 8
     for (int m = q; m < nrows; m += 4) {
       const size_t r = (size_t)(row0 + m);
       const float f = Elem<T>::to_f(dy[r * d + n]);
-      v += row_w ? row_w[r] * f : f;
+      v += s.row_w ? s.row_w[r] * f : f;
     }
   }
   red[q][threadIdx.x & 63] = v;
   __syncthreads();
   if (q == 0 && n < d) {
     const int c = threadIdx.x;
-    part[(size_t)blockIdx.y * d + n] = (red[0][c] + red[1][c]) + (red[2][c] + red[3][c]);
+    s.col_part[(size_t)blockIdx.y * d + n] = (red[0][c] + red[1][c]) + (red[2][c] + red[3][c]);
   }
 }
 
-// out [G, N]: the expert's tile partials in tile order (0 for an expert without rows)
-__global__ void __launch_bounds__(256) k_col_reduce(const float *part, const int32_t *mprefix,
-                                                    int N, float *out) {
+// out [G, N]: the expert's partials in order (0 for an expert without rows); expert g's
+// are first[g] / unit up to first[g + 1] / unit
+__global__ void __launch_bounds__(256) k_col_reduce(const float *part, const int32_t *first,
+                                                    int unit, int N, float *out) {
   pdl_wait();
   pdl_trigger();
   const int n = blockIdx.x * 256 + threadIdx.x, g = blockIdx.y;
   if (n >= N) return;
   float v = 0.f;
-  for (int t = mprefix[g]; t < mprefix[g + 1]; ++t) v += part[(size_t)t * N + n];
+#pragma unroll 4
+  for (int t = first[g] / unit; t < first[g + 1] / unit; ++t) v += part[(size_t)t * N + n];
   out[(size_t)g * N + n] = v;
 }
 
 // row_dot[r] = sum of the row's column-tile partials (+ <dy_r, b2 of its expert>), a
-// warp per row
+// warp per row (padding rows are left out)
 template <typename T>
 __global__ void __launch_bounds__(256) k_row_dot(FfnGradArgs s, int nt) {
   pdl_wait();
   pdl_trigger();
   const int r = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  if (r >= s.offsets[s.G]) return;
+  if (r >= s.poff[s.G]) return;
+  int lo = 0, hi = s.G - 1;  // last g with poff[g] <= r
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (s.poff[mid] <= r) lo = mid; else hi = mid - 1;
+  }
+  if (r - s.poff[lo] >= s.offsets[lo + 1] - s.offsets[lo]) return;
   float v = 0.f;
   for (int i = lane; i < nt; i += 32) v += s.dot_part[(size_t)i * s.rows + r];
   if (s.b2) {
-    int lo = 0, hi = s.G - 1;  // last g with offsets[g] <= r
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (s.offsets[mid] <= r) lo = mid; else hi = mid - 1;
-    }
     const T *dy = static_cast<const T *>(s.dy) + (size_t)r * s.d;
     const float *b = s.b2 + (size_t)lo * s.d;
     for (int i = lane; i < s.d; i += 32) v = fmaf(Elem<T>::to_f(dy[i]), b[i], v);
@@ -256,9 +260,10 @@ __global__ void __launch_bounds__(256) k_row_dot(FfnGradArgs s, int nt) {
 }
 
 // One warp: offsets -> checked copy (all zero when they are no partition of at most
-// max_rows rows) and the 128-row tile prefix.
-__global__ void k_grad_tables(const int32_t *offsets, int G, int max_rows, int32_t *checked,
-                              int32_t *mprefix, int32_t *err) {
+// max_rows rows), the 128-row tile prefix, and the prefix of the row counts rounded up to
+// multiples of `pad`.
+__global__ void k_grad_tables(const int32_t *offsets, int G, int max_rows, int pad,
+                              int32_t *checked, int32_t *mprefix, int32_t *poff, int32_t *err) {
   pdl_wait();
   pdl_trigger();
   const int lane = threadIdx.x;
@@ -270,59 +275,70 @@ __global__ void k_grad_tables(const int32_t *offsets, int G, int max_rows, int32
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) bad = min(bad, __shfl_xor_sync(0xffffffffu, bad, o));
   const bool ok = bad == G;
-  int sm = 0, mt[8];
+  int sm = 0, sp = 0, mt[8], pr[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) {  // G <= 256: eight groups per lane
     const int g = lane * 8 + j;
-    mt[j] = (ok && g < G) ? ceil_div(offsets[g + 1] - offsets[g], kRowTile) : 0;
+    const int n = (ok && g < G) ? offsets[g + 1] - offsets[g] : 0;
+    mt[j] = ceil_div(n, kRowTile);
+    pr[j] = ceil_div(n, pad) * pad;
     sm += mt[j];
+    sp += pr[j];
   }
-  int incl = sm;
+  int im = sm, ip = sp;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int v = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += v;
+    const int v = __shfl_up_sync(0xffffffffu, im, o), u = __shfl_up_sync(0xffffffffu, ip, o);
+    if (lane >= o) {
+      im += v;
+      ip += u;
+    }
   }
-  int run = incl - sm;
+  int rm = im - sm, rp = ip - sp;
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     const int g = lane * 8 + j;
     if (g < G) {
-      mprefix[g] = run;
+      mprefix[g] = rm;
+      poff[g] = rp;
       checked[g] = ok ? offsets[g] : 0;
     }
-    run += mt[j];
+    rm += mt[j];
+    rp += pr[j];
   }
   if (lane == 31) {
-    mprefix[G] = incl;
+    mprefix[G] = im;
+    poff[G] = ip;
     checked[G] = ok ? offsets[G] : 0;
   }
   if (!ok && lane == 0) report_error(err, MOE_DEVERR_OFFSETS, bad);
 }
 
-__global__ void k_one_group(int n, int32_t *offsets, int32_t *mprefix) {
+__global__ void k_one_group(int n, int pad, int32_t *offsets, int32_t *mprefix, int32_t *poff) {
   pdl_wait();
   pdl_trigger();
-  offsets[0] = mprefix[0] = 0;
+  offsets[0] = mprefix[0] = poff[0] = 0;
   offsets[1] = n;
   mprefix[1] = ceil_div(n, kRowTile);
+  poff[1] = ceil_div(n, pad) * pad;
 }
 
+// `groups`: db1's partials are one per 32 padded rows, else one per 128-row tile
 template <typename T>
-cudaError_t bias_and_row_grads(const FfnGradArgs &a, cudaStream_t st) {
+cudaError_t bias_and_row_grads(const FfnGradArgs &a, bool groups, cudaStream_t st) {
   cudaError_t e = cudaSuccess;
-  if (a.db1) {  // col_part holds step 1's tile sums
+  if (a.db1) {  // col_part holds step 1's sums
     e = launch_pdl(k_col_reduce, dim3(ceil_div(a.F, 256), a.G), dim3(256), 0, st,
-                   (const float *)a.col_part, a.mprefix, a.F, a.db1);
+                   (const float *)a.col_part, groups ? a.poff : a.mprefix, groups ? 32 : 1, a.F,
+                   a.db1);
     if (e != cudaSuccess) return e;
   }
   if (a.db2) {
     e = launch_pdl(k_col_sums<T>, dim3(ceil_div(a.d, 64), a.m_tiles_ub), dim3(256), 0, st,
-                   static_cast<const T *>(a.dy), a.row_w, a.offsets, a.mprefix, a.G, a.d,
-                   a.col_part);
+                   a);
     if (e != cudaSuccess) return e;
     e = launch_pdl(k_col_reduce, dim3(ceil_div(a.d, 256), a.G), dim3(256), 0, st,
-                   (const float *)a.col_part, a.mprefix, a.d, a.db2);
+                   (const float *)a.col_part, a.mprefix, 1, a.d, a.db2);
     if (e != cudaSuccess) return e;
   }
   if (a.row_dot)
@@ -339,7 +355,7 @@ cudaError_t ffn_bwd_simt(const FfnGradArgs &a, cudaStream_t st) {
   cudaError_t e = glu ? launch_pdl(k_dact<T, true>, g1, b, 0, st, a)
                       : launch_pdl(k_dact<T, false>, g1, b, 0, st, a);
   if (e != cudaSuccess) return e;
-  e = bias_and_row_grads<T>(a, st);
+  e = bias_and_row_grads<T>(a, false, st);
   if (e != cudaSuccess) return e;
   if (a.dx) {
     const dim3 g2(ceil_div(a.d, BN), a.m_tiles_ub);
@@ -389,22 +405,35 @@ cudaError_t ffn_bwd_simt(const FfnGradArgs &a, cudaStream_t st) {
   return launch_pdl(k_gemm<T, T, T, true>, dim3(nt, mt, n * a.G), b, 0, st, w);
 }
 
-}  // namespace
-
-cudaError_t launch_grad_tables(const int32_t *offsets, int G, int max_rows, int32_t *checked,
-                               int32_t *mprefix, int32_t *err, cudaStream_t st) {
-  return launch_pdl(k_grad_tables, dim3(1), dim3(32), 0, st, offsets, G, max_rows, checked,
-                    mprefix, err);
+// bf16: the three steps on the tensor cores
+cudaError_t ffn_bwd_tc(const FfnGradArgs &a, cudaStream_t st) {
+  cudaError_t e = launch_act_grad_tc(a, st);
+  if (e != cudaSuccess) return e;
+  e = bias_and_row_grads<__nv_bfloat16>(a, true, st);
+  if (e != cudaSuccess) return e;
+  if (a.dx) {
+    e = launch_dx_tc(a, st);
+    if (e != cudaSuccess) return e;
+  }
+  return launch_dw_tc(a, st);
 }
 
-cudaError_t launch_one_group(int n, int32_t *offsets, int32_t *mprefix, cudaStream_t st) {
-  return launch_pdl(k_one_group, dim3(1), dim3(1), 0, st, n, offsets, mprefix);
+}  // namespace
+
+cudaError_t launch_grad_tables(const int32_t *offsets, int G, int max_rows, int pad,
+                               int32_t *checked, int32_t *mprefix, int32_t *poff, int32_t *err,
+                               cudaStream_t st) {
+  return launch_pdl(k_grad_tables, dim3(1), dim3(32), 0, st, offsets, G, max_rows, pad, checked,
+                    mprefix, poff, err);
+}
+
+cudaError_t launch_one_group(int n, int pad, int32_t *offsets, int32_t *mprefix, int32_t *poff,
+                             cudaStream_t st) {
+  return launch_pdl(k_one_group, dim3(1), dim3(1), 0, st, n, pad, offsets, mprefix, poff);
 }
 
 cudaError_t launch_ffn_bwd(const FfnGradArgs &a, int dtype, cudaStream_t st) {
-  if (a.m_tiles_ub <= 0) return cudaSuccess;
-  if (dtype == MOE_DTYPE_F32) return ffn_bwd_simt<float>(a, st);
-  return ffn_bwd_simt<__nv_bfloat16>(a, st);
+  return dtype == MOE_DTYPE_F32 ? ffn_bwd_simt<float>(a, st) : ffn_bwd_tc(a, st);
 }
 
 }  // namespace moe

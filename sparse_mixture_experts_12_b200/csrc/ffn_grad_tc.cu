@@ -1,0 +1,762 @@
+// Gradient of the grouped expert FFN on the 5th-generation tensor cores (bf16 layers):
+// the formulas of ffn_grad.cu as three persistent grids of CTA pairs.
+//
+//   k_act_grad    a = x W1^T (and u = x W3^T) and q = dy W2, reduction length d, into
+//                 tensor memory together; the epilogue turns them into h, da, du
+//   k_pair_gemm   dx = da W1 (+ du W3), reduction length F (2 F)
+//   k_pair_gemm   dW1 = da^T x, dW3 = du^T x, dW2 = dy^T h, reduction over an expert's rows
+//
+// Every product is a 256-row tcgen05.mma.cta_group::2 over K slices of 64; operands whose
+// contiguous index is not the reduction's (W2 in q, W1 / W3 in dx, both in the weights'
+// gradients) are loaded as they lie and marked MN-major, so nothing is transposed in
+// memory. x, dy and the scratch rows lie padded: each expert begins at a multiple of 64
+// rows and the rows up to the next are zero. A slice of an expert's rows is then a whole
+// K slice, with no masking in the weights' gradients (zero rows add exact zeros).
+//
+// A CTA pair's roles, barriers and bounded waits are those of the forward's GEMM
+// (ffn_tc.cu): warp 0 of each CTA loads its operand halves, warp 1 of the leader issues
+// the MMAs, warps 4-11 drain tensor memory; a wait that runs out records
+// MOE_DEVERR_WAIT_TIMEOUT and ends both CTAs.
+#include <algorithm>
+#include <mutex>
+
+#include "grad.cuh"
+#include "tc_ptx.cuh"
+
+namespace moe {
+
+namespace {
+
+using namespace tc;
+
+constexpr int kPairM = 2 * kRowTile;
+constexpr int kStages = 6;
+constexpr int kOperand = kRowTile * kBlockK * 2;  // 16 KB: a CTA's half of a 256-wide operand
+constexpr int kStageBytes = 2 * kOperand;
+constexpr int kMnBlock = kBlockK * kBlockK * 2;   // 8 KB: 64 K rows x 64 contiguous elements
+constexpr int kThreads = 384;
+constexpr int kEpiWarps = 8;
+constexpr int kTmemCols = 512;
+constexpr uint64_t kDrainNs = 50000000ull;
+
+struct Ctl {
+  uint64_t full[kStages];   // leader: both CTAs' copies of the stage landed
+  uint64_t empty[kStages];  // each CTA: the pair's MMAs are done with the stage
+  uint64_t tfull[2];        // each CTA: the tile's accumulators are complete
+  uint64_t tempty[2];       // leader: both epilogues have drained them
+  uint64_t drain;
+  uint32_t tmem_base;
+  int abort_flag;
+  int pre[kMaxExperts + 1];   // prefix of the experts' 256-row tiles
+  int poff[kMaxExperts + 1];  // first (padded) row of each expert
+};
+constexpr size_t kRing = (size_t)kStages * kStageBytes;
+constexpr size_t kSmemBytes = kRing + (size_t)kEpiWarps * kStageOutBytes + sizeof(Ctl) + 1024;
+
+// what both kernels do before their roles split up; returns the tensor memory's base
+struct Setup {
+  uint8_t *smem;
+  Ctl *ctl;
+  uint32_t tmem, peer_abort;
+  int rank, c0, cstep;
+};
+
+__device__ __forceinline__ Setup set_up(uint8_t *raw, const int32_t *poff, int G) {
+  Setup s;
+  s.smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) &
+                                       ~static_cast<uintptr_t>(1023));
+  s.ctl = reinterpret_cast<Ctl *>(s.smem + kRing + kEpiWarps * kStageOutBytes);
+  Ctl *ctl = s.ctl;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  s.rank = (int)cluster_ctarank();
+  if (tid == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&ctl->full[i], 1);
+      mbar_init(&ctl->empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&ctl->tfull[i], 1);
+      mbar_init(&ctl->tempty[i], 2 * kEpiWarps * 32);
+    }
+    mbar_init(&ctl->drain, 1);
+    ctl->abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 2) {
+    tmem_alloc_pair(&ctl->tmem_base, kTmemCols);
+    tmem_relinquish_pair();
+  }
+  pdl_wait();
+  for (int i = tid; i <= G; i += kThreads) ctl->poff[i] = poff[i];
+  if (warp == 1) {
+    const int per = ceil_div(G, 32);
+    const int j0 = min(G, lane * per), j1 = min(G, j0 + per);
+    int sum = 0;
+    for (int j = j0; j < j1; ++j) sum += ceil_div(poff[j + 1] - poff[j], kPairM);
+    int incl = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    int run = incl - sum;
+    for (int j = j0; j < j1; ++j) {
+      ctl->pre[j] = run;
+      run += ceil_div(poff[j + 1] - poff[j], kPairM);
+    }
+    if (lane == 31) ctl->pre[G] = incl;
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();  // both CTAs' barriers and tensor memory exist
+  pdl_trigger();
+  tc_fence_after();
+  s.tmem = ctl->tmem_base;
+  s.peer_abort = mapa_rank(smem_u32(&ctl->abort_flag), (uint32_t)(s.rank ^ 1));
+  s.c0 = (int)cluster_index();
+  s.cstep = (int)cluster_count();
+  return s;
+}
+
+__device__ __forceinline__ bool wait_on(const Setup &s, uint64_t *bar, uint32_t parity,
+                                        int32_t *err, int site, bool honour_abort = true,
+                                        uint64_t limit_ns = kWaitLimitNs) {
+  return wait_mbar(bar, parity, &s.ctl->abort_flag, s.peer_abort, err, site, honour_abort,
+                   limit_ns);
+}
+
+// the ring's position, and (producer) which stages were filled and when
+struct Ring {
+  int stage = 0;
+  uint32_t phase = 0, issued = 0, last_phase = 0;
+  __device__ __forceinline__ void mark() {
+    issued |= 1u << stage;
+    last_phase = (last_phase & ~(1u << stage)) | (phase << stage);
+  }
+  __device__ __forceinline__ void next() {
+    if (++stage == kStages) { stage = 0; phase ^= 1u; }
+  }
+};
+
+// the pair's MMAs have released every stage this CTA filled
+__device__ __forceinline__ void drain_ring(const Setup &s, const Ring &r, bool ok) {
+  for (int i = 0; i < kStages; ++i)
+    if (r.issued & (1u << i))
+      wait_on(s, &s.ctl->empty[i], (r.last_phase >> i) & 1u, nullptr, 0, false,
+              ok ? kWaitLimitNs : kDrainNs);
+}
+
+__device__ __forceinline__ void tear_down(const Setup &s) {
+  if (*(volatile int *)&s.ctl->abort_flag) settle_ns(100000);  // copies in flight land
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();  // the peer's remote arrivals are done before either CTA exits
+  if ((threadIdx.x >> 5) == 2) {
+    tc_fence_after();
+    tmem_dealloc_pair(s.tmem, kTmemCols);
+  }
+}
+
+// 64 K rows x 128 contiguous elements, as two 64-element blocks
+__device__ __forceinline__ void load_mn(const CUtensorMap *map, uint32_t bar, uint8_t *dst, int c,
+                                        int row) {
+  tma_load_2d_pair(map, bar, dst, c, row);
+  tma_load_2d_pair(map, bar, dst + kMnBlock, c + kBlockK, row);
+}
+
+__device__ __forceinline__ void pack32(const float (&f)[32], uint4 (&pk)[4]) {
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    float h[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) h[j] = f[q * 8 + j];
+    pk[q] = pack16(h);
+  }
+}
+
+// ================================================================= activations
+struct ActArgs {
+  const int32_t *poff, *offsets;  // padded first rows; the experts' row counts
+  int G, F, d, act, n_tiles;
+  const float *b1, *row_w;
+  float *dot_part;  // [ceil(F / 64), rows] or nullptr
+  float *col_part;  // [rows / 32, F] or nullptr
+  void *h, *dg, *du;
+  int rows;
+  int32_t *err;
+};
+struct ActMaps {
+  CUtensorMap x, dy, w1, w3, w2, h, dg, du;
+};
+
+// Column sums of 16 values per lane over the warp's 32 lanes: lane l ends with column
+// l & 15 (a butterfly that halves the columns a lane holds at each step).
+__device__ __forceinline__ float column_sum16(float (&v)[16], int lane) {
+#pragma unroll
+  for (int w = 8; w > 0; w >>= 1) {
+    const bool up = lane & w;
+#pragma unroll
+    for (int i = 0; i < w; ++i) {
+      const float give = up ? v[i] : v[i + w];
+      const float keep = up ? v[i + w] : v[i];
+      v[i] = keep + __shfl_xor_sync(0xffffffffu, give, w);
+    }
+  }
+  return v[0] + __shfl_xor_sync(0xffffffffu, v[0], 16);
+}
+
+// d gelu / dv (with the forward's erf) and gelu
+__device__ __forceinline__ void gelu_and_slope(float v, float &h, float &s) {
+  const float c = 0.5f * (1.f + erf_as7126(v * 0.70710678118654752f));
+  h = v * c;
+  s = c + v * 0.39894228040143268f * __expf(-0.5f * v * v);
+}
+
+// One tile: 256 rows x 128 columns of F. Tensor memory: a | u at columns 0-255 (SwiGLU) or
+// a at 0 / 128 (alternating, MLP); q at 256 / 384 (alternating). With SwiGLU the a | u
+// region is single: the next tile's first kLead slices of q run while it is drained.
+constexpr int kTileN = 128;
+constexpr int kLead = 16;
+
+template <bool GLU>
+__global__ void __launch_bounds__(kThreads, 1)
+k_act_grad(const __grid_constant__ ActMaps maps, ActArgs a) {
+  extern __shared__ uint8_t smem_raw[];
+  const Setup s = set_up(smem_raw, a.poff, a.G);
+  Ctl *ctl = s.ctl;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int total = ctl->pre[a.G] * a.n_tiles;
+  const int nkb = ceil_div(a.d, kBlockK);
+  const int lead = GLU ? min(kLead, nkb) : 0;
+  constexpr int kBytesQ = kOperand + kMnBlock;
+  constexpr int kBytesA = GLU ? 2 * kOperand : kOperand + kMnBlock;
+
+  if (warp == 0 && lane == 0) {
+    // ------------------------------------------------------------ TMA producer
+    prefetch_map(&maps.x);
+    prefetch_map(&maps.dy);
+    prefetch_map(&maps.w1);
+    prefetch_map(&maps.w2);
+    if (GLU) prefetch_map(&maps.w3);
+    const uint32_t full0 = mapa_rank(smem_u32(&ctl->full[0]), 0);
+    Ring ring;
+    bool ok = true;
+    for (int t = s.c0; ok && t < total; t += s.cstep) {
+      int g, n, m;
+      decode_tile(t, ctl->pre, a.G, a.n_tiles, g, n, m);
+      const int arow = ctl->poff[g] + m * kPairM + s.rank * kRowTile;
+      const int n0 = n * kTileN;
+      auto stage_for = [&](int bytes) -> uint8_t * {
+        if (!wait_on(s, &ctl->empty[ring.stage], ring.phase ^ 1u, a.err, 21)) return nullptr;
+        if (s.rank == 0) mbar_expect_tx(&ctl->full[ring.stage], 2 * bytes);
+        return s.smem + (size_t)ring.stage * kStageBytes;
+      };
+      for (int i = 0; i < nkb + lead; ++i) {
+        if (i < nkb) {
+          uint8_t *st = stage_for(kBytesQ);
+          if (!(ok = st != nullptr)) break;
+          const uint32_t bar = full0 + (uint32_t)(ring.stage * sizeof(uint64_t));
+          tma_load_2d_pair(&maps.dy, bar, st, i * kBlockK, arow);
+          tma_load_2d_pair(&maps.w2, bar, st + kOperand, n0 + s.rank * kBlockK,
+                           g * a.d + i * kBlockK);
+          ring.mark();
+          ring.next();
+        }
+        if (i >= lead) {
+          uint8_t *st = stage_for(kBytesA);
+          if (!(ok = st != nullptr)) break;
+          const uint32_t bar = full0 + (uint32_t)(ring.stage * sizeof(uint64_t));
+          const int k0 = (i - lead) * kBlockK;
+          tma_load_2d_pair(&maps.x, bar, st, k0, arow);
+          if (GLU)
+            tma_load_2d_pair(s.rank ? &maps.w3 : &maps.w1, bar, st + kOperand, k0, g * a.F + n0);
+          else
+            tma_load_2d_pair(&maps.w1, bar, st + kOperand, k0, g * a.F + n0 + s.rank * kBlockK);
+          ring.mark();
+          ring.next();
+        }
+      }
+    }
+    drain_ring(s, ring, ok);
+  } else if (warp == 1 && lane == 0 && s.rank == 0) {
+    // --------------------------------------------------------------- MMA issuer
+    constexpr uint32_t idesc_q = make_idesc(kPairM, kTileN) | kIdescMnB;
+    constexpr uint32_t idesc_a = make_idesc(kPairM, GLU ? 2 * kTileN : kTileN);
+    Ring ring;
+    bool ok = true, any = false;
+    int it = 0;
+    for (int t = s.c0; ok && t < total; t += s.cstep, ++it) {
+      const int buf = it & 1;
+      const uint32_t dq = s.tmem + 256u + (uint32_t)(buf * kTileN);
+      const uint32_t da = s.tmem + (GLU ? 0u : (uint32_t)(buf * kTileN));
+      // tile it - 2, which used the same buffers, has been drained
+      if (!(ok = wait_on(s, &ctl->tempty[buf], ((it >> 1) & 1) ^ 1u, a.err, 22))) break;
+      tc_fence_after();
+      for (int i = 0; i < nkb + lead; ++i) {
+        if (i < nkb) {
+          if (!(ok = wait_on(s, &ctl->full[ring.stage], ring.phase, a.err, 23))) break;
+          tc_fence_after();
+          const uint32_t sa = smem_u32(s.smem + (size_t)ring.stage * kStageBytes);
+          const uint64_t xa = sw128_desc(sa), xb = sw128_desc_mn(sa + kOperand, kMnBlock);
+#pragma unroll
+          for (int kk = 0; kk < kBlockK / 16; ++kk)
+            umma_bf16_pair(dq, xa + 2 * kk, xb + 128 * kk, idesc_q, (i | kk) != 0);
+          any = true;
+          umma_commit_pair_both(&ctl->empty[ring.stage]);
+          ring.next();
+        }
+        if (i >= lead) {
+          // the one a | u region: tile it - 1 has been drained
+          if (GLU && i == lead && it > 0 &&
+              !(ok = wait_on(s, &ctl->tempty[buf ^ 1], ((it - 1) >> 1) & 1, a.err, 22)))
+            break;
+          if (!(ok = wait_on(s, &ctl->full[ring.stage], ring.phase, a.err, 23))) break;
+          tc_fence_after();
+          const uint32_t sa = smem_u32(s.smem + (size_t)ring.stage * kStageBytes);
+          const uint64_t xa = sw128_desc(sa), xb = sw128_desc(sa + kOperand);
+#pragma unroll
+          for (int kk = 0; kk < kBlockK / 16; ++kk)
+            umma_bf16_pair(da, xa + 2 * kk, xb + 2 * kk, idesc_a, ((i - lead) | kk) != 0);
+          any = true;
+          umma_commit_pair_both(&ctl->empty[ring.stage]);
+          ring.next();
+        }
+      }
+      if (!ok) break;
+      umma_commit_pair_both(&ctl->tfull[buf]);
+    }
+    if (!ok && any) {  // retire the MMAs in flight before TMEM is released
+      umma_commit_pair_own(&ctl->drain);
+      wait_on(s, &ctl->drain, 0, nullptr, 0, false, kDrainNs);
+    }
+  } else if (warp >= 4) {
+    // ----------------------------------------------------------------- epilogue
+    const int ew = warp & 3, half = (warp - 4) >> 2;
+    const uint32_t tempty0 = mapa_rank(smem_u32(&ctl->tempty[0]), 0);
+    uint8_t *stage_out = s.smem + kRing + (warp - 4) * kStageOutBytes;
+    int it = 0;
+    for (int t = s.c0; t < total; t += s.cstep, ++it) {
+      int g, n, m;
+      decode_tile(t, ctl->pre, a.G, a.n_tiles, g, n, m);
+      const int buf = it & 1;
+      const int lrow = m * kPairM + s.rank * kRowTile + ew * 32;  // the warp's first row
+      const int base = ctl->poff[g], prow = base + lrow;
+      const bool mine = prow < ctl->poff[g + 1];  // padded groups of 32 rows: all or none
+      const bool valid = lrow + lane < a.offsets[g + 1] - a.offsets[g];
+      const float w = (valid && mine) ? (a.row_w ? a.row_w[prow + lane] : 1.f) : 0.f;
+      bool ok = wait_on(s, &ctl->tfull[buf], (it >> 1) & 1, a.err, 24);
+      __syncwarp();
+      if (!__all_sync(0xffffffffu, ok)) break;
+      tc_fence_after();
+      const uint32_t tq = s.tmem + ((uint32_t)(ew * 32) << 16) + 256u + (uint32_t)(buf * kTileN);
+      const uint32_t ta = s.tmem + ((uint32_t)(ew * 32) << 16) +
+                          (GLU ? 0u : (uint32_t)(buf * kTileN));
+      float dot = 0.f;
+#pragma unroll 1
+      for (int c = 2 * half; c < 2 * half + 2; ++c) {
+        const int col0 = n * kTileN + c * 32;
+        if (!mine || col0 >= a.F) break;  // F is a multiple of 64
+        uint32_t hp[16], gp[16], up[GLU ? 16 : 1];  // packed pairs of columns
+#pragma unroll
+        for (int j2 = 0; j2 < 2; ++j2) {
+          uint32_t av[16], uv[16], qv[16];
+          tmem_ld16(ta + c * 32 + j2 * 16, av);
+          if (GLU) tmem_ld16(ta + kTileN + c * 32 + j2 * 16, uv);
+          tmem_ld16(tq + c * 32 + j2 * 16, qv);
+          tmem_ld_wait();
+          float h[16], da[16], du[16];
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            const float q = __uint_as_float(qv[j]);
+            float v = __uint_as_float(av[j]);
+            if (GLU) {
+              const float u = __uint_as_float(uv[j]);
+              const float sg = __fdividef(1.f, 1.f + __expf(-v));
+              const float si = v * sg;
+              h[j] = si * u;
+              du[j] = q * si;
+              da[j] = q * u * fmaf(si, 1.f - sg, sg);
+            } else {
+              if (a.b1) v += __ldg(a.b1 + (size_t)g * a.F + col0 + j2 * 16 + j);
+              float sl;
+              if (a.act == MOE_ACT_RELU) {
+                h[j] = fmaxf(v, 0.f);
+                sl = v > 0.f ? 1.f : 0.f;
+              } else {
+                gelu_and_slope(v, h[j], sl);
+              }
+              da[j] = q * sl;
+            }
+            dot = fmaf(q, h[j], dot);
+          }
+          // rows past the expert's: zeros, whatever the weights hold
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            h[j] = valid ? w * h[j] : 0.f;
+            da[j] = valid ? w * da[j] : 0.f;
+            if (GLU) du[j] = valid ? w * du[j] : 0.f;
+          }
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            hp[j2 * 8 + j] = pack_bf16x2(h[2 * j], h[2 * j + 1]);
+            gp[j2 * 8 + j] = pack_bf16x2(da[2 * j], da[2 * j + 1]);
+            if (GLU) up[j2 * 8 + j] = pack_bf16x2(du[2 * j], du[2 * j + 1]);
+          }
+          if (a.col_part) {
+            const float v = column_sum16(da, lane);
+            if (lane < 16)
+              a.col_part[(size_t)(prow >> 5) * a.F + col0 + j2 * 16 + lane] = v;
+          }
+        }
+        auto out = [&](const CUtensorMap *map, const uint32_t *p) {
+          const EpiStore st{map, stage_out, true, prow};
+          uint4 pk[4];
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            pk[q] = make_uint4(p[4 * q], p[4 * q + 1], p[4 * q + 2], p[4 * q + 3]);
+          emit_chunk(st, pk, nullptr, col0);
+        };
+        out(&maps.h, hp);
+        out(&maps.dg, gp);
+        if (GLU) out(&maps.du, up);
+      }
+      tc_fence_before();
+      mbar_arrive_cluster(tempty0 + (uint32_t)(buf * sizeof(uint64_t)));
+      if (a.dot_part && valid && mine && n * kTileN + half * 64 < a.F)
+        a.dot_part[(size_t)(2 * n + half) * a.rows + prow + lane] = dot;
+    }
+    if (lane == 0) bulk_wait_all();  // this warp's output stores are done
+    __syncwarp();
+  }
+  tear_down(s);
+}
+
+// ============================================================ dx and the weights
+struct GemmArgs {
+  const int32_t *poff, *offsets;
+  const int32_t *dx_off;  // first row of each expert in dx
+  int G, err_site;
+  // dx: N = d, K = F, nseg pairs (A, B). Weights: njobs products of M x N.
+  int N, K, nseg;
+  int M[3], Ns[3], njobs;
+  void *out;              // dx
+  int out_f32;
+  int32_t *err;
+};
+struct GemmMaps {
+  CUtensorMap a[3], b[3], o[3];
+};
+
+template <bool DW>
+__global__ void __launch_bounds__(kThreads, 1)
+k_pair_gemm(const __grid_constant__ GemmMaps maps, GemmArgs a) {
+  extern __shared__ uint8_t smem_raw[];
+  const Setup s = set_up(smem_raw, a.poff, a.G);
+  Ctl *ctl = s.ctl;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int per = 0;  // weights: tiles of one expert
+  if (DW)
+    for (int j = 0; j < a.njobs; ++j) per += ceil_div(a.M[j], kPairM) * ceil_div(a.Ns[j], 256);
+  const int n_tiles = ceil_div(a.N, 256);
+  const int total = DW ? a.G * per : ctl->pre[a.G] * n_tiles;
+  // a tile: expert, job (weights), first row and column, K slices
+  struct Tile {
+    int g, job, m0, n0, nkb;
+  };
+  const int nk1 = ceil_div(a.K, kBlockK);
+  auto tile_at = [&](int t) -> Tile {
+    Tile r;
+    r.job = 0;
+    if (DW) {
+      r.g = t / per;
+      int rem = t % per;
+      while (true) {
+        const int cnt = ceil_div(a.M[r.job], kPairM) * ceil_div(a.Ns[r.job], 256);
+        if (rem < cnt) break;
+        rem -= cnt;
+        ++r.job;
+      }
+      const int mt = ceil_div(a.M[r.job], kPairM);
+      r.m0 = (rem % mt) * kPairM;
+      r.n0 = (rem / mt) * 256;
+      r.nkb = (ctl->poff[r.g + 1] - ctl->poff[r.g]) / kBlockK;
+    } else {
+      int n, m;
+      decode_tile(t, ctl->pre, a.G, n_tiles, r.g, n, m);
+      r.m0 = m * kPairM;
+      r.n0 = n * 256;
+      r.nkb = a.nseg * nk1;
+    }
+    return r;
+  };
+
+  if (warp == 0 && lane == 0) {
+    // ------------------------------------------------------------ TMA producer
+    const int nm = DW ? a.njobs : a.nseg;
+    for (int j = 0; j < nm; ++j) {
+      prefetch_map(&maps.a[j]);
+      prefetch_map(&maps.b[j]);
+    }
+    const uint32_t full0 = mapa_rank(smem_u32(&ctl->full[0]), 0);
+    Ring ring;
+    bool ok = true;
+    for (int t = s.c0; ok && t < total; t += s.cstep) {
+      const Tile q = tile_at(t);
+      const int row0 = ctl->poff[q.g];
+      const int bcol = q.n0 + s.rank * kRowTile;
+      for (int kb = 0; kb < q.nkb; ++kb) {
+        if (!(ok = wait_on(s, &ctl->empty[ring.stage], ring.phase ^ 1u, a.err, 31))) break;
+        if (s.rank == 0) mbar_expect_tx(&ctl->full[ring.stage], 2 * kStageBytes);
+        uint8_t *st = s.smem + (size_t)ring.stage * kStageBytes;
+        const uint32_t bar = full0 + (uint32_t)(ring.stage * sizeof(uint64_t));
+        if (DW) {
+          const int r = row0 + kb * kBlockK;
+          load_mn(&maps.a[q.job], bar, st, q.m0 + s.rank * kRowTile, r);
+          load_mn(&maps.b[q.job], bar, st + kOperand, bcol, r);
+        } else {
+          const int seg = kb >= nk1, k0 = (kb - seg * nk1) * kBlockK;
+          tma_load_2d_pair(&maps.a[seg], bar, st, k0, row0 + q.m0 + s.rank * kRowTile);
+          load_mn(&maps.b[seg], bar, st + kOperand, bcol, q.g * a.K + k0);
+        }
+        ring.mark();
+        ring.next();
+      }
+    }
+    drain_ring(s, ring, ok);
+  } else if (warp == 1 && lane == 0 && s.rank == 0) {
+    // --------------------------------------------------------------- MMA issuer
+    constexpr uint32_t idesc = make_idesc(kPairM, 256) | kIdescMnB | (DW ? kIdescMnA : 0u);
+    constexpr int kStepA = DW ? 128 : 2;  // a K = 16 step in the A descriptor
+    Ring ring;
+    bool ok = true, any = false;
+    int it = 0;
+    for (int t = s.c0; ok && t < total; t += s.cstep, ++it) {
+      const Tile q = tile_at(t);
+      const int buf = it & 1;
+      if (!(ok = wait_on(s, &ctl->tempty[buf], ((it >> 1) & 1) ^ 1u, a.err, 32))) break;
+      tc_fence_after();
+      const uint32_t acc = s.tmem + (uint32_t)(buf * 256);
+      for (int kb = 0; kb < q.nkb; ++kb) {
+        if (!(ok = wait_on(s, &ctl->full[ring.stage], ring.phase, a.err, 33))) break;
+        tc_fence_after();
+        const uint32_t sa = smem_u32(s.smem + (size_t)ring.stage * kStageBytes);
+        const uint64_t xa = DW ? sw128_desc_mn(sa, kMnBlock) : sw128_desc(sa);
+        const uint64_t xb = sw128_desc_mn(sa + kOperand, kMnBlock);
+#pragma unroll
+        for (int kk = 0; kk < kBlockK / 16; ++kk)
+          umma_bf16_pair(acc, xa + kStepA * kk, xb + 128 * kk, idesc, (kb | kk) != 0);
+        any = true;
+        umma_commit_pair_both(&ctl->empty[ring.stage]);
+        ring.next();
+      }
+      if (!ok) break;
+      umma_commit_pair_both(&ctl->tfull[buf]);
+    }
+    if (!ok && any) {
+      umma_commit_pair_own(&ctl->drain);
+      wait_on(s, &ctl->drain, 0, nullptr, 0, false, kDrainNs);
+    }
+  } else if (warp >= 4) {
+    // ----------------------------------------------------------------- epilogue
+    const int ew = warp & 3, half = (warp - 4) >> 2;
+    const uint32_t tempty0 = mapa_rank(smem_u32(&ctl->tempty[0]), 0);
+    uint8_t *stage_out = s.smem + kRing + (warp - 4) * kStageOutBytes;
+    int it = 0;
+    for (int t = s.c0; t < total; t += s.cstep, ++it) {
+      const Tile q = tile_at(t);
+      const int buf = it & 1;
+      const int lrow = q.m0 + s.rank * kRowTile + ew * 32;
+      int rows, N;      // the output's valid rows from q's first, its width
+      size_t orow;      // output row of lane 0
+      if (DW) {
+        rows = a.M[q.job];
+        N = a.Ns[q.job];
+        orow = (size_t)q.g * rows + lrow;
+      } else {
+        rows = a.offsets[q.g + 1] - a.offsets[q.g];
+        N = a.N;
+        orow = (size_t)a.dx_off[q.g] + lrow;
+      }
+      const bool valid = lrow + lane < rows;
+      const EpiStore st{(DW || !a.out_f32) ? &maps.o[q.job] : nullptr, stage_out,
+                        lrow + 32 <= rows, (int)orow};
+      bool ok = wait_on(s, &ctl->tfull[buf], (it >> 1) & 1, a.err, 34);
+      __syncwarp();
+      if (!__all_sync(0xffffffffu, ok)) break;
+      tc_fence_after();
+      const uint32_t ta = s.tmem + ((uint32_t)(ew * 32) << 16) + (uint32_t)(buf * 256);
+#pragma unroll 1
+      for (int c = 4 * half; c < 4 * half + 4; ++c) {
+        const int col0 = q.n0 + c * 32;
+        if (lrow >= rows || col0 >= N) break;
+        float f[32];
+        if (DW && q.nkb == 0) {  // an expert without rows
+#pragma unroll
+          for (int j = 0; j < 32; ++j) f[j] = 0.f;
+        } else {
+          uint32_t v[32];
+          tmem_ld32(ta + c * 32, v);
+          tmem_ld_wait();
+#pragma unroll
+          for (int j = 0; j < 32; ++j) f[j] = __uint_as_float(v[j]);
+        }
+        if (!DW && a.out_f32) {
+          if (valid) {
+            float4 *dst = reinterpret_cast<float4 *>(static_cast<float *>(a.out) +
+                                                     (orow + lane) * (size_t)N + col0);
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              dst[j] = make_float4(f[4 * j], f[4 * j + 1], f[4 * j + 2], f[4 * j + 3]);
+          }
+        } else if (valid) {  // a full group's lanes are all valid
+          uint4 pk[4];
+          pack32(f, pk);
+          __nv_bfloat16 *dst =
+              DW ? nullptr : static_cast<__nv_bfloat16 *>(a.out) + (orow + lane) * (size_t)N;
+          emit_chunk(st, pk, dst, col0);
+        }
+      }
+      tc_fence_before();
+      mbar_arrive_cluster(tempty0 + (uint32_t)(buf * sizeof(uint64_t)));
+    }
+    if (lane == 0) bulk_wait_all();
+    __syncwarp();
+  }
+  tear_down(s);
+}
+
+// ------------------------------------------------------------------ host side
+std::mutex g_mu;
+
+// A persistent grid of CTA pairs, at most `tiles` of them; `slot` names the kernel in the
+// per-device table of grid sizes.
+template <typename... KArgs, typename... Args>
+cudaError_t launch_pairs(void (*kernel)(KArgs...), int slot, long long tiles, cudaStream_t st,
+                         const Args &...args) {
+  static int max_pairs[64][4] = {};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmemBytes;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int &most = max_pairs[dev & 63][slot];
+  {
+    std::lock_guard<std::mutex> lock(g_mu);
+    if (most == 0) {
+      e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               (int)kSmemBytes);
+      if (e != cudaSuccess) return e;
+      cfg.gridDim = dim3(2 * (sm_count() / 2));
+      int n = 0;
+      if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n <= 0)
+        n = sm_count() / 2;
+      most = n;
+    }
+  }
+  cfg.gridDim = dim3((unsigned)(2 * std::max<long long>(1, std::min<long long>(tiles, most))));
+  cfg.numAttrs = take_pdl() ? 2 : 1;
+  e = cudaLaunchKernelEx(&cfg, kernel, args...);
+  return e == cudaSuccess ? cudaGetLastError() : e;
+}
+
+}  // namespace
+
+cudaError_t launch_act_grad_tc(const FfnGradArgs &f, cudaStream_t st) {
+  const bool glu = f.act == MOE_ACT_SWIGLU;
+  ActMaps m;
+  const uint64_t R = (uint64_t)f.rows, X = (uint64_t)f.x_rows, d = (uint64_t)f.d,
+                 F = (uint64_t)f.F, G = (uint64_t)f.G;
+  bool ok = make_map(&m.x, f.x, X, d, kRowTile) && make_map(&m.dy, f.dy, X, d, kRowTile) &&
+            make_map(&m.w1, f.w1, G * F, d, glu ? kRowTile : kBlockK) &&
+            make_map(&m.w2, f.w2, G * d, F, kBlockK) && make_store_map(&m.h, f.h, R, F) &&
+            make_store_map(&m.dg, f.dg, R, F);
+  m.w3 = m.w1;
+  m.du = m.dg;
+  if (glu)
+    ok = ok && make_map(&m.w3, f.w3, G * F, d, kRowTile) && make_store_map(&m.du, f.du, R, F);
+  if (!ok) return cudaErrorInvalidValue;
+  ActArgs a{};
+  a.poff = f.poff;
+  a.offsets = f.offsets;
+  a.G = f.G;
+  a.F = f.F;
+  a.d = f.d;
+  a.act = f.act;
+  a.n_tiles = ceil_div(f.F, kTileN);
+  a.b1 = f.b1;
+  a.row_w = f.row_w;
+  a.dot_part = f.row_dot ? f.dot_part : nullptr;
+  a.col_part = f.db1 ? f.col_part : nullptr;
+  a.rows = f.rows;
+  a.err = f.err;
+  const long long tiles = (long long)f.pair_tiles_ub * a.n_tiles;
+  return glu ? launch_pairs(k_act_grad<true>, 0, tiles, st, m, a)
+             : launch_pairs(k_act_grad<false>, 1, tiles, st, m, a);
+}
+
+cudaError_t launch_dx_tc(const FfnGradArgs &f, cudaStream_t st) {
+  const bool glu = f.act == MOE_ACT_SWIGLU;
+  const uint64_t R = (uint64_t)f.rows, d = (uint64_t)f.d, F = (uint64_t)f.F, G = (uint64_t)f.G;
+  GemmMaps m;
+  bool ok = make_map(&m.a[0], f.dg, R, F, kRowTile) && make_map(&m.b[0], f.w1, G * F, d, kBlockK);
+  if (glu)
+    ok = ok && make_map(&m.a[1], f.du, R, F, kRowTile) &&
+         make_map(&m.b[1], f.w3, G * F, d, kBlockK);
+  if (!f.dx_f32) ok = ok && make_store_map(&m.o[0], f.dx, (uint64_t)f.dx_rows, d);
+  if (!ok) return cudaErrorInvalidValue;
+  GemmArgs a{};
+  a.poff = f.poff;
+  a.offsets = f.offsets;
+  a.dx_off = f.dx_off;
+  a.G = f.G;
+  a.N = f.d;
+  a.K = f.F;
+  a.nseg = glu ? 2 : 1;
+  a.out = f.dx;
+  a.out_f32 = f.dx_f32;
+  a.err = f.err;
+  return launch_pairs(k_pair_gemm<false>, 2, (long long)f.pair_tiles_ub * ceil_div(f.d, 256), st,
+                      m, a);
+}
+
+cudaError_t launch_dw_tc(const FfnGradArgs &f, cudaStream_t st) {
+  const uint64_t R = (uint64_t)f.rows, X = (uint64_t)f.x_rows, G = (uint64_t)f.G;
+  GemmMaps m;
+  GemmArgs a{};
+  bool ok = true;
+  long long tiles = 0;
+  auto job = [&](const void *p, uint64_t prows, const void *q, uint64_t qrows, void *out, int M,
+                 int N) {
+    if (out == nullptr) return;
+    const int j = a.njobs++;
+    ok = ok && make_map(&m.a[j], p, prows, (uint64_t)M, kBlockK) &&
+         make_map(&m.b[j], q, qrows, (uint64_t)N, kBlockK) &&
+         make_store_map(&m.o[j], out, G * (uint64_t)M, (uint64_t)N);
+    a.M[j] = M;
+    a.Ns[j] = N;
+    tiles += (long long)f.G * ceil_div(M, kPairM) * ceil_div(N, 256);
+  };
+  job(f.dg, R, f.x, X, f.dw1, f.F, f.d);
+  if (f.act == MOE_ACT_SWIGLU) job(f.du, R, f.x, X, f.dw3, f.F, f.d);
+  job(f.dy, X, f.h, R, f.dw2, f.d, f.F);
+  if (a.njobs == 0) return cudaSuccess;
+  if (!ok) return cudaErrorInvalidValue;
+  a.poff = f.poff;
+  a.offsets = f.offsets;
+  a.G = f.G;
+  a.err = f.err;
+  return launch_pairs(k_pair_gemm<true>, 3, tiles, st, m, a);
+}
+
+}  // namespace moe

@@ -30,17 +30,23 @@ struct PermuteBwdArgs {
 };
 cudaError_t launch_permute_bwd(const PermuteBwdArgs &a, int dtype, cudaStream_t st);
 
-// x and dy rows to every kept slot's row, and the slot's gate to row_w [R]
-struct GatherRowsArgs {
-  const void *x, *dy;    // [T, d] dtype
-  const int32_t *inv;    // [T*k]
-  const float *gate;     // [T*k]
-  void *x_perm, *dy_perm;  // [R, d] dtype
-  float *row_w;          // [R]
-  int T, k, R, row_bytes;
+// The experts' rows of x and dy in the padded layout of the experts' gradients: expert
+// g's rows begin at poff[g], rows up to poff[g+1] are zero (see launch_grad_tables).
+struct PadRowsArgs {
+  const void *x, *dy;      // [R, d] expert-contiguous rows, or [T, d] with inv
+  const int32_t *inv;      // [T*k] or nullptr; with it also:
+  const float *gate;       //   [T*k]
+  float *row_w;            //   [poff[G]] each row's gate, 0 for a padding row
+  int32_t *inv_pad;        //   [T*k] inv in the padded layout (-1: no row)
+  int T, k;
+  int R;                   // rows that offsets may name
+  const int32_t *offsets, *poff;  // [G+1] checked
+  int G, rows;             // rows: bound of poff[G]
+  void *x_pad, *dy_pad;    // [rows, d]
+  int row_bytes;
   int32_t *err;
 };
-cudaError_t launch_gather_rows(const GatherRowsArgs &a, cudaStream_t st);
+cudaError_t launch_pad_rows(const PadRowsArgs &a, cudaStream_t st);
 
 // ------------------------------------------------------------- route_grad.cu
 struct RouteBwdArgs {
@@ -65,34 +71,60 @@ struct RouteBwdArgs {
 size_t route_bwd_scratch_bytes(int T, int d, int E, int dtype);
 cudaError_t launch_route_bwd(const RouteBwdArgs &a, int dtype, cudaStream_t st);
 
-// --------------------------------------------------------------- ffn_grad.cu
+// -------------------------------------------- ffn_grad.cu, ffn_grad_tc.cu
 // Gradient of the grouped expert FFN (see GroupedFfnArgs). The pre-activations are
 // recomputed. With row_w the rows' output is weighted: dy is the gradient of
 // w_r E(x_r), and row_dot[r] = <dy_r, E(x_r)> is the gradient of w_r.
 struct FfnGradArgs {
-  const void *x, *dy;        // [rows, d] dtype
-  int rows;                  // rows allocated in x, dy, dx and the scratch
-  const int32_t *offsets;    // [G+1] checked (all zero when the caller's were invalid)
-  const int32_t *mprefix;    // [G+1]
-  int G, m_tiles_ub, d, F, act;
+  const void *x, *dy;        // [x_rows, d] dtype
+  int x_rows;                // rows allocated in x and dy (rows past the experts' are zero
+                             // up to the padding, or not allocated)
+  int rows;                  // rows allocated in the scratch, row_w and row_dot
+  const int32_t *offsets;    // [G+1] checked (all zero when the caller's were invalid):
+                             // expert g has offsets[g+1] - offsets[g] rows
+  const int32_t *poff;       // [G+1] its first row in all arrays but dx
+  const int32_t *dx_off;     // [G+1] its first row in dx: offsets or poff
+  const int32_t *mprefix;    // [G+1] prefix of the experts' 128-row tiles
+  int G, m_tiles_ub, pair_tiles_ub;  // bounds of the 128-row and the 256-row tiles
+  int d, F, act;
   const void *w1, *w3, *w2;
   const float *b1, *b2;
   const float *row_w;        // [rows] or nullptr
   float *row_dot;            // [rows] or nullptr
   float *dot_part;           // [ceil(F / 64), rows] scratch (with row_dot)
   void *h, *dg, *du;         // [rows, F] dtype scratch: w h, w dg, w du
-  void *dx;                  // [rows, d] or nullptr
-  int dx_f32;
+  void *dx;                  // [dx_rows, d] or nullptr
+  int dx_f32, dx_rows;
   void *dw1, *dw3, *dw2;     // [G, F, d], [G, F, d], [G, d, F] dtype, or nullptr
   float *db1, *db2;          // [G, F], [G, d] fp32, or nullptr
-  float *col_part;           // [m_tiles_ub, max(F, d)] scratch (with db1 or db2)
+  float *col_part;           // scratch of col_part_rows() x max(F, d) (with db1 or db2)
   int32_t *err;
 };
 cudaError_t launch_ffn_bwd(const FfnGradArgs &a, int dtype, cudaStream_t st);
-// offsets -> checked copy and tile prefix
-cudaError_t launch_grad_tables(const int32_t *offsets, int G, int max_rows, int32_t *checked,
-                               int32_t *mprefix, int32_t *err, cudaStream_t st);
-// one group of n rows: offsets {0, n} and its tile prefix
-cudaError_t launch_one_group(int n, int32_t *offsets, int32_t *mprefix, cudaStream_t st);
+// its steps on the tensor cores (bf16)
+cudaError_t launch_act_grad_tc(const FfnGradArgs &a, cudaStream_t st);
+cudaError_t launch_dx_tc(const FfnGradArgs &a, cudaStream_t st);
+cudaError_t launch_dw_tc(const FfnGradArgs &a, cudaStream_t st);
+
+// Rows to which each expert's are padded: the K slice of the tensor-core products of the
+// weights' gradients (bf16), none on CUDA cores.
+inline int row_pad(int dtype) { return dtype == MOE_DTYPE_F32 ? 1 : 64; }
+// bound of the padded rows of at most R rows of G experts
+inline long long padded_rows_ub(long long R, int G, int pad) {
+  const long long r = R + (long long)(pad - 1) * (R < G ? R : G);
+  return (r + pad - 1) / pad * pad;
+}
+// column-sum partials: one per 128-row tile, and (bf16) one per 32 rows
+inline long long col_part_rows(long long rows, int m_tiles, int dtype) {
+  const long long g = dtype == MOE_DTYPE_F32 ? 0 : (rows + 31) / 32;
+  return g > m_tiles ? g : m_tiles;
+}
+// offsets -> checked copy, tile prefix and the padded first rows
+cudaError_t launch_grad_tables(const int32_t *offsets, int G, int max_rows, int pad,
+                               int32_t *checked, int32_t *mprefix, int32_t *poff, int32_t *err,
+                               cudaStream_t st);
+// the tables of one group of n rows
+cudaError_t launch_one_group(int n, int pad, int32_t *offsets, int32_t *mprefix, int32_t *poff,
+                             cudaStream_t st);
 
 }  // namespace moe

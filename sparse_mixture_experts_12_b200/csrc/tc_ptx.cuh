@@ -154,11 +154,24 @@ __device__ __forceinline__ uint64_t sw128_desc(uint32_t saddr) {
   d |= (uint64_t)2 << 61;                    // SWIZZLE_128B
   return d;
 }
+// The same for an operand whose M (or N) index is the contiguous one: 64-element blocks of
+// it, each K rows of 128 bytes (8-row swizzle atoms, 1024 bytes apart along K), follow
+// each other every `block_bytes`. A K = 16 step is 2048 bytes.
+__device__ __forceinline__ uint64_t sw128_desc_mn(uint32_t saddr, uint32_t block_bytes) {
+  uint64_t d = 0;
+  d |= (uint64_t)((saddr >> 4) & 0x3FFFu);
+  d |= (uint64_t)(block_bytes >> 4) << 16;   // leading-dim byte offset: the next block
+  d |= (uint64_t)(1024 >> 4) << 32;          // stride-dim byte offset: the next 8 K rows
+  d |= (uint64_t)1 << 46;
+  d |= (uint64_t)2 << 61;
+  return d;
+}
 // Instruction descriptor, kind::f16: D fp32, A and B bf16, both K-major.
 __host__ __device__ constexpr uint32_t make_idesc(int M, int N) {
   return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) |
          ((uint32_t)(M >> 4) << 24);
 }
+constexpr uint32_t kIdescMnA = 1u << 15, kIdescMnB = 1u << 16;  // A, B not K-major
 
 __device__ __forceinline__ void decode_tile(int tile, const int *mpre, int G, int n_tiles,
                                             int &g, int &n, int &m) {
@@ -172,6 +185,42 @@ __device__ __forceinline__ void decode_tile(int tile, const int *mpre, int G, in
   const int local = tile - mpre[g] * n_tiles;
   n = local / mt;
   m = local % mt;
+}
+
+// The output path of one epilogue warp for one tile. With a map, a chunk whose 32
+// rows are all the expert's is staged in the warp's 2 KB shared-memory buffer (64-
+// byte swizzle) and written by one TMA store; other chunks use masked direct stores.
+struct EpiStore {
+  const CUtensorMap *map;  // 32 x 32 bf16 output boxes, or nullptr
+  uint8_t *stage;          // this warp's staging buffer
+  bool rows_full;          // all 32 rows of the warp belong to the expert
+  int row0;                // output row of lane 0
+};
+constexpr int kStoreBox = 32;
+constexpr int kStageOutBytes = kStoreBox * kStoreBox * 2;  // 2 KB per epilogue warp
+
+// one 32-row x 32-column bf16 chunk (pk = this lane's row) to global memory
+__device__ __forceinline__ void emit_chunk(const EpiStore &st, const uint4 (&pk)[4],
+                                           __nv_bfloat16 *dst_row, int col0) {
+  if (st.map != nullptr && st.rows_full) {
+    const int lane = threadIdx.x & 31;
+    if (lane == 0) bulk_wait_read_all();  // the previous store has read the buffer
+    __syncwarp();
+    uint4 *row = reinterpret_cast<uint4 *>(st.stage + lane * 64);
+    const int sw = (lane >> 1) & 3;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) row[q ^ sw] = pk[q];
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+      tma_store_2d(st.map, st.stage, col0, st.row0);
+      bulk_commit();
+    }
+  } else {
+    uint4 *dst = reinterpret_cast<uint4 *>(dst_row + col0);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) dst[q] = pk[q];
+  }
 }
 
 // erf by Abramowitz & Stegun, Handbook of Mathematical Functions, formula 7.1.26
@@ -362,7 +411,6 @@ inline bool make_map(CUtensorMap *map, const void *ptr, uint64_t rows, uint64_t 
 
 // 2-D bf16 map for TMA stores of 32 x 32 output tiles (64-byte rows, 64-byte swizzle:
 // the 16-byte chunk index of a row is XORed with (row >> 1) & 3 in shared memory).
-constexpr int kStoreBox = 32;
 inline bool make_store_map(CUtensorMap *map, void *ptr, uint64_t rows, uint64_t cols) {
   auto fn = encode_fn();
   if (fn == nullptr) return false;

@@ -1,6 +1,6 @@
 // Gradients of the token movement: the gate-weighted combine and the
-// expert-contiguous permutation (and the row gather that the whole layer's
-// gradient starts with).
+// expert-contiguous permutation, and the padded rows that the experts' gradients start
+// with.
 //
 //   combine  y[t] = sum_s g[t,s] Y[inv[t,s]]   dY[inv[t,s]] = g[t,s] dy[t]
 //                                              dg[t,s] = <dy[t], Y[inv[t,s]]>
@@ -198,52 +198,36 @@ __global__ void __launch_bounds__(kThreads) k_permute_bwd(PermuteBwdArgs a, int 
   }
 }
 
-__global__ void __launch_bounds__(kThreads) k_gather_rows(GatherRowsArgs a, int wpt) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int sub = warp % wpt;
-  const int t = blockIdx.x * (kWarps / wpt) + warp / wpt;
-  pdl_wait();
-  pdl_trigger();
-  if (t >= a.T) return;
-  int row[kMaxTopK];
-  bool any = false;
-#pragma unroll
-  for (int s = 0; s < kMaxTopK; ++s) {
-    row[s] = -1;
-    if (s < a.k) {
-      const size_t p = (size_t)t * a.k + s;
-      row[s] = checked_row(a.inv, p, a.R, a.err, lane == 0 && sub == 0);
-      if (row[s] >= 0 && lane == 0 && sub == 0) a.row_w[row[s]] = a.gate[p];
-    }
-    any |= row[s] >= 0;
-  }
-  if (!any) return;
+// NB vectors of two rows, requested before any is used, to up to kMaxTopK places
+template <int N>
+__device__ __forceinline__ void copy_rows(const PadRowsArgs &a, int from, const int (&to)[N],
+                                          int v0, int step) {
+  constexpr int NB = 4;
   const int nvec = a.row_bytes / 16;
   const uint4 *x = reinterpret_cast<const uint4 *>(static_cast<const char *>(a.x) +
-                                                   (size_t)t * a.row_bytes);
+                                                   (size_t)from * a.row_bytes);
   const uint4 *dy = reinterpret_cast<const uint4 *>(static_cast<const char *>(a.dy) +
-                                                    (size_t)t * a.row_bytes);
-  constexpr int NB = 4;
-  for (int v0 = sub * 32 + lane; v0 < nvec; v0 += 32 * wpt * NB) {
+                                                    (size_t)from * a.row_bytes);
+  for (; v0 < nvec; v0 += step * NB) {
     uint4 p[NB], q[NB];
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
-      const int v = v0 + 32 * wpt * b;
+      const int v = v0 + step * b;
       if (v < nvec) {
         p[b] = __ldg(x + v);
         q[b] = __ldg(dy + v);
       }
     }
 #pragma unroll
-    for (int s = 0; s < kMaxTopK; ++s) {
-      if (row[s] < 0) continue;
-      uint4 *xo = reinterpret_cast<uint4 *>(static_cast<char *>(a.x_perm) +
-                                            (size_t)row[s] * a.row_bytes);
-      uint4 *yo = reinterpret_cast<uint4 *>(static_cast<char *>(a.dy_perm) +
-                                            (size_t)row[s] * a.row_bytes);
+    for (int s = 0; s < N; ++s) {
+      if (to[s] < 0) continue;
+      uint4 *xo = reinterpret_cast<uint4 *>(static_cast<char *>(a.x_pad) +
+                                            (size_t)to[s] * a.row_bytes);
+      uint4 *yo = reinterpret_cast<uint4 *>(static_cast<char *>(a.dy_pad) +
+                                            (size_t)to[s] * a.row_bytes);
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
-        const int v = v0 + 32 * wpt * b;
+        const int v = v0 + step * b;
         if (v < nvec) {
           xo[v] = p[b];
           yo[v] = q[b];
@@ -251,6 +235,79 @@ __global__ void __launch_bounds__(kThreads) k_gather_rows(GatherRowsArgs a, int 
       }
     }
   }
+}
+__device__ __forceinline__ void zero_rows(const PadRowsArgs &a, int to, int v0, int step) {
+  const uint4 z = make_uint4(0u, 0u, 0u, 0u);
+  uint4 *xo = reinterpret_cast<uint4 *>(static_cast<char *>(a.x_pad) + (size_t)to * a.row_bytes);
+  uint4 *yo = reinterpret_cast<uint4 *>(static_cast<char *>(a.dy_pad) + (size_t)to * a.row_bytes);
+  for (int v = v0; v < a.row_bytes / 16; v += step) xo[v] = yo[v] = z;
+}
+// last g < G with first[g] <= r (r below first[G])
+__device__ __forceinline__ int group_of(const int32_t *first, int G, int r) {
+  int lo = 0, hi = G - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (first[mid] <= r) lo = mid; else hi = mid - 1;
+  }
+  return lo;
+}
+
+// Expert-contiguous rows to padded rows: a warp per padded row.
+__global__ void __launch_bounds__(kThreads) k_pad_rows(PadRowsArgs a) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  pdl_wait();
+  pdl_trigger();
+  const int p = blockIdx.x * kWarps + warp;
+  if (p >= a.poff[a.G]) return;
+  const int g = group_of(a.poff, a.G, p), local = p - a.poff[g];
+  if (local < a.offsets[g + 1] - a.offsets[g]) {
+    const int to[1] = {p};
+    copy_rows<1>(a, a.offsets[g] + local, to, lane, 32);
+  } else {
+    zero_rows(a, p, lane, 32);
+  }
+}
+
+// Tokens to their slots' padded rows: `wpt` warps per token in the first blocks; the
+// blocks behind them zero each expert's padding rows.
+__global__ void __launch_bounds__(kThreads) k_gather_rows(PadRowsArgs a, int wpt, int token_blocks) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  pdl_wait();
+  pdl_trigger();
+  if ((int)blockIdx.x >= token_blocks) {
+    const int g = blockIdx.x - token_blocks;
+    for (int p = a.poff[g] + a.offsets[g + 1] - a.offsets[g] + warp; p < a.poff[g + 1];
+         p += kWarps) {
+      zero_rows(a, p, lane, 32);
+      if (lane == 0) a.row_w[p] = 0.f;
+    }
+    return;
+  }
+  const int sub = warp % wpt;
+  const int t = blockIdx.x * (kWarps / wpt) + warp / wpt;
+  if (t >= a.T) return;
+  const int live = a.offsets[a.G];  // rows past it belong to nobody
+  int row[kMaxTopK];
+  bool any = false;
+#pragma unroll
+  for (int s = 0; s < kMaxTopK; ++s) {
+    row[s] = -1;
+    if (s < a.k) {
+      const size_t p = (size_t)t * a.k + s;
+      const bool first = lane == 0 && sub == 0;
+      const int r = checked_row(a.inv, p, live, a.err, first);
+      if (r >= 0) {
+        const int g = group_of(a.offsets, a.G, r);
+        row[s] = r + a.poff[g] - a.offsets[g];
+      }
+      if (first) {
+        a.inv_pad[p] = row[s];
+        if (row[s] >= 0) a.row_w[row[s]] = a.gate[p];
+      }
+    }
+    any |= row[s] >= 0;
+  }
+  if (any) copy_rows<kMaxTopK>(a, t, row, sub * 32 + lane, 32 * wpt);
 }
 
 // Warps per token: one while the tokens alone give the GPU its warps, more (up to
@@ -292,11 +349,12 @@ cudaError_t launch_permute_bwd(const PermuteBwdArgs &a, int dtype, cudaStream_t 
                        : permute_bwd<__nv_bfloat16, __nv_bfloat16>(a, st);
 }
 
-cudaError_t launch_gather_rows(const GatherRowsArgs &a, cudaStream_t st) {
-  if (a.T == 0) return cudaSuccess;
+cudaError_t launch_pad_rows(const PadRowsArgs &a, cudaStream_t st) {
+  if (a.inv == nullptr)
+    return launch_pdl(k_pad_rows, dim3(ceil_div(a.rows, kWarps)), dim3(kThreads), 0, st, a);
   const int wpt = warps_per_token(a.T, a.row_bytes / 16);
-  return launch_pdl(k_gather_rows, dim3(ceil_div(a.T, kWarps / wpt)), dim3(kThreads), 0, st, a,
-                    wpt);
+  const int tb = ceil_div(a.T, kWarps / wpt);
+  return launch_pdl(k_gather_rows, dim3(tb + a.G), dim3(kThreads), 0, st, a, wpt, tb);
 }
 
 }  // namespace moe

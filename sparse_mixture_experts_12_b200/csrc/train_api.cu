@@ -8,9 +8,9 @@ namespace moe {
 namespace {
 
 enum Buf {
-  G_ERR, G_OFFSETS, G_MPREFIX, G_SH_OFFSETS, G_SH_MPREFIX, G_H, G_DG, G_DU, G_COL, G_DLOGITS,
-  G_ROUTE, G_XPERM, G_DYPERM, G_DXPERM, G_ROW_W, G_ROW_DOT, G_DOT_PART, G_DX_ROUTER, G_DX_SHARED,
-  G_NBUF
+  G_ERR, G_OFFSETS, G_MPREFIX, G_POFF, G_SH_OFFSETS, G_SH_MPREFIX, G_SH_POFF, G_H, G_DG, G_DU,
+  G_COL, G_DLOGITS, G_ROUTE, G_X, G_DY, G_INV, G_DX, G_ROW_W, G_ROW_DOT, G_DOT_PART, G_DX_ROUTER,
+  G_DX_SHARED, G_NBUF
 };
 
 struct Layout {
@@ -18,33 +18,47 @@ struct Layout {
   size_t total;
 };
 
+size_t elem_bytes(const moe_cfg_t &c) { return c.dtype == MOE_DTYPE_F32 ? 4 : 2; }
+
+// rows of the experts' padded buffers
+long long scratch_rows(const moe_cfg_t &c) {
+  return padded_rows_ub(expert_rows(c), c.n_experts, row_pad(c.dtype));
+}
+
+// bound of the experts' 256-row tiles
+int pair_tiles_ub(long long rows, int groups) {
+  return (int)(rows / (2 * kRowTile) + (rows < groups ? rows : groups));
+}
+
 size_t larger(size_t a, size_t b) { return a > b ? a : b; }
 
 Layout layout_for(const moe_cfg_t &c) {
   const size_t T = (size_t)c.n_tokens, E = (size_t)c.n_experts;
   const size_t d = (size_t)c.d_model, F = (size_t)c.d_ff;
-  const size_t eb = c.dtype == MOE_DTYPE_F32 ? 4 : 2;
-  const size_t R = (size_t)expert_rows(c);
+  const size_t eb = elem_bytes(c);
   const size_t Fs = (size_t)c.n_shared * (size_t)c.d_ff_shared;
   const bool glu = c.act == MOE_ACT_SWIGLU;
   const bool tc = !expert_choice(c);  // moe_backward's own buffers: token choice
-  // the shared experts run after the routed ones, in the same h / dg / du
-  const size_t act = larger(R * F, T * Fs);
+  // the experts' rows, padded; the shared experts run after the routed ones, in the same
+  // h / dg / du
+  const size_t R = (size_t)scratch_rows(c), Ts = (size_t)padded_rows_ub(c.n_tokens, 1, row_pad(c.dtype));
+  const size_t act = larger(R * F, Ts * Fs);
+  const int tiles = m_tiles_ub(expert_rows(c), c.n_experts);
+  const bool copies = c.dtype != MOE_DTYPE_F32 || tc;  // of x and dy rows
   size_t sz[G_NBUF];
   sz[G_ERR] = 4 * sizeof(int32_t);
-  sz[G_OFFSETS] = (E + 1) * 4;
-  sz[G_MPREFIX] = (E + 1) * 4;
-  sz[G_SH_OFFSETS] = 2 * 4;
-  sz[G_SH_MPREFIX] = 2 * 4;
+  sz[G_OFFSETS] = sz[G_MPREFIX] = sz[G_POFF] = (E + 1) * 4;
+  sz[G_SH_OFFSETS] = sz[G_SH_MPREFIX] = sz[G_SH_POFF] = 2 * 4;
   sz[G_H] = act * eb;
   sz[G_DG] = act * eb;
   sz[G_DU] = (glu || Fs ? act : 0) * eb;
-  sz[G_COL] = glu ? 0 : (size_t)m_tiles_ub((long long)R, c.n_experts) * larger(F, d) * 4;
+  sz[G_COL] = glu ? 0 : (size_t)col_part_rows((long long)R, tiles, c.dtype) * larger(F, d) * 4;
   sz[G_DLOGITS] = tc ? T * E * 4 : 0;
   sz[G_ROUTE] = tc ? route_bwd_scratch_bytes(c.n_tokens, c.d_model, c.n_experts, c.dtype) : 0;
-  sz[G_XPERM] = tc ? R * d * eb : 0;
-  sz[G_DYPERM] = tc ? R * d * eb : 0;
-  sz[G_DXPERM] = tc ? R * d * 4 : 0;
+  sz[G_X] = copies ? R * d * eb : 0;
+  sz[G_DY] = copies ? R * d * eb : 0;
+  sz[G_INV] = tc ? T * (size_t)c.top_k * 4 : 0;
+  sz[G_DX] = tc ? R * d * 4 : 0;
   sz[G_ROW_W] = tc ? R * 4 : 0;
   sz[G_ROW_DOT] = tc ? R * 4 : 0;
   sz[G_DOT_PART] = tc ? R * (size_t)ceil_div(c.d_ff, 64) * 4 : 0;
@@ -86,8 +100,6 @@ moe_status_t check_expert_grads(const moe_cfg_t &c, const moe_weights_t *w, cons
   return check_ptrs({{g.w1, false}, {g.w3, false}, {g.w2, false}, {g.b1, false}, {g.b2, false}});
 }
 
-size_t elem_bytes(const moe_cfg_t &c) { return c.dtype == MOE_DTYPE_F32 ? 4 : 2; }
-
 moe_status_t zero(void *p, size_t bytes, cudaStream_t st) {
   return p ? cuda_status(cudaMemsetAsync(p, 0, bytes, st)) : MOE_OK;
 }
@@ -109,11 +121,13 @@ moe_status_t zero_expert_grads(const moe_cfg_t &c, const moe_grads_t &g, cudaStr
 FfnGradArgs expert_args(const moe_cfg_t &c, const moe_weights_t &w, const moe_grads_t &g, void *ws,
                         const Layout &L) {
   FfnGradArgs a{};
-  a.rows = (int)expert_rows(c);
+  a.rows = a.x_rows = (int)scratch_rows(c);
   a.offsets = at<int32_t>(ws, L, G_OFFSETS);
   a.mprefix = at<int32_t>(ws, L, G_MPREFIX);
+  a.poff = at<int32_t>(ws, L, G_POFF);
   a.G = c.n_experts;
-  a.m_tiles_ub = m_tiles_ub(a.rows, c.n_experts);
+  a.m_tiles_ub = m_tiles_ub(expert_rows(c), c.n_experts);
+  a.pair_tiles_ub = pair_tiles_ub(expert_rows(c), c.n_experts);
   a.d = c.d_model;
   a.F = c.d_ff;
   a.act = c.act;
@@ -131,6 +145,30 @@ FfnGradArgs expert_args(const moe_cfg_t &c, const moe_weights_t &w, const moe_gr
   a.dw2 = g.w2;
   a.db1 = g.b1;
   a.db2 = g.b2;
+  a.err = at<int32_t>(ws, L, G_ERR);
+  return a;
+}
+
+moe_status_t expert_tables(const moe_cfg_t &c, const int32_t *offsets, void *ws, const Layout &L,
+                           cudaStream_t st) {
+  return cuda_status(launch_grad_tables(
+      offsets, c.n_experts, (int)expert_rows(c), row_pad(c.dtype), at<int32_t>(ws, L, G_OFFSETS),
+      at<int32_t>(ws, L, G_MPREFIX), at<int32_t>(ws, L, G_POFF), at<int32_t>(ws, L, G_ERR), st));
+}
+
+// copies of the experts' rows of x and dy, padded
+PadRowsArgs pad_args(const moe_cfg_t &c, const void *x, const void *dy, void *ws, const Layout &L) {
+  PadRowsArgs a{};
+  a.x = x;
+  a.dy = dy;
+  a.R = (int)expert_rows(c);
+  a.offsets = at<int32_t>(ws, L, G_OFFSETS);
+  a.poff = at<int32_t>(ws, L, G_POFF);
+  a.G = c.n_experts;
+  a.rows = (int)scratch_rows(c);
+  a.x_pad = at<void>(ws, L, G_X);
+  a.dy_pad = at<void>(ws, L, G_DY);
+  a.row_bytes = (int)(c.d_model * elem_bytes(c));
   a.err = at<int32_t>(ws, L, G_ERR);
   return a;
 }
@@ -250,15 +288,23 @@ MOE_API moe_status_t moe_expert_ffn_backward(const moe_cfg_t *cfg, const moe_wei
   moe_grads_t g{};
   if (grads) g = *grads;
   MOE_TRY(check_expert_grads(c, w, g));
-  if (c.n_tokens == 0) return zero_expert_grads(c, g, stream);
+  if (expert_rows(c) == 0) return zero_expert_grads(c, g, stream);
   MOE_TRY(check_ptrs({{x_perm, true}, {offsets, true}, {dy_perm, true}, {dx_perm, false}}));
   const Layout L = layout_for(c);
   FfnGradArgs a = expert_args(c, *w, g, ws, L);
-  a.x = x_perm;
-  a.dy = dy_perm;
+  MOE_TRY(expert_tables(c, offsets, ws, L, stream));
+  if (row_pad(c.dtype) == 1) {
+    a.x = x_perm;
+    a.dy = dy_perm;
+  } else {
+    const PadRowsArgs p = pad_args(c, x_perm, dy_perm, ws, L);
+    MOE_CUDA(launch_pad_rows(p, stream));
+    a.x = p.x_pad;
+    a.dy = p.dy_pad;
+  }
   a.dx = dx_perm;
-  MOE_CUDA(launch_grad_tables(offsets, a.G, a.rows, at<int32_t>(ws, L, G_OFFSETS),
-                              at<int32_t>(ws, L, G_MPREFIX), a.err, stream));
+  a.dx_off = a.offsets;
+  a.dx_rows = (int)expert_rows(c);
   return cuda_status(launch_ffn_bwd(a, c.dtype, stream));
 }
 
@@ -292,31 +338,26 @@ MOE_API moe_status_t moe_backward(const moe_cfg_t *cfg, const moe_weights_t *w, 
   const Layout L = layout_for(c);
   // 1. the experts' rows of x and dy, and each row's gate
   FfnGradArgs a = expert_args(c, *w, g, ws, L);
-  MOE_CUDA(launch_grad_tables(taps->offsets, a.G, a.rows, at<int32_t>(ws, L, G_OFFSETS),
-                              at<int32_t>(ws, L, G_MPREFIX), a.err, stream));
-  GatherRowsArgs gr{};
-  gr.x = x;
-  gr.dy = dy;
+  MOE_TRY(expert_tables(c, taps->offsets, ws, L, stream));
+  PadRowsArgs gr = pad_args(c, x, dy, ws, L);
   gr.inv = taps->inv;
   gr.gate = taps->topk_gate;
-  gr.x_perm = at<void>(ws, L, G_XPERM);
-  gr.dy_perm = at<void>(ws, L, G_DYPERM);
   gr.row_w = at<float>(ws, L, G_ROW_W);
+  gr.inv_pad = at<int32_t>(ws, L, G_INV);
   gr.T = c.n_tokens;
   gr.k = c.top_k;
-  gr.R = a.rows;
-  gr.row_bytes = (int)(c.d_model * elem_bytes(c));
-  gr.err = a.err;
-  MOE_CUDA(launch_gather_rows(gr, stream));
+  MOE_CUDA(launch_pad_rows(gr, stream));
   // 2. the routed experts; the gates' gradient comes from their rows
   const bool router = dx || g.w_router || g.b_router;
-  a.x = gr.x_perm;
-  a.dy = gr.dy_perm;
+  a.x = gr.x_pad;
+  a.dy = gr.dy_pad;
   a.row_w = gr.row_w;
   a.row_dot = router ? at<float>(ws, L, G_ROW_DOT) : nullptr;
   a.dot_part = at<float>(ws, L, G_DOT_PART);
-  a.dx = dx ? at<void>(ws, L, G_DXPERM) : nullptr;
+  a.dx = dx ? at<void>(ws, L, G_DX) : nullptr;
   a.dx_f32 = 1;
+  a.dx_off = a.poff;
+  a.dx_rows = a.rows;
   MOE_CUDA(launch_ffn_bwd(a, c.dtype, stream));
   // 3. the router
   if (router) {
@@ -327,7 +368,8 @@ MOE_API moe_status_t moe_backward(const moe_cfg_t *cfg, const moe_weights_t *w, 
     r.topk_idx = taps->topk_idx;
     r.counts = taps->counts;
     r.row_dot = a.row_dot;
-    r.inv = taps->inv;
+    r.inv = gr.inv_pad;
+    r.R = a.rows;
     r.d_losses = d_losses;
     r.dx = dx ? at<float>(ws, L, G_DX_ROUTER) : nullptr;
     r.dw = g.w_router;
@@ -338,15 +380,19 @@ MOE_API moe_status_t moe_backward(const moe_cfg_t *cfg, const moe_weights_t *w, 
   float *dx_shared = nullptr;
   if (c.n_shared > 0 && (dx || g.ws_gate || g.ws_up || g.ws_down)) {
     FfnGradArgs s{};
-    int32_t *so = at<int32_t>(ws, L, G_SH_OFFSETS), *sm = at<int32_t>(ws, L, G_SH_MPREFIX);
-    MOE_CUDA(launch_one_group(c.n_tokens, so, sm, stream));
+    int32_t *so = at<int32_t>(ws, L, G_SH_OFFSETS), *sm = at<int32_t>(ws, L, G_SH_MPREFIX),
+            *sp = at<int32_t>(ws, L, G_SH_POFF);
+    MOE_CUDA(launch_one_group(c.n_tokens, row_pad(c.dtype), so, sm, sp, stream));
     s.x = x;
     s.dy = dy;
-    s.rows = c.n_tokens;
+    s.x_rows = c.n_tokens;  // the padding rows lie past the operands' bounds: read as zero
+    s.rows = (int)padded_rows_ub(c.n_tokens, 1, row_pad(c.dtype));
     s.offsets = so;
     s.mprefix = sm;
+    s.poff = s.dx_off = sp;
     s.G = 1;
     s.m_tiles_ub = ceil_div(c.n_tokens, kRowTile);
+    s.pair_tiles_ub = ceil_div(c.n_tokens, 2 * kRowTile);
     s.d = c.d_model;
     s.F = c.n_shared * c.d_ff_shared;
     s.act = MOE_ACT_SWIGLU;
@@ -358,6 +404,7 @@ MOE_API moe_status_t moe_backward(const moe_cfg_t *cfg, const moe_weights_t *w, 
     s.du = at<void>(ws, L, G_DU);
     s.dx = dx_shared = dx ? at<float>(ws, L, G_DX_SHARED) : nullptr;
     s.dx_f32 = 1;
+    s.dx_rows = c.n_tokens;
     s.dw1 = g.ws_gate;
     s.dw3 = g.ws_up;
     s.dw2 = g.ws_down;
@@ -369,7 +416,7 @@ MOE_API moe_status_t moe_backward(const moe_cfg_t *cfg, const moe_weights_t *w, 
     PermuteBwdArgs p{};
     p.dx_perm = a.dx;
     p.dx_perm_f32 = 1;
-    p.inv = taps->inv;
+    p.inv = gr.inv_pad;
     p.add0 = at<float>(ws, L, G_DX_ROUTER);
     p.add1 = dx_shared;
     p.dx = dx;
