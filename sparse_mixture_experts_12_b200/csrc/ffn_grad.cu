@@ -323,7 +323,8 @@ __global__ void k_one_group(int n, int pad, int32_t *offsets, int32_t *mprefix, 
   poff[1] = ceil_div(n, pad) * pad;
 }
 
-// `groups`: db1's partials are one per 32 padded rows, else one per 128-row tile
+// `groups`: the partials of db1 are one per 32 padded rows, those of row_dot one per 32
+// columns; else one per 128-row and per 64-column tile
 template <typename T>
 cudaError_t bias_and_row_grads(const FfnGradArgs &a, bool groups, cudaStream_t st) {
   cudaError_t e = cudaSuccess;
@@ -343,7 +344,7 @@ cudaError_t bias_and_row_grads(const FfnGradArgs &a, bool groups, cudaStream_t s
   }
   if (a.row_dot)
     e = launch_pdl(k_row_dot<T>, dim3(ceil_div(a.rows, 8)), dim3(256), 0, st, a,
-                   ceil_div(a.F, 64));
+                   groups ? a.F / 32 : ceil_div(a.F, BN));
   return e;
 }
 

@@ -15,7 +15,7 @@
 //
 // A CTA pair's roles, barriers and bounded waits are those of the forward's GEMM
 // (ffn_tc.cu): warp 0 of each CTA loads its operand halves, warp 1 of the leader issues
-// the MMAs, warps 4-11 drain tensor memory; a wait that runs out records
+// the MMAs, warps 4-19 drain tensor memory; a wait that runs out records
 // MOE_DEVERR_WAIT_TIMEOUT and ends both CTAs.
 #include <algorithm>
 #include <mutex>
@@ -30,12 +30,16 @@ namespace {
 using namespace tc;
 
 constexpr int kPairM = 2 * kRowTile;
-constexpr int kStages = 6;
+constexpr int kStages = 5;
 constexpr int kOperand = kRowTile * kBlockK * 2;  // 16 KB: a CTA's half of a 256-wide operand
 constexpr int kStageBytes = 2 * kOperand;
 constexpr int kMnBlock = kBlockK * kBlockK * 2;   // 8 KB: 64 K rows x 64 contiguous elements
-constexpr int kThreads = 384;
-constexpr int kEpiWarps = 8;
+// Sixteen epilogue warps, four to a lane quarter of tensor memory: the activations'
+// derivatives take some 25 instructions an element in long dependent chains, and the
+// output stores wait for shared memory to be read; eight warps did not keep up.
+constexpr int kEpiWarps = 16;
+constexpr int kThreads = 128 + 32 * kEpiWarps;
+constexpr int kStageOut = 4096;  // output staging of an epilogue warp
 constexpr int kTmemCols = 512;
 constexpr uint64_t kDrainNs = 50000000ull;
 
@@ -47,11 +51,10 @@ struct Ctl {
   uint64_t drain;
   uint32_t tmem_base;
   int abort_flag;
-  int pre[kMaxExperts + 1];   // prefix of the experts' 256-row tiles
-  int poff[kMaxExperts + 1];  // first (padded) row of each expert
+  int pre[kMaxExperts + 1];  // prefix of the experts' 256-row tiles
 };
 constexpr size_t kRing = (size_t)kStages * kStageBytes;
-constexpr size_t kSmemBytes = kRing + (size_t)kEpiWarps * kStageOutBytes + sizeof(Ctl) + 1024;
+constexpr size_t kSmemBytes = kRing + (size_t)kEpiWarps * kStageOut + sizeof(Ctl) + 1024;
 
 // what both kernels do before their roles split up; returns the tensor memory's base
 struct Setup {
@@ -65,7 +68,7 @@ __device__ __forceinline__ Setup set_up(uint8_t *raw, const int32_t *poff, int G
   Setup s;
   s.smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) &
                                        ~static_cast<uintptr_t>(1023));
-  s.ctl = reinterpret_cast<Ctl *>(s.smem + kRing + kEpiWarps * kStageOutBytes);
+  s.ctl = reinterpret_cast<Ctl *>(s.smem + kRing + kEpiWarps * kStageOut);
   Ctl *ctl = s.ctl;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   s.rank = (int)cluster_ctarank();
@@ -87,7 +90,6 @@ __device__ __forceinline__ Setup set_up(uint8_t *raw, const int32_t *poff, int G
     tmem_relinquish_pair();
   }
   pdl_wait();
-  for (int i = tid; i <= G; i += kThreads) ctl->poff[i] = poff[i];
   if (warp == 1) {
     const int per = ceil_div(G, 32);
     const int j0 = min(G, lane * per), j1 = min(G, j0 + per);
@@ -164,22 +166,40 @@ __device__ __forceinline__ void load_mn(const CUtensorMap *map, uint32_t bar, ui
   tma_load_2d_pair(map, bar, dst + kMnBlock, c + kBlockK, row);
 }
 
-__device__ __forceinline__ void pack32(const float (&f)[32], uint4 (&pk)[4]) {
+// The output path of an epilogue warp: 4 KB of shared memory that TMA stores read, as two
+// 32 x 32 chunks in turn or one of 32 x 64. One lane issues the stores and, before a
+// buffer is written again, waits until they have read it.
+struct Stage {
+  uint8_t *buf;
+  int turn = 0;
+  // 32 rows (a lane each) x 32 columns: the lane's 64 bytes, 16-byte pieces swizzled
+  __device__ __forceinline__ void put32(const CUtensorMap *map, const uint32_t *p, int col0,
+                                        int row0) {
+    const int lane = threadIdx.x & 31;
+    if (lane == 0) bulk_wait_read<1>();
+    __syncwarp();
+    uint8_t *b = buf + turn * (kStageOut / 2);
+    uint4 *row = reinterpret_cast<uint4 *>(b + lane * 64);
+    const int sw = (lane >> 1) & 3;
 #pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    float h[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) h[j] = f[q * 8 + j];
-    pk[q] = pack16(h);
+    for (int q = 0; q < 4; ++q)
+      row[q ^ sw] = make_uint4(p[4 * q], p[4 * q + 1], p[4 * q + 2], p[4 * q + 3]);
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+      tma_store_2d(map, b, col0, row0);
+      bulk_commit();
+    }
+    turn ^= 1;
   }
-}
+};
 
 // ================================================================= activations
 struct ActArgs {
   const int32_t *poff, *offsets;  // padded first rows; the experts' row counts
   int G, F, d, act, n_tiles;
   const float *b1, *row_w;
-  float *dot_part;  // [ceil(F / 64), rows] or nullptr
+  float *dot_part;  // [F / 32, rows] or nullptr
   float *col_part;  // [rows / 32, F] or nullptr
   void *h, *dg, *du;
   int rows;
@@ -205,18 +225,24 @@ __device__ __forceinline__ float column_sum16(float (&v)[16], int lane) {
   return v[0] + __shfl_xor_sync(0xffffffffu, v[0], 16);
 }
 
-// d gelu / dv (with the forward's erf) and gelu
+// gelu and d gelu / dv, with the forward's erf (formula 7.1.26 of Abramowitz & Stegun): its
+// exp(-(v / sqrt 2)^2) is the density's exponential as well.
 __device__ __forceinline__ void gelu_and_slope(float v, float &h, float &s) {
-  const float c = 0.5f * (1.f + erf_as7126(v * 0.70710678118654752f));
+  const float e = __expf(-0.5f * v * v);
+  const float t = rcp_approx(fmaf(0.3275911f * 0.70710678118654752f, fabsf(v), 1.f));
+  const float p =
+      fmaf(fmaf(fmaf(fmaf(0.5f * 1.061405429f, t, -0.5f * 1.453152027f), t, 0.5f * 1.421413741f),
+                t, -0.5f * 0.284496736f), t, 0.5f * 0.254829592f) * t;
+  const float c = 0.5f + copysignf(fmaf(-p, e, 0.5f), v);  // (1 + erf(v / sqrt 2)) / 2
   h = v * c;
-  s = c + v * 0.39894228040143268f * __expf(-0.5f * v * v);
+  s = fmaf(v * 0.39894228040143268f, e, c);
 }
 
-// One tile: 256 rows x 128 columns of F. Tensor memory: a | u at columns 0-255 (SwiGLU) or
+// One tile: 256 rows x 128 columns of F (32 to an epilogue warp). Tensor memory: a | u at columns 0-255 (SwiGLU) or
 // a at 0 / 128 (alternating, MLP); q at 256 / 384 (alternating). With SwiGLU the a | u
 // region is single: the next tile's first kLead slices of q run while it is drained.
 constexpr int kTileN = 128;
-constexpr int kLead = 16;
+constexpr int kLead = 24;
 
 template <bool GLU>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -244,7 +270,7 @@ k_act_grad(const __grid_constant__ ActMaps maps, ActArgs a) {
     for (int t = s.c0; ok && t < total; t += s.cstep) {
       int g, n, m;
       decode_tile(t, ctl->pre, a.G, a.n_tiles, g, n, m);
-      const int arow = ctl->poff[g] + m * kPairM + s.rank * kRowTile;
+      const int arow = a.poff[g] + m * kPairM + s.rank * kRowTile;
       const int n0 = n * kTileN;
       auto stage_for = [&](int bytes) -> uint8_t * {
         if (!wait_on(s, &ctl->empty[ring.stage], ring.phase ^ 1u, a.err, 21)) return nullptr;
@@ -331,99 +357,99 @@ k_act_grad(const __grid_constant__ ActMaps maps, ActArgs a) {
     }
   } else if (warp >= 4) {
     // ----------------------------------------------------------------- epilogue
-    const int ew = warp & 3, half = (warp - 4) >> 2;
+    const int ew = warp & 3, part = (warp - 4) >> 2;  // lanes 32 ew.., columns 32 part..
     const uint32_t tempty0 = mapa_rank(smem_u32(&ctl->tempty[0]), 0);
-    uint8_t *stage_out = s.smem + kRing + (warp - 4) * kStageOutBytes;
+    Stage out{s.smem + kRing + (warp - 4) * kStageOut};
     int it = 0;
     for (int t = s.c0; t < total; t += s.cstep, ++it) {
       int g, n, m;
       decode_tile(t, ctl->pre, a.G, a.n_tiles, g, n, m);
       const int buf = it & 1;
       const int lrow = m * kPairM + s.rank * kRowTile + ew * 32;  // the warp's first row
-      const int base = ctl->poff[g], prow = base + lrow;
-      const bool mine = prow < ctl->poff[g + 1];  // padded groups of 32 rows: all or none
+      const int prow = a.poff[g] + lrow, col0 = n * kTileN + part * 32;
+      // padded groups of 32 rows belong to the expert as a whole or not at all; F is a
+      // multiple of 64
+      const bool mine = prow < a.poff[g + 1] && col0 < a.F;
       const bool valid = lrow + lane < a.offsets[g + 1] - a.offsets[g];
-      const float w = (valid && mine) ? (a.row_w ? a.row_w[prow + lane] : 1.f) : 0.f;
+      const float w = (a.row_w && mine) ? a.row_w[prow + lane] : 1.f;
       bool ok = wait_on(s, &ctl->tfull[buf], (it >> 1) & 1, a.err, 24);
       __syncwarp();
       if (!__all_sync(0xffffffffu, ok)) break;
       tc_fence_after();
-      const uint32_t tq = s.tmem + ((uint32_t)(ew * 32) << 16) + 256u + (uint32_t)(buf * kTileN);
-      const uint32_t ta = s.tmem + ((uint32_t)(ew * 32) << 16) +
-                          (GLU ? 0u : (uint32_t)(buf * kTileN));
+      const uint32_t lane_base = s.tmem + ((uint32_t)(ew * 32) << 16) + (uint32_t)(part * 32);
+      const uint32_t tq = lane_base + 256u + (uint32_t)(buf * kTileN);
+      const uint32_t ta = lane_base + (GLU ? 0u : (uint32_t)(buf * kTileN));
       float dot = 0.f;
-#pragma unroll 1
-      for (int c = 2 * half; c < 2 * half + 2; ++c) {
-        const int col0 = n * kTileN + c * 32;
-        if (!mine || col0 >= a.F) break;  // F is a multiple of 64
-        uint32_t hp[16], gp[16], up[GLU ? 16 : 1];  // packed pairs of columns
+      uint32_t hp[16], gp[16], up[GLU ? 16 : 1];  // packed pairs of columns
+      if (mine) {
 #pragma unroll
         for (int j2 = 0; j2 < 2; ++j2) {
-          uint32_t av[16], uv[16], qv[16];
-          tmem_ld16(ta + c * 32 + j2 * 16, av);
-          if (GLU) tmem_ld16(ta + kTileN + c * 32 + j2 * 16, uv);
-          tmem_ld16(tq + c * 32 + j2 * 16, qv);
-          tmem_ld_wait();
-          float h[16], da[16], du[16];
+          uint32_t av[16], uv[GLU ? 16 : 1], qv[16];
+          tmem_ld16(ta + j2 * 16, av);
+          if constexpr (GLU) tmem_ld16(ta + kTileN + j2 * 16, uv);
+          tmem_ld16(tq + j2 * 16, qv);
+          float bias[GLU ? 1 : 16];
+          if constexpr (!GLU) {
 #pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            const float q = __uint_as_float(qv[j]);
-            float v = __uint_as_float(av[j]);
-            if (GLU) {
-              const float u = __uint_as_float(uv[j]);
-              const float sg = __fdividef(1.f, 1.f + __expf(-v));
-              const float si = v * sg;
-              h[j] = si * u;
-              du[j] = q * si;
-              da[j] = q * u * fmaf(si, 1.f - sg, sg);
-            } else {
-              if (a.b1) v += __ldg(a.b1 + (size_t)g * a.F + col0 + j2 * 16 + j);
-              float sl;
-              if (a.act == MOE_ACT_RELU) {
-                h[j] = fmaxf(v, 0.f);
-                sl = v > 0.f ? 1.f : 0.f;
-              } else {
-                gelu_and_slope(v, h[j], sl);
-              }
-              da[j] = q * sl;
+            for (int j = 0; j < 16; j += 4) {  // the same for every lane
+              const float4 b = a.b1 ? __ldg(reinterpret_cast<const float4 *>(
+                                          a.b1 + (size_t)g * a.F + col0 + j2 * 16 + j))
+                                    : make_float4(0.f, 0.f, 0.f, 0.f);
+              bias[j] = b.x; bias[j + 1] = b.y; bias[j + 2] = b.z; bias[j + 3] = b.w;
             }
-            dot = fmaf(q, h[j], dot);
           }
-          // rows past the expert's: zeros, whatever the weights hold
+          tmem_ld_wait();
+          float da[16];
 #pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            h[j] = valid ? w * h[j] : 0.f;
-            da[j] = valid ? w * da[j] : 0.f;
-            if (GLU) du[j] = valid ? w * du[j] : 0.f;
-          }
+          for (int j = 0; j < 16; j += 2) {
+            float h[2], du[2];
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            hp[j2 * 8 + j] = pack_bf16x2(h[2 * j], h[2 * j + 1]);
-            gp[j2 * 8 + j] = pack_bf16x2(da[2 * j], da[2 * j + 1]);
-            if (GLU) up[j2 * 8 + j] = pack_bf16x2(du[2 * j], du[2 * j + 1]);
+            for (int i = 0; i < 2; ++i) {
+              const float q = __uint_as_float(qv[j + i]);
+              float v = __uint_as_float(av[j + i]), x;
+              if constexpr (GLU) {
+                const float u = __uint_as_float(uv[j + i]);
+                const float sg = __fdividef(1.f, 1.f + __expf(-v));
+                const float si = v * sg;
+                h[i] = si * u;
+                du[i] = q * si;
+                x = q * u * fmaf(si, 1.f - sg, sg);
+              } else {
+                v += bias[j + i];
+                float sl;
+                if (a.act == MOE_ACT_RELU) {
+                  h[i] = fmaxf(v, 0.f);
+                  sl = v > 0.f ? 1.f : 0.f;
+                } else {
+                  gelu_and_slope(v, h[i], sl);
+                }
+                x = q * sl;
+              }
+              dot = fmaf(q, h[i], dot);
+              // rows past the expert's: zeros, whatever the weights hold
+              h[i] = valid ? w * h[i] : 0.f;
+              da[j + i] = valid ? w * x : 0.f;
+              if constexpr (GLU) du[i] = valid ? w * du[i] : 0.f;
+            }
+            hp[j2 * 8 + j / 2] = pack_bf16x2(h[0], h[1]);
+            gp[j2 * 8 + j / 2] = pack_bf16x2(da[j], da[j + 1]);
+            if constexpr (GLU) up[j2 * 8 + j / 2] = pack_bf16x2(du[0], du[1]);
           }
-          if (a.col_part) {
+          if (!GLU && a.col_part) {
             const float v = column_sum16(da, lane);
             if (lane < 16)
               a.col_part[(size_t)(prow >> 5) * a.F + col0 + j2 * 16 + lane] = v;
           }
         }
-        auto out = [&](const CUtensorMap *map, const uint32_t *p) {
-          const EpiStore st{map, stage_out, true, prow};
-          uint4 pk[4];
-#pragma unroll
-          for (int q = 0; q < 4; ++q)
-            pk[q] = make_uint4(p[4 * q], p[4 * q + 1], p[4 * q + 2], p[4 * q + 3]);
-          emit_chunk(st, pk, nullptr, col0);
-        };
-        out(&maps.h, hp);
-        out(&maps.dg, gp);
-        if (GLU) out(&maps.du, up);
       }
       tc_fence_before();
       mbar_arrive_cluster(tempty0 + (uint32_t)(buf * sizeof(uint64_t)));
-      if (a.dot_part && valid && mine && n * kTileN + half * 64 < a.F)
-        a.dot_part[(size_t)(2 * n + half) * a.rows + prow + lane] = dot;
+      if (mine) {
+        out.put32(&maps.h, hp, col0, prow);
+        out.put32(&maps.dg, gp, col0, prow);
+        if constexpr (GLU) out.put32(&maps.du, up, col0, prow);
+        if (a.dot_part && valid) a.dot_part[(size_t)(col0 / 32) * a.rows + prow + lane] = dot;
+      }
     }
     if (lane == 0) bulk_wait_all();  // this warp's output stores are done
     __syncwarp();
@@ -435,7 +461,7 @@ k_act_grad(const __grid_constant__ ActMaps maps, ActArgs a) {
 struct GemmArgs {
   const int32_t *poff, *offsets;
   const int32_t *dx_off;  // first row of each expert in dx
-  int G, err_site;
+  int G;
   // dx: N = d, K = F, nseg pairs (A, B). Weights: njobs products of M x N.
   int N, K, nseg;
   int M[3], Ns[3], njobs;
@@ -479,7 +505,7 @@ k_pair_gemm(const __grid_constant__ GemmMaps maps, GemmArgs a) {
       const int mt = ceil_div(a.M[r.job], kPairM);
       r.m0 = (rem % mt) * kPairM;
       r.n0 = (rem / mt) * 256;
-      r.nkb = (ctl->poff[r.g + 1] - ctl->poff[r.g]) / kBlockK;
+      r.nkb = (a.poff[r.g + 1] - a.poff[r.g]) / kBlockK;
     } else {
       int n, m;
       decode_tile(t, ctl->pre, a.G, n_tiles, r.g, n, m);
@@ -502,7 +528,7 @@ k_pair_gemm(const __grid_constant__ GemmMaps maps, GemmArgs a) {
     bool ok = true;
     for (int t = s.c0; ok && t < total; t += s.cstep) {
       const Tile q = tile_at(t);
-      const int row0 = ctl->poff[q.g];
+      const int row0 = a.poff[q.g];
       const int bcol = q.n0 + s.rank * kRowTile;
       for (int kb = 0; kb < q.nkb; ++kb) {
         if (!(ok = wait_on(s, &ctl->empty[ring.stage], ring.phase ^ 1u, a.err, 31))) break;
@@ -558,14 +584,14 @@ k_pair_gemm(const __grid_constant__ GemmMaps maps, GemmArgs a) {
     }
   } else if (warp >= 4) {
     // ----------------------------------------------------------------- epilogue
-    const int ew = warp & 3, half = (warp - 4) >> 2;
+    const int ew = warp & 3, part = (warp - 4) >> 2;  // lanes 32 ew.., columns 64 part..
     const uint32_t tempty0 = mapa_rank(smem_u32(&ctl->tempty[0]), 0);
-    uint8_t *stage_out = s.smem + kRing + (warp - 4) * kStageOutBytes;
+    uint8_t *stage = s.smem + kRing + (warp - 4) * kStageOut;
     int it = 0;
     for (int t = s.c0; t < total; t += s.cstep, ++it) {
       const Tile q = tile_at(t);
       const int buf = it & 1;
-      const int lrow = q.m0 + s.rank * kRowTile + ew * 32;
+      const int lrow = q.m0 + s.rank * kRowTile + ew * 32, col0 = q.n0 + part * 64;
       int rows, N;      // the output's valid rows from q's first, its width
       size_t orow;      // output row of lane 0
       if (DW) {
@@ -577,47 +603,66 @@ k_pair_gemm(const __grid_constant__ GemmMaps maps, GemmArgs a) {
         N = a.N;
         orow = (size_t)a.dx_off[q.g] + lrow;
       }
+      const bool mine = lrow < rows && col0 < N;  // N is a multiple of 64
       const bool valid = lrow + lane < rows;
-      const EpiStore st{(DW || !a.out_f32) ? &maps.o[q.job] : nullptr, stage_out,
-                        lrow + 32 <= rows, (int)orow};
+      const bool staged = (DW || !a.out_f32) && lrow + 32 <= rows;
       bool ok = wait_on(s, &ctl->tfull[buf], (it >> 1) & 1, a.err, 34);
       __syncwarp();
       if (!__all_sync(0xffffffffu, ok)) break;
       tc_fence_after();
-      const uint32_t ta = s.tmem + ((uint32_t)(ew * 32) << 16) + (uint32_t)(buf * 256);
-#pragma unroll 1
-      for (int c = 4 * half; c < 4 * half + 4; ++c) {
-        const int col0 = q.n0 + c * 32;
-        if (lrow >= rows || col0 >= N) break;
-        float f[32];
-        if (DW && q.nkb == 0) {  // an expert without rows
+      const uint32_t ta = s.tmem + ((uint32_t)(ew * 32) << 16) + (uint32_t)(buf * 256 + part * 64);
+      if (mine && staged) {
+        if (lane == 0) bulk_wait_read<0>();  // the previous tile's store has read the buffer
+        __syncwarp();
+      }
+      if (mine) {
 #pragma unroll
-          for (int j = 0; j < 32; ++j) f[j] = 0.f;
-        } else {
-          uint32_t v[32];
-          tmem_ld32(ta + c * 32, v);
-          tmem_ld_wait();
+        for (int c = 0; c < 2; ++c) {
+          float f[32];
+          if (DW && q.nkb == 0) {  // an expert without rows
 #pragma unroll
-          for (int j = 0; j < 32; ++j) f[j] = __uint_as_float(v[j]);
-        }
-        if (!DW && a.out_f32) {
-          if (valid) {
-            float4 *dst = reinterpret_cast<float4 *>(static_cast<float *>(a.out) +
-                                                     (orow + lane) * (size_t)N + col0);
+            for (int j = 0; j < 32; ++j) f[j] = 0.f;
+          } else {
+            uint32_t v[32];
+            tmem_ld32(ta + c * 32, v);
+            tmem_ld_wait();
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-              dst[j] = make_float4(f[4 * j], f[4 * j + 1], f[4 * j + 2], f[4 * j + 3]);
+            for (int j = 0; j < 32; ++j) f[j] = __uint_as_float(v[j]);
           }
-        } else if (valid) {  // a full group's lanes are all valid
-          uint4 pk[4];
-          pack32(f, pk);
-          __nv_bfloat16 *dst =
-              DW ? nullptr : static_cast<__nv_bfloat16 *>(a.out) + (orow + lane) * (size_t)N;
-          emit_chunk(st, pk, dst, col0);
+          if (!DW && a.out_f32) {
+            if (valid) {
+              float4 *dst = reinterpret_cast<float4 *>(static_cast<float *>(a.out) +
+                                                       (orow + lane) * (size_t)N + col0 + c * 32);
+#pragma unroll
+              for (int j = 0; j < 8; ++j)
+                dst[j] = make_float4(f[4 * j], f[4 * j + 1], f[4 * j + 2], f[4 * j + 3]);
+            }
+          } else if (valid) {
+            // staged: the lane's row of 128 bytes, 16-byte pieces swizzled
+            uint4 *dst = staged ? reinterpret_cast<uint4 *>(stage + lane * 128)
+                                : reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) +
+                                                            (orow + lane) * (size_t)N + col0);
+            const int sw = staged ? lane & 7 : 0;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              float h[8];
+#pragma unroll
+              for (int i = 0; i < 8; ++i) h[i] = f[j * 8 + i];
+              dst[(c * 4 + j) ^ sw] = pack16(h);
+            }
+          }
         }
       }
       tc_fence_before();
       mbar_arrive_cluster(tempty0 + (uint32_t)(buf * sizeof(uint64_t)));
+      if (mine && staged) {
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          tma_store_2d(&maps.o[q.job], stage, col0, (int)orow);
+          bulk_commit();
+        }
+      }
     }
     if (lane == 0) bulk_wait_all();
     __syncwarp();
@@ -713,7 +758,7 @@ cudaError_t launch_dx_tc(const FfnGradArgs &f, cudaStream_t st) {
   if (glu)
     ok = ok && make_map(&m.a[1], f.du, R, F, kRowTile) &&
          make_map(&m.b[1], f.w3, G * F, d, kBlockK);
-  if (!f.dx_f32) ok = ok && make_store_map(&m.o[0], f.dx, (uint64_t)f.dx_rows, d);
+  if (!f.dx_f32) ok = ok && make_map(&m.o[0], f.dx, (uint64_t)f.dx_rows, d, 32);
   if (!ok) return cudaErrorInvalidValue;
   GemmArgs a{};
   a.poff = f.poff;
@@ -742,7 +787,7 @@ cudaError_t launch_dw_tc(const FfnGradArgs &f, cudaStream_t st) {
     const int j = a.njobs++;
     ok = ok && make_map(&m.a[j], p, prows, (uint64_t)M, kBlockK) &&
          make_map(&m.b[j], q, qrows, (uint64_t)N, kBlockK) &&
-         make_store_map(&m.o[j], out, G * (uint64_t)M, (uint64_t)N);
+         make_map(&m.o[j], out, G * (uint64_t)M, (uint64_t)N, 32);
     a.M[j] = M;
     a.Ns[j] = N;
     tiles += (long long)f.G * ceil_div(M, kPairM) * ceil_div(N, 256);

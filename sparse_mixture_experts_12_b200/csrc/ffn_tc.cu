@@ -79,6 +79,41 @@ struct TcArgs {
                            // CTA is never issued, so the waits on it run out
 };
 
+// The output path of one epilogue warp for one tile. With a map, a chunk whose 32
+// rows are all the expert's is staged in the warp's 2 KB shared-memory buffer (64-
+// byte swizzle) and written by one TMA store; other chunks use masked direct stores.
+struct EpiStore {
+  const CUtensorMap *map;  // 32 x 32 bf16 output boxes, or nullptr
+  uint8_t *stage;          // this warp's staging buffer
+  bool rows_full;          // all 32 rows of the warp belong to the expert
+  int row0;                // output row of lane 0
+};
+constexpr int kStageOutBytes = kStoreBox * kStoreBox * 2;  // 2 KB per epilogue warp
+
+// one 32-row x 32-column bf16 chunk (pk = this lane's row) to global memory
+__device__ __forceinline__ void emit_chunk(const EpiStore &st, const uint4 (&pk)[4],
+                                           __nv_bfloat16 *dst_row, int col0) {
+  if (st.map != nullptr && st.rows_full) {
+    const int lane = threadIdx.x & 31;
+    if (lane == 0) bulk_wait_read_all();  // the previous store has read the buffer
+    __syncwarp();
+    uint4 *row = reinterpret_cast<uint4 *>(st.stage + lane * 64);
+    const int sw = (lane >> 1) & 3;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) row[q ^ sw] = pk[q];
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+      tma_store_2d(st.map, st.stage, col0, st.row0);
+      bulk_commit();
+    }
+  } else {
+    uint4 *dst = reinterpret_cast<uint4 *>(dst_row + col0);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) dst[q] = pk[q];
+  }
+}
+
 // Row tiles of an expert with c rows: mt = ceil(c / 128). A split launch gives the
 // CTA-pair kernel the floor(mt / 2) full pair tiles and, when mt is odd (the last
 // 128-row tile holds at most 128 rows), hands that tile to the single-CTA kernel

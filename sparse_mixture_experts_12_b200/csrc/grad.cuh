@@ -91,7 +91,7 @@ struct FfnGradArgs {
   const float *b1, *b2;
   const float *row_w;        // [rows] or nullptr
   float *row_dot;            // [rows] or nullptr
-  float *dot_part;           // [ceil(F / 64), rows] scratch (with row_dot)
+  float *dot_part;           // [ceil(F / 32), rows] scratch (with row_dot)
   void *h, *dg, *du;         // [rows, F] dtype scratch: w h, w dg, w du
   void *dx;                  // [dx_rows, d] or nullptr
   int dx_f32, dx_rows;

@@ -72,6 +72,11 @@ __device__ __forceinline__ void bulk_commit() {
 __device__ __forceinline__ void bulk_wait_read_all() {
   asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
 }
+// ... of all but the latest N
+template <int N>
+__device__ __forceinline__ void bulk_wait_read() {
+  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
+}
 // all committed stores have completed
 __device__ __forceinline__ void bulk_wait_all() {
   asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
@@ -185,42 +190,6 @@ __device__ __forceinline__ void decode_tile(int tile, const int *mpre, int G, in
   const int local = tile - mpre[g] * n_tiles;
   n = local / mt;
   m = local % mt;
-}
-
-// The output path of one epilogue warp for one tile. With a map, a chunk whose 32
-// rows are all the expert's is staged in the warp's 2 KB shared-memory buffer (64-
-// byte swizzle) and written by one TMA store; other chunks use masked direct stores.
-struct EpiStore {
-  const CUtensorMap *map;  // 32 x 32 bf16 output boxes, or nullptr
-  uint8_t *stage;          // this warp's staging buffer
-  bool rows_full;          // all 32 rows of the warp belong to the expert
-  int row0;                // output row of lane 0
-};
-constexpr int kStoreBox = 32;
-constexpr int kStageOutBytes = kStoreBox * kStoreBox * 2;  // 2 KB per epilogue warp
-
-// one 32-row x 32-column bf16 chunk (pk = this lane's row) to global memory
-__device__ __forceinline__ void emit_chunk(const EpiStore &st, const uint4 (&pk)[4],
-                                           __nv_bfloat16 *dst_row, int col0) {
-  if (st.map != nullptr && st.rows_full) {
-    const int lane = threadIdx.x & 31;
-    if (lane == 0) bulk_wait_read_all();  // the previous store has read the buffer
-    __syncwarp();
-    uint4 *row = reinterpret_cast<uint4 *>(st.stage + lane * 64);
-    const int sw = (lane >> 1) & 3;
-#pragma unroll
-    for (int q = 0; q < 4; ++q) row[q ^ sw] = pk[q];
-    fence_proxy_async_smem();
-    __syncwarp();
-    if (lane == 0) {
-      tma_store_2d(st.map, st.stage, col0, st.row0);
-      bulk_commit();
-    }
-  } else {
-    uint4 *dst = reinterpret_cast<uint4 *>(dst_row + col0);
-#pragma unroll
-    for (int q = 0; q < 4; ++q) dst[q] = pk[q];
-  }
 }
 
 // erf by Abramowitz & Stegun, Handbook of Mathematical Functions, formula 7.1.26
@@ -411,6 +380,7 @@ inline bool make_map(CUtensorMap *map, const void *ptr, uint64_t rows, uint64_t 
 
 // 2-D bf16 map for TMA stores of 32 x 32 output tiles (64-byte rows, 64-byte swizzle:
 // the 16-byte chunk index of a row is XORed with (row >> 1) & 3 in shared memory).
+constexpr int kStoreBox = 32;
 inline bool make_store_map(CUtensorMap *map, void *ptr, uint64_t rows, uint64_t cols) {
   auto fn = encode_fn();
   if (fn == nullptr) return false;

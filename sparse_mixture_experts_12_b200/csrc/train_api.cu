@@ -61,7 +61,7 @@ Layout layout_for(const moe_cfg_t &c) {
   sz[G_DX] = tc ? R * d * 4 : 0;
   sz[G_ROW_W] = tc ? R * 4 : 0;
   sz[G_ROW_DOT] = tc ? R * 4 : 0;
-  sz[G_DOT_PART] = tc ? R * (size_t)ceil_div(c.d_ff, 64) * 4 : 0;
+  sz[G_DOT_PART] = tc ? R * (size_t)ceil_div(c.d_ff, 32) * 4 : 0;
   sz[G_DX_ROUTER] = tc ? T * d * 4 : 0;
   sz[G_DX_SHARED] = Fs ? T * d * 4 : 0;
   Layout L;
