@@ -462,10 +462,11 @@ struct GemmArgs {
   const int32_t *poff, *offsets;
   const int32_t *dx_off;  // first row of each expert in dx
   int G;
-  // dx: N = d, K = F, nseg pairs (A, B). Weights: njobs products of M x N.
+  // dx: N = d, K = F, nseg pairs (A, B) added. Weights: njobs products of M x N, each the
+  // sum of nseg pairs.
   int N, K, nseg;
   int M[3], Ns[3], njobs;
-  void *out;              // dx
+  void *out;              // dx; fp32 weights' gradients
   int out_f32;
   int32_t *err;
 };
@@ -505,7 +506,7 @@ k_pair_gemm(const __grid_constant__ GemmMaps maps, GemmArgs a) {
       const int mt = ceil_div(a.M[r.job], kPairM);
       r.m0 = (rem % mt) * kPairM;
       r.n0 = (rem / mt) * 256;
-      r.nkb = (a.poff[r.g + 1] - a.poff[r.g]) / kBlockK;
+      r.nkb = a.nseg * ((a.poff[r.g + 1] - a.poff[r.g]) / kBlockK);
     } else {
       int n, m;
       decode_tile(t, ctl->pre, a.G, n_tiles, r.g, n, m);
@@ -518,8 +519,7 @@ k_pair_gemm(const __grid_constant__ GemmMaps maps, GemmArgs a) {
 
   if (warp == 0 && lane == 0) {
     // ------------------------------------------------------------ TMA producer
-    const int nm = DW ? a.njobs : a.nseg;
-    for (int j = 0; j < nm; ++j) {
+    for (int j = 0; j < max(a.njobs, a.nseg); ++j) {
       prefetch_map(&maps.a[j]);
       prefetch_map(&maps.b[j]);
     }
@@ -530,19 +530,25 @@ k_pair_gemm(const __grid_constant__ GemmMaps maps, GemmArgs a) {
       const Tile q = tile_at(t);
       const int row0 = a.poff[q.g];
       const int bcol = q.n0 + s.rank * kRowTile;
+      const int nk = DW ? (a.poff[q.g + 1] - row0) / kBlockK : nk1;  // slices of a segment
+      int seg = 0, k = 0;
       for (int kb = 0; kb < q.nkb; ++kb) {
         if (!(ok = wait_on(s, &ctl->empty[ring.stage], ring.phase ^ 1u, a.err, 31))) break;
         if (s.rank == 0) mbar_expect_tx(&ctl->full[ring.stage], 2 * kStageBytes);
         uint8_t *st = s.smem + (size_t)ring.stage * kStageBytes;
         const uint32_t bar = full0 + (uint32_t)(ring.stage * sizeof(uint64_t));
         if (DW) {
-          const int r = row0 + kb * kBlockK;
-          load_mn(&maps.a[q.job], bar, st, q.m0 + s.rank * kRowTile, r);
-          load_mn(&maps.b[q.job], bar, st + kOperand, bcol, r);
+          const int r = row0 + k * kBlockK, j = q.job + seg;
+          load_mn(&maps.a[j], bar, st, q.m0 + s.rank * kRowTile, r);
+          load_mn(&maps.b[j], bar, st + kOperand, bcol, r);
         } else {
-          const int seg = kb >= nk1, k0 = (kb - seg * nk1) * kBlockK;
+          const int k0 = k * kBlockK;
           tma_load_2d_pair(&maps.a[seg], bar, st, k0, row0 + q.m0 + s.rank * kRowTile);
           load_mn(&maps.b[seg], bar, st + kOperand, bcol, q.g * a.K + k0);
+        }
+        if (++k == nk) {
+          k = 0;
+          ++seg;
         }
         ring.mark();
         ring.next();
@@ -605,7 +611,7 @@ k_pair_gemm(const __grid_constant__ GemmMaps maps, GemmArgs a) {
       }
       const bool mine = lrow < rows && col0 < N;  // N is a multiple of 64
       const bool valid = lrow + lane < rows;
-      const bool staged = (DW || !a.out_f32) && lrow + 32 <= rows;
+      const bool staged = !a.out_f32 && lrow + 32 <= rows;
       bool ok = wait_on(s, &ctl->tfull[buf], (it >> 1) & 1, a.err, 34);
       __syncwarp();
       if (!__all_sync(0xffffffffu, ok)) break;
@@ -629,7 +635,7 @@ k_pair_gemm(const __grid_constant__ GemmMaps maps, GemmArgs a) {
 #pragma unroll
             for (int j = 0; j < 32; ++j) f[j] = __uint_as_float(v[j]);
           }
-          if (!DW && a.out_f32) {
+          if (a.out_f32) {
             if (valid) {
               float4 *dst = reinterpret_cast<float4 *>(static_cast<float *>(a.out) +
                                                        (orow + lane) * (size_t)N + col0 + c * 32);
@@ -800,8 +806,48 @@ cudaError_t launch_dw_tc(const FfnGradArgs &f, cudaStream_t st) {
   a.poff = f.poff;
   a.offsets = f.offsets;
   a.G = f.G;
+  a.nseg = 1;
   a.err = f.err;
   return launch_pairs(k_pair_gemm<true>, 3, tiles, st, m, a);
+}
+
+cudaError_t launch_route_dx_tc(const RouteTcArgs &r, cudaStream_t st) {
+  GemmMaps m;
+  GemmArgs a{};
+  for (int j = 0; j < kSplit; ++j)
+    if (!make_map(&m.a[j], r.term[j], (uint64_t)r.T, (uint64_t)r.Ep, kRowTile) ||
+        !make_map(&m.b[j], r.w, (uint64_t)r.E, (uint64_t)r.d, kBlockK))
+      return cudaErrorInvalidValue;
+  a.poff = r.all;
+  a.offsets = a.dx_off = r.all_rows;
+  a.G = 1;
+  a.N = r.d;
+  a.K = r.Ep;
+  a.nseg = kSplit;
+  a.out = r.dx;
+  a.out_f32 = 1;
+  a.err = r.err;
+  return launch_pairs(k_pair_gemm<false>, 2,
+                      (long long)ceil_div(r.T, kPairM) * ceil_div(r.d, 256), st, m, a);
+}
+
+cudaError_t launch_route_dw_tc(const RouteTcArgs &r, cudaStream_t st) {
+  GemmMaps m;
+  GemmArgs a{};
+  for (int j = 0; j < kSplitDw; ++j)
+    if (!make_map(&m.a[j], r.term[j], (uint64_t)r.T, (uint64_t)r.Ep, kBlockK) ||
+        !make_map(&m.b[j], r.x, (uint64_t)r.T, (uint64_t)r.d, kBlockK))
+      return cudaErrorInvalidValue;
+  a.poff = a.offsets = r.piece;
+  a.G = r.pieces;
+  a.nseg = kSplitDw;
+  a.njobs = 1;
+  a.M[0] = r.E;
+  a.Ns[0] = r.d;
+  a.out = r.dw_part;
+  a.out_f32 = 1;
+  a.err = r.err;
+  return launch_pairs(k_pair_gemm<true>, 3, (long long)r.pieces * ceil_div(r.d, 256), st, m, a);
 }
 
 }  // namespace moe

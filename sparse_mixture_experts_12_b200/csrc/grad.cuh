@@ -59,7 +59,7 @@ struct RouteBwdArgs {
   const float *row_dot;      // [R] or nullptr: dgate[t,s] = row_dot[inv[t,s]]
   const int32_t *inv;        // [T*k] (with row_dot)
   const float *d_losses;     // [2] or nullptr
-  float *dlogits;            // [T, E]
+  float *dlogits;            // [T, E] (nullptr: bf16 keeps its terms only)
   float *dx;                 // [T, d] fp32 or nullptr
   void *dw;                  // [E, d] dtype or nullptr
   float *db;                 // [E] or nullptr
@@ -68,6 +68,21 @@ struct RouteBwdArgs {
   float alpha;
   int32_t *err;
 };
+// The projection's gradients on the tensor cores (bf16), in ffn_grad_tc.cu: dz as a sum of
+// bf16 terms, rounded one after another. dx takes three (dz to its last bit: the result
+// stays fp32), dW two (2^-16 of dz, far below the rounding of the result to bf16).
+constexpr int kSplit = 3, kSplitDw = 2;
+struct RouteTcArgs {
+  const void *x, *w;           // [T, d], [E, d]
+  __nv_bfloat16 *term[kSplit]; // [T, Ep] each, Ep = E rounded up to 64 (zeros behind E)
+  int32_t *all, *all_rows;     // {0, T rounded up to 64}, {0, T}
+  int32_t *piece;              // [pieces + 1] first tokens (multiples of 64) of the pieces of dW
+  float *dx, *dw_part;         // [T, d]; [pieces, E, d]
+  int T, d, E, Ep, pieces;
+  int32_t *err;
+};
+cudaError_t launch_route_dx_tc(const RouteTcArgs &a, cudaStream_t st);
+cudaError_t launch_route_dw_tc(const RouteTcArgs &a, cudaStream_t st);
 size_t route_bwd_scratch_bytes(int T, int d, int E, int dtype);
 cudaError_t launch_route_bwd(const RouteBwdArgs &a, int dtype, cudaStream_t st);
 

@@ -10,8 +10,9 @@
 //       dz_i += c0 alpha E / T p_i (f_i - sum_j f_j p_j)
 //   z_loss = mean_t lse_t^2:  dz_i += c1 2 / T lse_t p_i
 //   dW = dz^T x, db = sum_t dz (also the logit bias's), dx = dz W.
-// Everything is fp32. The sums over tokens are split into pieces whose partial sums a
-// second kernel adds in a fixed order.
+// dz is fp32; the two products run on CUDA cores (fp32 layers) or, with dz split into bf16
+// terms, on the tensor cores. The sums over tokens are split into pieces whose partial
+// sums a second kernel adds in a fixed order.
 #include "grad.cuh"
 #include "grad_simt.cuh"
 
@@ -19,18 +20,39 @@ namespace moe {
 
 namespace {
 
-constexpr int kMaxBlocks = 592;  // of k_dlogits: four per SM
-constexpr int kEpl = kMaxExperts / 32;
+constexpr int kMaxBlocks = 1184;  // of k_dlogits: eight per SM
 
 __device__ __forceinline__ float neg_inf() { return __int_as_float(0xff800000); }
 
-// A warp per token (blocks stride over the tokens): lane l holds experts l + 32 j.
-__global__ void __launch_bounds__(256) k_dlogits(RouteBwdArgs a, float *db_part) {
-  __shared__ float red[8][kMaxExperts];
+// dz as bf16 terms: each the rounding of what the ones before it leave
+__device__ __forceinline__ void split_terms(float v, __nv_bfloat16 (&t)[kSplit]) {
+#pragma unroll
+  for (int i = 0; i < kSplit; ++i) {
+    t[i] = __float2bfloat16_rn(v);
+    const float r = __bfloat162float(t[i]);
+    v = isinf(r) ? 0.f : v - r;  // an infinite value has no remainder
+  }
+}
+
+// A warp per token (blocks stride over the tokens): lane l holds experts l + 32 j, j <
+// kEpl. With TC dz also goes out as bf16 terms, and the first block writes the tables of
+// the tensor-core products.
+template <int kEpl, bool TC>
+__global__ void __launch_bounds__(256) k_dlogits(RouteBwdArgs a, float *db_part, RouteTcArgs tc) {
+  __shared__ float red[8][32 * kEpl];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_wait();
   pdl_trigger();
   const int E = a.E, k = a.k;
+  if (TC && blockIdx.x == 0) {
+    const int slices = ceil_div(a.T, 64), per = ceil_div(slices, tc.pieces);
+    for (int i = threadIdx.x; i <= tc.pieces; i += 256) tc.piece[i] = 64 * min(slices, i * per);
+    if (threadIdx.x == 0) {
+      tc.all[0] = tc.all_rows[0] = 0;
+      tc.all[1] = 64 * slices;
+      tc.all_rows[1] = a.T;
+    }
+  }
   const bool losses = a.d_losses != nullptr;
   const bool need_p = losses || a.gate_mode == MOE_GATE_SOFTMAX_TOPK_RAW;
   const float c0 = losses ? a.d_losses[0] * a.alpha * (float)E / (float)a.T : 0.f;
@@ -127,8 +149,15 @@ __global__ void __launch_bounds__(256) k_dlogits(RouteBwdArgs a, float *db_part)
 #pragma unroll
     for (int j = 0; j < kEpl; ++j) {
       const int e = lane + 32 * j;
-      if (e < E) a.dlogits[(size_t)t * E + e] = dz[j];
+      if (e < E && a.dlogits) a.dlogits[(size_t)t * E + e] = dz[j];
       db[j] += dz[j];
+      if (TC && e < tc.Ep) {
+        __nv_bfloat16 part[kSplit];
+        split_terms(e < E ? dz[j] : 0.f, part);
+#pragma unroll
+        for (int i = 0; i < kSplit; ++i)
+          if (tc.term[i]) tc.term[i][(size_t)t * tc.Ep + e] = part[i];
+      }
     }
   }
   if (db_part == nullptr) return;
@@ -143,27 +172,34 @@ __global__ void __launch_bounds__(256) k_dlogits(RouteBwdArgs a, float *db_part)
   }
 }
 
-// out[i] = sum over the pieces of part [pieces, n], in order
+// dw[i] = sum over the pieces of part [pieces, n], and (the last E blocks) db[e] = the
+// sum of the blocks' partials, each in a fixed order
 template <typename T>
-__global__ void __launch_bounds__(256) k_sum_pieces(const float *part, int pieces, size_t n,
-                                                    T *out) {
-  pdl_wait();
-  pdl_trigger();
-  const size_t i = (size_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= n) return;
-  float v = 0.f;
-  for (int s = 0; s < pieces; ++s) v += part[(size_t)s * n + i];
-  out[i] = Elem<T>::from_f(v);
-}
-
-// db [E] from the blocks' sums: a block per expert
-__global__ void __launch_bounds__(128) k_db(const float *part, int blocks, int E, float *db) {
+__global__ void __launch_bounds__(128) k_route_sums(const float *part, int pieces, size_t n, T *dw,
+                                                    int dw_blocks, const float *db_part, int blocks,
+                                                    int E, float *db) {
   __shared__ float red[4];
   pdl_wait();
   pdl_trigger();
-  const int e = blockIdx.x;
+  if ((int)blockIdx.x < dw_blocks) {  // n is a multiple of 4
+    const size_t i = ((size_t)blockIdx.x * 128 + threadIdx.x) * 4;
+    if (i >= n) return;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+    for (int s = 0; s < pieces; ++s) {
+      const float4 p = __ldg(reinterpret_cast<const float4 *>(part + (size_t)s * n + i));
+      v.x += p.x; v.y += p.y; v.z += p.z; v.w += p.w;
+    }
+    dw[i] = Elem<T>::from_f(v.x);
+    dw[i + 1] = Elem<T>::from_f(v.y);
+    dw[i + 2] = Elem<T>::from_f(v.z);
+    dw[i + 3] = Elem<T>::from_f(v.w);
+    return;
+  }
+  const int e = blockIdx.x - dw_blocks;
   float v = 0.f;
-  for (int i = threadIdx.x; i < blocks; i += 128) v += part[(size_t)i * E + e];
+#pragma unroll 4
+  for (int i = threadIdx.x; i < blocks; i += 128) v += db_part[(size_t)i * E + e];
   v = warp_sum(v);
   if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
   __syncthreads();
@@ -184,21 +220,43 @@ int dw_pieces(int T, int d, int E) {
   return s < most ? s : most;
 }
 
+// ... with the CTA-pair tiles: one per pair, K long enough to pay for the reduction
+int dw_pieces_tc(int T, int d) {
+  const int s = 74 / ceil_div(d, 256), most = ceil_div(T, 256);
+  return s < 1 ? 1 : (s < most ? s : most);
+}
+
+int e_padded(int E) { return (E + 63) / 64 * 64; }
+
+template <bool TC>
+cudaError_t dlogits(const RouteBwdArgs &a, float *db_part, const RouteTcArgs &tc, cudaStream_t st) {
+  const dim3 g(dlogits_blocks(a.T)), b(256);
+  const int cols = TC ? tc.Ep : a.E;
+  if (cols <= 32) return launch_pdl(k_dlogits<1, TC>, g, b, 0, st, a, db_part, tc);
+  if (cols <= 64) return launch_pdl(k_dlogits<2, TC>, g, b, 0, st, a, db_part, tc);
+  if (cols <= 128) return launch_pdl(k_dlogits<4, TC>, g, b, 0, st, a, db_part, tc);
+  return launch_pdl(k_dlogits<8, TC>, g, b, 0, st, a, db_part, tc);
+}
+
 template <typename T>
-cudaError_t route_bwd(const RouteBwdArgs &a, cudaStream_t st) {
+cudaError_t sums(const RouteBwdArgs &a, const float *dw_part, int pieces, const float *db_part,
+                 cudaStream_t st) {
+  const size_t n = a.dw ? (size_t)a.E * a.d : 0;
+  const int dw_blocks = (int)((n / 4 + 127) / 128), db_blocks = a.db ? a.E : 0;
+  if (dw_blocks + db_blocks == 0) return cudaSuccess;
+  return launch_pdl(k_route_sums<T>, dim3(dw_blocks + db_blocks), dim3(128), 0, st, dw_part, pieces,
+                    n, static_cast<T *>(a.dw), dw_blocks, db_part, dlogits_blocks(a.T), a.E, a.db);
+}
+
+// fp32: CUDA cores
+cudaError_t route_bwd_simt(const RouteBwdArgs &a, cudaStream_t st) {
   float *db_part = static_cast<float *>(a.part);
-  const int blocks = dlogits_blocks(a.T);
   const dim3 b(256);
-  cudaError_t e = launch_pdl(k_dlogits, dim3(blocks), b, 0, st, a,
-                             a.db ? db_part : static_cast<float *>(nullptr));
+  cudaError_t e = dlogits<false>(a, a.db ? db_part : nullptr, RouteTcArgs{}, st);
   if (e != cudaSuccess) return e;
-  if (a.db) {
-    e = launch_pdl(k_db, dim3(a.E), dim3(128), 0, st, (const float *)db_part, blocks, a.E, a.db);
-    if (e != cudaSuccess) return e;
-  }
-  const T *x = static_cast<const T *>(a.x), *w = static_cast<const T *>(a.w);
+  const float *x = static_cast<const float *>(a.x), *w = static_cast<const float *>(a.w);
   if (a.dx) {
-    simt::Gemm<float, T, float> m{};
+    simt::Gemm<float, float, float> m{};
     m.a[0] = a.dlogits;
     m.b[0] = w;
     m.c[0] = a.dx;
@@ -208,15 +266,14 @@ cudaError_t route_bwd(const RouteBwdArgs &a, cudaStream_t st) {
     m.nseg = 1;
     m.K = a.E;
     m.G = 1;
-    e = launch_pdl(simt::k_gemm<float, T, float, false>,
+    e = launch_pdl(simt::k_gemm<float, float, float, false>,
                    dim3(ceil_div(a.d, simt::BN), ceil_div(a.T, simt::BM)), b, 0, st, m);
     if (e != cudaSuccess) return e;
   }
+  const int pieces = dw_pieces(a.T, a.d, a.E);
+  float *dw_part = db_part + (size_t)kMaxBlocks * a.E;
   if (a.dw) {
-    const int pieces = dw_pieces(a.T, a.d, a.E);
-    const size_t n = (size_t)a.E * a.d;
-    float *dw_part = db_part + (size_t)kMaxBlocks * a.E;
-    simt::Gemm<float, T, float> m{};
+    simt::Gemm<float, float, float> m{};
     m.a[0] = a.dlogits;
     m.b[0] = x;
     m.c[0] = dw_part;
@@ -226,25 +283,75 @@ cudaError_t route_bwd(const RouteBwdArgs &a, cudaStream_t st) {
     m.K = a.T;
     m.chunk = ceil_div(a.T, pieces);
     m.G = pieces;
-    e = launch_pdl(simt::k_gemm<float, T, float, true>,
+    e = launch_pdl(simt::k_gemm<float, float, float, true>,
                    dim3(ceil_div(a.d, simt::BN), ceil_div(a.E, simt::BM), pieces), b, 0, st, m);
     if (e != cudaSuccess) return e;
-    e = launch_pdl(k_sum_pieces<T>, dim3((unsigned)((n + 255) / 256)), b, 0, st,
-                   (const float *)dw_part, pieces, n, static_cast<T *>(a.dw));
   }
-  return e;
+  return sums<float>(a, dw_part, pieces, db_part, st);
+}
+
+// bf16 scratch: tables | db partials | dW partials | terms
+struct TcScratch {
+  size_t tables, db, dw, term, term_bytes, total;
+};
+TcScratch tc_scratch(int T, int d, int E) {
+  auto up = [](size_t v) { return (v + 255) & ~(size_t)255; };
+  TcScratch s;
+  s.tables = 0;
+  s.db = up((kMaxExperts + 1 + 4) * 4);
+  s.dw = s.db + up((size_t)kMaxBlocks * E * 4);
+  s.term = s.dw + up((size_t)dw_pieces_tc(T, d) * E * d * 4);
+  s.term_bytes = up((size_t)T * e_padded(E) * 2);
+  s.total = s.term + kSplit * s.term_bytes;
+  return s;
+}
+
+cudaError_t route_bwd_tc(const RouteBwdArgs &a, cudaStream_t st) {
+  const TcScratch s = tc_scratch(a.T, a.d, a.E);
+  char *base = static_cast<char *>(a.part);
+  float *db_part = reinterpret_cast<float *>(base + s.db);
+  RouteTcArgs tc{};
+  tc.x = a.x;
+  tc.w = a.w;
+  const int terms = a.dx ? kSplit : (a.dw ? kSplitDw : 0);
+  for (int i = 0; i < terms; ++i)
+    tc.term[i] = reinterpret_cast<__nv_bfloat16 *>(base + s.term + i * s.term_bytes);
+  tc.all = reinterpret_cast<int32_t *>(base);
+  tc.all_rows = tc.all + 2;
+  tc.piece = tc.all + 4;
+  tc.dx = a.dx;
+  tc.dw_part = reinterpret_cast<float *>(base + s.dw);
+  tc.T = a.T;
+  tc.d = a.d;
+  tc.E = a.E;
+  tc.Ep = e_padded(a.E);
+  tc.pieces = dw_pieces_tc(a.T, a.d);
+  tc.err = a.err;
+  cudaError_t e = terms ? dlogits<true>(a, a.db ? db_part : nullptr, tc, st)
+                        : dlogits<false>(a, a.db ? db_part : nullptr, tc, st);
+  if (e != cudaSuccess) return e;
+  if (a.dx) {
+    e = launch_route_dx_tc(tc, st);
+    if (e != cudaSuccess) return e;
+  }
+  if (a.dw) {
+    e = launch_route_dw_tc(tc, st);
+    if (e != cudaSuccess) return e;
+  }
+  return sums<__nv_bfloat16>(a, tc.dw_part, tc.pieces, db_part, st);
 }
 
 }  // namespace
 
 size_t route_bwd_scratch_bytes(int T, int d, int E, int dtype) {
-  (void)dtype;
-  return sizeof(float) * ((size_t)kMaxBlocks * E + (size_t)dw_pieces(T > 0 ? T : 1, d, E) * E * d);
+  if (T < 1) T = 1;
+  if (dtype != MOE_DTYPE_F32) return tc_scratch(T, d, E).total;
+  return sizeof(float) * ((size_t)kMaxBlocks * E + (size_t)dw_pieces(T, d, E) * E * d);
 }
 
 cudaError_t launch_route_bwd(const RouteBwdArgs &a, int dtype, cudaStream_t st) {
   if (a.T == 0) return cudaSuccess;
-  return dtype == MOE_DTYPE_F32 ? route_bwd<float>(a, st) : route_bwd<__nv_bfloat16>(a, st);
+  return dtype == MOE_DTYPE_F32 ? route_bwd_simt(a, st) : route_bwd_tc(a, st);
 }
 
 }  // namespace moe
