@@ -468,6 +468,8 @@ struct GemmArgs {
   int M[3], Ns[3], njobs;
   void *out;              // dx; fp32 weights' gradients
   int out_f32;
+  int clipped;            // dx: no other rows lie in an expert's last group of 32 (padding, or
+                          // the output ends and its map clips the stores)
   int32_t *err;
 };
 struct GemmMaps {
@@ -611,7 +613,8 @@ k_pair_gemm(const __grid_constant__ GemmMaps maps, GemmArgs a) {
       }
       const bool mine = lrow < rows && col0 < N;  // N is a multiple of 64
       const bool valid = lrow + lane < rows;
-      const bool staged = !a.out_f32 && lrow + 32 <= rows;
+      // full groups of 32 rows leave through TMA stores, others row by row
+      const bool staged = lrow + 32 <= rows || a.clipped;
       bool ok = wait_on(s, &ctl->tfull[buf], (it >> 1) & 1, a.err, 34);
       __syncwarp();
       if (!__all_sync(0xffffffffu, ok)) break;
@@ -635,7 +638,22 @@ k_pair_gemm(const __grid_constant__ GemmMaps maps, GemmArgs a) {
 #pragma unroll
             for (int j = 0; j < 32; ++j) f[j] = __uint_as_float(v[j]);
           }
-          if (a.out_f32) {
+          if (a.out_f32 && staged) {  // 32 rows of 128 bytes, 16-byte pieces swizzled
+            if (c > 0) {
+              if (lane == 0) bulk_wait_read<0>();
+              __syncwarp();
+            }
+            float4 *dst = reinterpret_cast<float4 *>(stage + lane * 128);
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              dst[j ^ (lane & 7)] = make_float4(f[4 * j], f[4 * j + 1], f[4 * j + 2], f[4 * j + 3]);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              tma_store_2d(&maps.o[q.job], stage, col0 + c * 32, (int)orow);
+              bulk_commit();
+            }
+          } else if (a.out_f32) {
             if (valid) {
               float4 *dst = reinterpret_cast<float4 *>(static_cast<float *>(a.out) +
                                                        (orow + lane) * (size_t)N + col0 + c * 32);
@@ -661,7 +679,7 @@ k_pair_gemm(const __grid_constant__ GemmMaps maps, GemmArgs a) {
       }
       tc_fence_before();
       mbar_arrive_cluster(tempty0 + (uint32_t)(buf * sizeof(uint64_t)));
-      if (mine && staged) {
+      if (mine && staged && !a.out_f32) {
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
@@ -764,7 +782,8 @@ cudaError_t launch_dx_tc(const FfnGradArgs &f, cudaStream_t st) {
   if (glu)
     ok = ok && make_map(&m.a[1], f.du, R, F, kRowTile) &&
          make_map(&m.b[1], f.w3, G * F, d, kBlockK);
-  if (!f.dx_f32) ok = ok && make_map(&m.o[0], f.dx, (uint64_t)f.dx_rows, d, 32);
+  ok = ok && (f.dx_f32 ? make_f32_map(&m.o[0], f.dx, (uint64_t)f.dx_rows, d)
+                       : make_map(&m.o[0], f.dx, (uint64_t)f.dx_rows, d, 32));
   if (!ok) return cudaErrorInvalidValue;
   GemmArgs a{};
   a.poff = f.poff;
@@ -776,6 +795,7 @@ cudaError_t launch_dx_tc(const FfnGradArgs &f, cudaStream_t st) {
   a.nseg = glu ? 2 : 1;
   a.out = f.dx;
   a.out_f32 = f.dx_f32;
+  a.clipped = f.dx_off == f.poff;  // the rows behind an expert's are its own padding
   a.err = f.err;
   return launch_pairs(k_pair_gemm<false>, 2, (long long)f.pair_tiles_ub * ceil_div(f.d, 256), st,
                       m, a);
@@ -818,6 +838,8 @@ cudaError_t launch_route_dx_tc(const RouteTcArgs &r, cudaStream_t st) {
     if (!make_map(&m.a[j], r.term[j], (uint64_t)r.T, (uint64_t)r.Ep, kRowTile) ||
         !make_map(&m.b[j], r.w, (uint64_t)r.E, (uint64_t)r.d, kBlockK))
       return cudaErrorInvalidValue;
+  if (!make_f32_map(&m.o[0], r.dx, (uint64_t)r.T, (uint64_t)r.d)) return cudaErrorInvalidValue;
+  a.clipped = 1;
   a.poff = r.all;
   a.offsets = a.dx_off = r.all_rows;
   a.G = 1;
@@ -838,6 +860,8 @@ cudaError_t launch_route_dw_tc(const RouteTcArgs &r, cudaStream_t st) {
     if (!make_map(&m.a[j], r.term[j], (uint64_t)r.T, (uint64_t)r.Ep, kBlockK) ||
         !make_map(&m.b[j], r.x, (uint64_t)r.T, (uint64_t)r.d, kBlockK))
       return cudaErrorInvalidValue;
+  if (!make_f32_map(&m.o[0], r.dw_part, (uint64_t)r.pieces * r.E, (uint64_t)r.d))
+    return cudaErrorInvalidValue;
   a.poff = a.offsets = r.piece;
   a.G = r.pieces;
   a.nseg = kSplitDw;

@@ -59,7 +59,7 @@ struct RouteBwdArgs {
   const float *row_dot;      // [R] or nullptr: dgate[t,s] = row_dot[inv[t,s]]
   const int32_t *inv;        // [T*k] (with row_dot)
   const float *d_losses;     // [2] or nullptr
-  float *dlogits;            // [T, E] (nullptr: bf16 keeps its terms only)
+  float *dlogits;            // [T, E]
   float *dx;                 // [T, d] fp32 or nullptr
   void *dw;                  // [E, d] dtype or nullptr
   float *db;                 // [E] or nullptr

@@ -172,6 +172,115 @@ __global__ void __launch_bounds__(256) k_dlogits(RouteBwdArgs a, float *db_part,
   }
 }
 
+// Few experts (EP >= E, at most kFewExperts): both products on CUDA cores in one pass over
+// x. A thread owns VC columns and keeps their EP rows of W and of dW in registers; the
+// block walks over its piece of the tokens with dz broadcast from shared memory. 4 E flops
+// per element of x: up to E = 16 the reads of x and the writes of dx bound it.
+constexpr int kFewExperts = 32;
+constexpr int kProjThreads = 128, kProjTokens = 32;
+
+template <typename T, int VC>
+__device__ __forceinline__ void load_cols(const T *p, float (&f)[VC]) {
+  if constexpr (sizeof(T) == 4) {
+    if constexpr (VC == 4) {
+      const float4 v = __ldg(reinterpret_cast<const float4 *>(p));
+      f[0] = v.x; f[1] = v.y; f[2] = v.z; f[3] = v.w;
+    } else {
+      const float2 v = __ldg(reinterpret_cast<const float2 *>(p));
+      f[0] = v.x; f[1] = v.y;
+    }
+  } else {
+    uint32_t u[VC / 2];
+    if constexpr (VC == 4) {
+      const uint2 v = __ldg(reinterpret_cast<const uint2 *>(p));
+      u[0] = v.x; u[1] = v.y;
+    } else {
+      u[0] = __ldg(reinterpret_cast<const uint32_t *>(p));
+    }
+#pragma unroll
+    for (int i = 0; i < VC / 2; ++i) {
+      f[2 * i] = __uint_as_float(u[i] << 16);
+      f[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+    }
+  }
+}
+
+template <typename T, int EP, int VC>
+__global__ void __launch_bounds__(kProjThreads) k_route_proj(const T *x, const T *w,
+                                                             const float *dz, float *dx,
+                                                             float *dw_part, int n_tok, int d,
+                                                             int E, int per) {
+  __shared__ __align__(16) float zs[kProjTokens][EP];
+  const int tid = threadIdx.x;
+  const int col = (blockIdx.x * kProjThreads + tid) * VC;
+  const bool live = col < d;
+  pdl_wait();
+  pdl_trigger();
+  float wr[EP][VC], acc[EP][VC];
+#pragma unroll
+  for (int e = 0; e < EP; ++e) {
+#pragma unroll
+    for (int c = 0; c < VC; ++c) wr[e][c] = acc[e][c] = 0.f;
+    if (dx && live && e < E) load_cols<T, VC>(w + (size_t)e * d + col, wr[e]);
+  }
+  const int t0 = blockIdx.y * per, t1 = min(n_tok, t0 + per);
+  for (int tb = t0; tb < t1; tb += kProjTokens) {
+    const int n = min(kProjTokens, t1 - tb);
+    __syncthreads();
+    for (int i = tid; i < kProjTokens * EP; i += kProjThreads) {
+      const int u = i / EP, e = i % EP;
+      zs[u][e] = (u < n && e < E) ? dz[(size_t)(tb + u) * E + e] : 0.f;
+    }
+    __syncthreads();
+    if (!live) continue;
+    constexpr int NB = 4;  // tokens requested before any is used
+    for (int u0 = 0; u0 < n; u0 += NB) {
+      float xv[NB][VC];
+#pragma unroll
+      for (int i = 0; i < NB; ++i)
+        if (dw_part && u0 + i < n) load_cols<T, VC>(x + (size_t)(tb + u0 + i) * d + col, xv[i]);
+#pragma unroll
+      for (int i = 0; i < NB; ++i) {
+        if (u0 + i >= n) break;
+        float o[VC], z[EP];
+#pragma unroll
+        for (int e = 0; e < EP; e += 4) {
+          const float4 q = *reinterpret_cast<const float4 *>(&zs[u0 + i][e]);
+          z[e] = q.x; z[e + 1] = q.y; z[e + 2] = q.z; z[e + 3] = q.w;
+        }
+        if (dx) {
+#pragma unroll
+          for (int c = 0; c < VC; ++c) {
+            o[c] = 0.f;
+#pragma unroll
+            for (int e = 0; e < EP; ++e) o[c] = fmaf(z[e], wr[e][c], o[c]);
+          }
+          float *out = dx + (size_t)(tb + u0 + i) * d + col;
+          if constexpr (VC == 4)
+            *reinterpret_cast<float4 *>(out) = make_float4(o[0], o[1], o[2], o[3]);
+          else
+            *reinterpret_cast<float2 *>(out) = make_float2(o[0], o[1]);
+        }
+        if (dw_part) {
+#pragma unroll
+          for (int e = 0; e < EP; ++e)
+#pragma unroll
+            for (int c = 0; c < VC; ++c) acc[e][c] = fmaf(z[e], xv[i][c], acc[e][c]);
+        }
+      }
+    }
+  }
+  if (dw_part && live) {
+#pragma unroll
+    for (int e = 0; e < EP; ++e)
+      if (e < E) {
+        float *out = dw_part + ((size_t)blockIdx.y * E + e) * d + col;
+#pragma unroll
+        for (int c = 0; c < VC; ++c) out[c] = acc[e][c];
+      }
+  }
+}
+
 // dw[i] = sum over the pieces of part [pieces, n], and (the last E blocks) db[e] = the
 // sum of the blocks' partials, each in a fixed order
 template <typename T>
@@ -226,6 +335,14 @@ int dw_pieces_tc(int T, int d) {
   return s < 1 ? 1 : (s < most ? s : most);
 }
 
+// ... of k_route_proj: three blocks per SM (as many as its registers let it hold), at
+// least sixteen tokens each
+int proj_cols(int E) { return E <= 16 ? 4 : 2; }
+int proj_pieces(int T, int d, int E) {
+  const int s = 148 * 3 / ceil_div(d, kProjThreads * proj_cols(E)), most = ceil_div(T, 16);
+  return s < 1 ? 1 : (s < most ? s : most);
+}
+
 int e_padded(int E) { return (E + 63) / 64 * 64; }
 
 template <bool TC>
@@ -248,7 +365,29 @@ cudaError_t sums(const RouteBwdArgs &a, const float *dw_part, int pieces, const 
                     n, static_cast<T *>(a.dw), dw_blocks, db_part, dlogits_blocks(a.T), a.E, a.db);
 }
 
-// fp32: CUDA cores
+template <typename T>
+cudaError_t route_bwd_few(const RouteBwdArgs &a, cudaStream_t st) {
+  float *db_part = static_cast<float *>(a.part);
+  cudaError_t e = dlogits<false>(a, a.db ? db_part : nullptr, RouteTcArgs{}, st);
+  if (e != cudaSuccess) return e;
+  const int pieces = proj_pieces(a.T, a.d, a.E);
+  float *dw_part = db_part + (size_t)kMaxBlocks * a.E;
+  if (a.dx || a.dw) {
+    const dim3 g(ceil_div(a.d, kProjThreads * proj_cols(a.E)), pieces), b(kProjThreads);
+    const T *x = static_cast<const T *>(a.x), *w = static_cast<const T *>(a.w);
+    auto run = [&](auto kernel) {
+      return launch_pdl(kernel, g, b, 0, st, x, w, (const float *)a.dlogits, a.dx,
+                        a.dw ? dw_part : static_cast<float *>(nullptr), a.T, a.d, a.E,
+                        ceil_div(a.T, pieces));
+    };
+    e = a.E <= 8 ? run(k_route_proj<T, 8, 4>)
+                 : (a.E <= 16 ? run(k_route_proj<T, 16, 4>) : run(k_route_proj<T, 32, 2>));
+    if (e != cudaSuccess) return e;
+  }
+  return sums<T>(a, dw_part, pieces, db_part, st);
+}
+
+// fp32, more experts: tiles on CUDA cores
 cudaError_t route_bwd_simt(const RouteBwdArgs &a, cudaStream_t st) {
   float *db_part = static_cast<float *>(a.part);
   const dim3 b(256);
@@ -345,13 +484,16 @@ cudaError_t route_bwd_tc(const RouteBwdArgs &a, cudaStream_t st) {
 
 size_t route_bwd_scratch_bytes(int T, int d, int E, int dtype) {
   if (T < 1) T = 1;
-  if (dtype != MOE_DTYPE_F32) return tc_scratch(T, d, E).total;
-  return sizeof(float) * ((size_t)kMaxBlocks * E + (size_t)dw_pieces(T, d, E) * E * d);
+  if (E > kFewExperts && dtype != MOE_DTYPE_F32) return tc_scratch(T, d, E).total;
+  const int pieces = E <= kFewExperts ? proj_pieces(T, d, E) : dw_pieces(T, d, E);
+  return sizeof(float) * ((size_t)kMaxBlocks * E + (size_t)pieces * E * d);
 }
 
 cudaError_t launch_route_bwd(const RouteBwdArgs &a, int dtype, cudaStream_t st) {
   if (a.T == 0) return cudaSuccess;
-  return dtype == MOE_DTYPE_F32 ? route_bwd_simt(a, st) : route_bwd_tc(a, st);
+  const bool f32 = dtype == MOE_DTYPE_F32;
+  if (a.E <= kFewExperts) return f32 ? route_bwd_few<float>(a, st) : route_bwd_few<__nv_bfloat16>(a, st);
+  return f32 ? route_bwd_simt(a, st) : route_bwd_tc(a, st);
 }
 
 }  // namespace moe

@@ -394,6 +394,20 @@ inline bool make_store_map(CUtensorMap *map, void *ptr, uint64_t rows, uint64_t 
   return r == CUDA_SUCCESS;
 }
 
+// 2-D fp32 map for TMA stores of 32 x 32 tiles (128-byte rows, 128-byte swizzle).
+inline bool make_f32_map(CUtensorMap *map, void *ptr, uint64_t rows, uint64_t cols) {
+  auto fn = encode_fn();
+  if (fn == nullptr) return false;
+  cuuint64_t dims[2] = {cols, rows};
+  cuuint64_t strides[1] = {cols * 4};
+  cuuint32_t box[2] = {(cuuint32_t)kStoreBox, (cuuint32_t)kStoreBox};
+  cuuint32_t estr[2] = {1, 1};
+  CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, ptr, dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
 inline int sm_count() {
   static int counts[64] = {};
   int dev = 0;
