@@ -34,140 +34,217 @@ __device__ __forceinline__ void split_terms(float v, __nv_bfloat16 (&t)[kSplit])
   }
 }
 
-// A warp per token (blocks stride over the tokens): lane l holds experts l + 32 j, j <
-// kEpl. With TC dz also goes out as bf16 terms, and the first block writes the tables of
-// the tensor-core products.
-template <int kEpl, bool TC>
-__global__ void __launch_bounds__(256) k_dlogits(RouteBwdArgs a, float *db_part, RouteTcArgs tc) {
-  __shared__ float red[8][32 * kEpl];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+// LPT lanes per token, eight consecutive experts each: a warp works on 32 / LPT tokens at
+// once, reductions over the experts take log2(LPT) exchanges, and rows move in 16-byte
+// pieces. Every lane goes through the token's slots by itself. With TC dz also goes out as
+// bf16 terms, and the first block writes the tables of the tensor-core products.
+constexpr int kDzThreads = 128, kEpl = 8;
+
+template <int LPT>
+__device__ __forceinline__ float group_max(float v) {
+#pragma unroll
+  for (int o = LPT / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
+}
+template <int LPT>
+__device__ __forceinline__ float group_sum(float v) {
+#pragma unroll
+  for (int o = LPT / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+template <int LPT, bool TC>
+__global__ void __launch_bounds__(kDzThreads) k_dlogits(RouteBwdArgs a, float *db_part,
+                                                        RouteTcArgs tc) {
+  constexpr int kTokens = kDzThreads / LPT, kWarps = kDzThreads / 32;
+  __shared__ float red[kWarps][LPT * kEpl];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int sub = threadIdx.x % LPT, e0 = sub * kEpl;
   pdl_wait();
   pdl_trigger();
   const int E = a.E, k = a.k;
   if (TC && blockIdx.x == 0) {
     const int slices = ceil_div(a.T, 64), per = ceil_div(slices, tc.pieces);
-    for (int i = threadIdx.x; i <= tc.pieces; i += 256) tc.piece[i] = 64 * min(slices, i * per);
+    for (int i = threadIdx.x; i <= tc.pieces; i += kDzThreads)
+      tc.piece[i] = 64 * min(slices, i * per);
     if (threadIdx.x == 0) {
       tc.all[0] = tc.all_rows[0] = 0;
       tc.all[1] = 64 * slices;
       tc.all_rows[1] = a.T;
     }
   }
-  const bool losses = a.d_losses != nullptr;
-  const bool need_p = losses || a.gate_mode == MOE_GATE_SOFTMAX_TOPK_RAW;
+  const bool losses = a.d_losses != nullptr, raw = a.gate_mode == MOE_GATE_SOFTMAX_TOPK_RAW;
+  const bool need_p = losses || raw, vec = (E & 3) == 0;
   const float c0 = losses ? a.d_losses[0] * a.alpha * (float)E / (float)a.T : 0.f;
   const float c1 = losses ? a.d_losses[1] * 2.f / (float)a.T : 0.f;
   float f[kEpl], db[kEpl];
 #pragma unroll
   for (int j = 0; j < kEpl; ++j) {
-    const int e = lane + 32 * j;
     db[j] = 0.f;
-    f[j] = (losses && e < E) ? (float)a.counts[e] / ((float)a.T * (float)k) : 0.f;
+    f[j] = (losses && e0 + j < E) ? (float)a.counts[e0 + j] / ((float)a.T * (float)k) : 0.f;
   }
-  for (int t = blockIdx.x * 8 + warp; t < a.T; t += gridDim.x * 8) {
-    const float *zt = a.logits + (size_t)t * E;
-    // the slots: lane s < k
-    int idx = -1;
-    float dg = 0.f, zs = neg_inf();
-    if (lane < k) {
-      const size_t q = (size_t)t * k + lane;
-      idx = a.topk_idx[q];
-      if (idx < 0 || idx >= E) {
-        report_error(a.err, MOE_DEVERR_EXPERT_INDEX, (int32_t)q);
-        idx = -1;
-      }
-      if (idx >= 0) {
-        zs = zt[idx];
-        if (a.row_dot) {
-          const int r = a.inv[q];
-          dg = (r >= 0 && r < a.R) ? a.row_dot[r] : 0.f;
-        } else if (a.dgate) {
-          dg = a.dgate[q];
-        }
-      }
-    }
+  for (int base = blockIdx.x * kTokens; base < a.T; base += gridDim.x * kTokens) {
+    const int t = base + threadIdx.x / LPT;
+    const bool live = t < a.T;
+    const float *zt = a.logits + (size_t)(live ? t : 0) * E;
     float p[kEpl], dz[kEpl];
 #pragma unroll
-    for (int j = 0; j < kEpl; ++j) p[j] = dz[j] = 0.f;
-    float ds = 0.f;  // this lane's slot: what its expert's logit gets
+    for (int j = 0; j < kEpl; ++j) {
+      p[j] = neg_inf();
+      dz[j] = 0.f;
+    }
+    if (need_p && live) {
+#pragma unroll
+      for (int j = 0; j < kEpl; j += 4) {
+        if (vec && e0 + j < E) {
+          const float4 q = __ldg(reinterpret_cast<const float4 *>(zt + e0 + j));
+          p[j] = q.x; p[j + 1] = q.y; p[j + 2] = q.z; p[j + 3] = q.w;
+        } else if (!vec) {
+#pragma unroll
+          for (int i = j; i < j + 4; ++i)
+            if (e0 + i < E) p[i] = __ldg(zt + e0 + i);
+        }
+      }
+    }
+    // the slots: expert, logit, and the gate's gradient
+    int idx[kMaxTopK];
+    float zs[kMaxTopK], ds[kMaxTopK];
+#pragma unroll
+    for (int s = 0; s < kMaxTopK; ++s) {
+      idx[s] = -1;
+      zs[s] = neg_inf();
+      ds[s] = 0.f;
+      if (s < k && live) {
+        const size_t q = (size_t)t * k + s;
+        idx[s] = __ldg(a.topk_idx + q);
+        if (idx[s] < 0 || idx[s] >= E) {
+          if (sub == 0) report_error(a.err, MOE_DEVERR_EXPERT_INDEX, (int32_t)q);
+          idx[s] = -1;
+        } else {
+          zs[s] = __ldg(zt + idx[s]);
+          if (a.row_dot) {
+            const int r = a.inv[q];
+            ds[s] = (r >= 0 && r < a.R) ? a.row_dot[r] : 0.f;
+          } else if (a.dgate) {
+            ds[s] = __ldg(a.dgate + q);
+          }
+        }
+      }
+    }
+    float m = neg_inf(), inv = 0.f;  // of all experts
     if (need_p) {
-      float m = neg_inf();
+#pragma unroll
+      for (int j = 0; j < kEpl; ++j) m = fmaxf(m, p[j]);
+      m = group_max<LPT>(m);
+      // a token whose logits are all -inf has no probabilities
+      const float top = m > neg_inf() ? m : 0.f;
+      float sum = 0.f;
 #pragma unroll
       for (int j = 0; j < kEpl; ++j) {
-        const int e = lane + 32 * j;
-        p[j] = e < E ? zt[e] : neg_inf();
-        m = fmaxf(m, p[j]);
+        p[j] = e0 + j < E ? expf(p[j] - top) : 0.f;
+        sum += p[j];
       }
-      m = warp_max(m);
-      if (m > neg_inf()) {  // a token whose logits are all -inf has no probabilities
-        float sum = 0.f;
+      sum = group_sum<LPT>(sum);
+      const bool some = m > neg_inf();
+      inv = some ? 1.f / sum : 0.f;
+      const float lse = some ? m + logf(sum) : 0.f;
+      float pf = 0.f;
 #pragma unroll
-        for (int j = 0; j < kEpl; ++j) {
-          p[j] = lane + 32 * j < E ? expf(p[j] - m) : 0.f;
-          sum += p[j];
-        }
-        sum = warp_sum(sum);
-        const float inv = 1.f / sum, lse = m + logf(sum);
-        float pf = 0.f;
+      for (int j = 0; j < kEpl; ++j) {
+        p[j] = some ? p[j] * inv : 0.f;
+        pf = fmaf(p[j], f[j], pf);
+      }
+      if (losses) {
+        pf = group_sum<LPT>(pf);
 #pragma unroll
-        for (int j = 0; j < kEpl; ++j) {
-          p[j] *= inv;
-          pf = fmaf(p[j], f[j], pf);
-        }
-        if (losses) {
-          pf = warp_sum(pf);
-#pragma unroll
-          for (int j = 0; j < kEpl; ++j) dz[j] = p[j] * (c0 * (f[j] - pf) + c1 * lse);
-        }
-        if (a.gate_mode == MOE_GATE_SOFTMAX_TOPK_RAW) {
-          const float ps = idx >= 0 ? expf(zs - m) * inv : 0.f;
-          ds = ps * dg;
-          const float sd = warp_sum(ds);
-#pragma unroll
-          for (int j = 0; j < kEpl; ++j) dz[j] = fmaf(-p[j], sd, dz[j]);
-        }
-      } else {
-#pragma unroll
-        for (int j = 0; j < kEpl; ++j) p[j] = 0.f;
+        for (int j = 0; j < kEpl; ++j) dz[j] = p[j] * (c0 * (f[j] - pf) + c1 * lse);
       }
     }
-    if (a.gate_mode != MOE_GATE_SOFTMAX_TOPK_RAW) {
-      const float m = warp_max(zs);
-      const float ex = (idx >= 0 && m > neg_inf()) ? expf(zs - m) : 0.f;
-      const float sum = warp_sum(ex);
-      const float gt = sum > 0.f ? ex / sum : ex;  // a NaN logit stays one
-      const float gd = warp_sum(gt * dg);
-      ds = gt * (dg - gd);
+    if (raw) {
+      float sd = 0.f;
+#pragma unroll
+      for (int s = 0; s < kMaxTopK; ++s)
+        if (s < k) {
+          const float ps = (idx[s] >= 0 && m > neg_inf()) ? expf(zs[s] - m) * inv : 0.f;
+          ds[s] *= ps;
+          sd += ds[s];
+        }
+#pragma unroll
+      for (int j = 0; j < kEpl; ++j) dz[j] = fmaf(-p[j], sd, dz[j]);
+    } else {
+      float ms = neg_inf(), sum = 0.f, gd = 0.f;
+#pragma unroll
+      for (int s = 0; s < kMaxTopK; ++s)
+        if (s < k) ms = fmaxf(ms, zs[s]);
+#pragma unroll
+      for (int s = 0; s < kMaxTopK; ++s)
+        if (s < k) {
+          zs[s] = (idx[s] >= 0 && ms > neg_inf()) ? expf(zs[s] - ms) : 0.f;
+          sum += zs[s];
+        }
+      const float is = sum != 0.f ? 1.f / sum : 0.f;  // a NaN logit stays one
+#pragma unroll
+      for (int s = 0; s < kMaxTopK; ++s)
+        if (s < k) {
+          zs[s] *= is;
+          gd = fmaf(zs[s], ds[s], gd);
+        }
+#pragma unroll
+      for (int s = 0; s < kMaxTopK; ++s)
+        if (s < k) ds[s] = zs[s] * (ds[s] - gd);
     }
-    for (int s = 0; s < k; ++s) {
-      const int e = __shfl_sync(0xffffffffu, idx, s);
-      const float v = __shfl_sync(0xffffffffu, ds, s);
 #pragma unroll
-      for (int j = 0; j < kEpl; ++j)
-        if (e == lane + 32 * j) dz[j] += v;
-    }
+    for (int s = 0; s < kMaxTopK; ++s)
+      if (s < k) {
 #pragma unroll
-    for (int j = 0; j < kEpl; ++j) {
-      const int e = lane + 32 * j;
-      if (e < E && a.dlogits) a.dlogits[(size_t)t * E + e] = dz[j];
-      db[j] += dz[j];
-      if (TC && e < tc.Ep) {
-        __nv_bfloat16 part[kSplit];
-        split_terms(e < E ? dz[j] : 0.f, part);
-#pragma unroll
-        for (int i = 0; i < kSplit; ++i)
-          if (tc.term[i]) tc.term[i][(size_t)t * tc.Ep + e] = part[i];
+        for (int j = 0; j < kEpl; ++j)
+          if (idx[s] == e0 + j) dz[j] += ds[s];
       }
+    if (!live) continue;
+#pragma unroll
+    for (int j = 0; j < kEpl; ++j) db[j] += dz[j];
+    if (a.dlogits) {
+      float *out = a.dlogits + (size_t)t * E + e0;
+#pragma unroll
+      for (int j = 0; j < kEpl; j += 4) {
+        if (vec && e0 + j < E) {
+          *reinterpret_cast<float4 *>(out + j) =
+              make_float4(dz[j], dz[j + 1], dz[j + 2], dz[j + 3]);
+        } else if (!vec) {
+#pragma unroll
+          for (int i = j; i < j + 4; ++i)
+            if (e0 + i < E) out[i] = dz[i];
+        }
+      }
+    }
+    if (TC && e0 < tc.Ep) {
+      __nv_bfloat16 part[kSplit][kEpl];
+#pragma unroll
+      for (int j = 0; j < kEpl; ++j) {
+        __nv_bfloat16 q[kSplit];
+        split_terms(e0 + j < E ? dz[j] : 0.f, q);
+#pragma unroll
+        for (int i = 0; i < kSplit; ++i) part[i][j] = q[i];
+      }
+#pragma unroll
+      for (int i = 0; i < kSplit; ++i)
+        if (tc.term[i])
+          *reinterpret_cast<uint4 *>(tc.term[i] + (size_t)t * tc.Ep + e0) =
+              *reinterpret_cast<const uint4 *>(part[i]);
     }
   }
   if (db_part == nullptr) return;
 #pragma unroll
-  for (int j = 0; j < kEpl; ++j) red[warp][lane + 32 * j] = db[j];
+  for (int j = 0; j < kEpl; ++j) {
+#pragma unroll
+    for (int o = 16; o >= LPT; o >>= 1) db[j] += __shfl_xor_sync(0xffffffffu, db[j], o);
+    if (lane < LPT) red[warp][e0 + j] = db[j];
+  }
   __syncthreads();
-  for (int e = threadIdx.x; e < E; e += 256) {
+  for (int e = threadIdx.x; e < E; e += kDzThreads) {
     float v = 0.f;
 #pragma unroll
-    for (int w = 0; w < 8; ++w) v += red[w][e];
+    for (int w = 0; w < kWarps; ++w) v += red[w][e];
     db_part[(size_t)blockIdx.x * E + e] = v;
   }
 }
@@ -177,33 +254,29 @@ __global__ void __launch_bounds__(256) k_dlogits(RouteBwdArgs a, float *db_part,
 // block walks over its piece of the tokens with dz broadcast from shared memory. 4 E flops
 // per element of x: up to E = 16 the reads of x and the writes of dx bound it.
 constexpr int kFewExperts = 32;
-constexpr int kProjThreads = 128, kProjTokens = 32;
+constexpr int kProjThreads = 128, kProjTokens = 128;
 
+// VC values of type T as they lie in memory, and unpacked
 template <typename T, int VC>
-__device__ __forceinline__ void load_cols(const T *p, float (&f)[VC]) {
-  if constexpr (sizeof(T) == 4) {
-    if constexpr (VC == 4) {
-      const float4 v = __ldg(reinterpret_cast<const float4 *>(p));
-      f[0] = v.x; f[1] = v.y; f[2] = v.z; f[3] = v.w;
-    } else {
-      const float2 v = __ldg(reinterpret_cast<const float2 *>(p));
-      f[0] = v.x; f[1] = v.y;
-    }
-  } else {
-    uint32_t u[VC / 2];
-    if constexpr (VC == 4) {
+struct Cols {
+  uint32_t u[VC * sizeof(T) / 4];
+  __device__ __forceinline__ void load(const T *p) {
+    constexpr int n = VC * sizeof(T) / 4;
+    if constexpr (n == 4) {
+      const uint4 v = __ldg(reinterpret_cast<const uint4 *>(p));
+      u[0] = v.x; u[1] = v.y; u[2] = v.z; u[3] = v.w;
+    } else if constexpr (n == 2) {
       const uint2 v = __ldg(reinterpret_cast<const uint2 *>(p));
       u[0] = v.x; u[1] = v.y;
     } else {
       u[0] = __ldg(reinterpret_cast<const uint32_t *>(p));
     }
-#pragma unroll
-    for (int i = 0; i < VC / 2; ++i) {
-      f[2 * i] = __uint_as_float(u[i] << 16);
-      f[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
-    }
   }
-}
+  __device__ __forceinline__ float get(int c) const {
+    if (sizeof(T) == 4) return __uint_as_float(u[c]);
+    return __uint_as_float((c & 1) ? u[c / 2] & 0xffff0000u : u[c / 2] << 16);
+  }
+};
 
 template <typename T, int EP, int VC>
 __global__ void __launch_bounds__(kProjThreads) k_route_proj(const T *x, const T *w,
@@ -221,7 +294,12 @@ __global__ void __launch_bounds__(kProjThreads) k_route_proj(const T *x, const T
   for (int e = 0; e < EP; ++e) {
 #pragma unroll
     for (int c = 0; c < VC; ++c) wr[e][c] = acc[e][c] = 0.f;
-    if (dx && live && e < E) load_cols<T, VC>(w + (size_t)e * d + col, wr[e]);
+    if (dx && live && e < E) {
+      Cols<T, VC> r;
+      r.load(w + (size_t)e * d + col);
+#pragma unroll
+      for (int c = 0; c < VC; ++c) wr[e][c] = r.get(c);
+    }
   }
   const int t0 = blockIdx.y * per, t1 = min(n_tok, t0 + per);
   for (int tb = t0; tb < t1; tb += kProjTokens) {
@@ -233,12 +311,20 @@ __global__ void __launch_bounds__(kProjThreads) k_route_proj(const T *x, const T
     }
     __syncthreads();
     if (!live) continue;
-    constexpr int NB = 4;  // tokens requested before any is used
-    for (int u0 = 0; u0 < n; u0 += NB) {
-      float xv[NB][VC];
+    // 32 bytes of x per thread are requested while the 32 before are worked on
+    constexpr int NB = 32 / (VC * (int)sizeof(T)) < 8 ? 32 / (VC * (int)sizeof(T)) : 8;
+    Cols<T, VC> next[NB];
+    auto request = [&](int u0) {
 #pragma unroll
       for (int i = 0; i < NB; ++i)
-        if (dw_part && u0 + i < n) load_cols<T, VC>(x + (size_t)(tb + u0 + i) * d + col, xv[i]);
+        if (dw_part && u0 + i < n) next[i].load(x + (size_t)(tb + u0 + i) * d + col);
+    };
+    request(0);
+    for (int u0 = 0; u0 < n; u0 += NB) {
+      Cols<T, VC> xv[NB];
+#pragma unroll
+      for (int i = 0; i < NB; ++i) xv[i] = next[i];
+      request(u0 + NB);
 #pragma unroll
       for (int i = 0; i < NB; ++i) {
         if (u0 + i >= n) break;
@@ -265,7 +351,7 @@ __global__ void __launch_bounds__(kProjThreads) k_route_proj(const T *x, const T
 #pragma unroll
           for (int e = 0; e < EP; ++e)
 #pragma unroll
-            for (int c = 0; c < VC; ++c) acc[e][c] = fmaf(z[e], xv[i][c], acc[e][c]);
+            for (int c = 0; c < VC; ++c) acc[e][c] = fmaf(z[e], xv[i].get(c), acc[e][c]);
         }
       }
     }
@@ -315,8 +401,14 @@ __global__ void __launch_bounds__(128) k_route_sums(const float *part, int piece
   if (threadIdx.x == 0) db[e] = (red[0] + red[1]) + (red[2] + red[3]);
 }
 
-int dlogits_blocks(int T) {
-  const int b = ceil_div(T, 8);
+// lanes per token of k_dlogits: eight experts each, the tensor-core terms' padding too
+int dz_lanes(int cols) {
+  int l = 1;
+  while (l * kEpl < cols) l *= 2;
+  return l;
+}
+int dlogits_blocks(int T, int lanes) {
+  const int b = ceil_div(T, kDzThreads / lanes);
   return b < kMaxBlocks ? b : kMaxBlocks;
 }
 
@@ -335,40 +427,45 @@ int dw_pieces_tc(int T, int d) {
   return s < 1 ? 1 : (s < most ? s : most);
 }
 
-// ... of k_route_proj: three blocks per SM (as many as its registers let it hold), at
-// least sixteen tokens each
+// ... of k_route_proj: as many blocks as the SMs hold (registers), at least sixteen tokens
+// each
 int proj_cols(int E) { return E <= 16 ? 4 : 2; }
 int proj_pieces(int T, int d, int E) {
-  const int s = 148 * 3 / ceil_div(d, kProjThreads * proj_cols(E)), most = ceil_div(T, 16);
+  const int s = 148 * (E <= 8 ? 4 : 2) / ceil_div(d, kProjThreads * proj_cols(E)), most = ceil_div(T, 16);
   return s < 1 ? 1 : (s < most ? s : most);
 }
 
 int e_padded(int E) { return (E + 63) / 64 * 64; }
 
 template <bool TC>
-cudaError_t dlogits(const RouteBwdArgs &a, float *db_part, const RouteTcArgs &tc, cudaStream_t st) {
-  const dim3 g(dlogits_blocks(a.T)), b(256);
-  const int cols = TC ? tc.Ep : a.E;
-  if (cols <= 32) return launch_pdl(k_dlogits<1, TC>, g, b, 0, st, a, db_part, tc);
-  if (cols <= 64) return launch_pdl(k_dlogits<2, TC>, g, b, 0, st, a, db_part, tc);
-  if (cols <= 128) return launch_pdl(k_dlogits<4, TC>, g, b, 0, st, a, db_part, tc);
-  return launch_pdl(k_dlogits<8, TC>, g, b, 0, st, a, db_part, tc);
+cudaError_t dlogits(const RouteBwdArgs &a, float *db_part, const RouteTcArgs &tc, int lanes,
+                    cudaStream_t st) {
+  const dim3 g(dlogits_blocks(a.T, lanes)), b(kDzThreads);
+  if constexpr (!TC) {  // the terms' rows are 64 experts at least
+    if (lanes == 1) return launch_pdl(k_dlogits<1, TC>, g, b, 0, st, a, db_part, tc);
+    if (lanes == 2) return launch_pdl(k_dlogits<2, TC>, g, b, 0, st, a, db_part, tc);
+    if (lanes == 4) return launch_pdl(k_dlogits<4, TC>, g, b, 0, st, a, db_part, tc);
+  }
+  if (lanes == 8) return launch_pdl(k_dlogits<8, TC>, g, b, 0, st, a, db_part, tc);
+  if (lanes == 16) return launch_pdl(k_dlogits<16, TC>, g, b, 0, st, a, db_part, tc);
+  return launch_pdl(k_dlogits<32, TC>, g, b, 0, st, a, db_part, tc);
 }
 
 template <typename T>
 cudaError_t sums(const RouteBwdArgs &a, const float *dw_part, int pieces, const float *db_part,
-                 cudaStream_t st) {
+                 int lanes, cudaStream_t st) {
   const size_t n = a.dw ? (size_t)a.E * a.d : 0;
   const int dw_blocks = (int)((n / 4 + 127) / 128), db_blocks = a.db ? a.E : 0;
   if (dw_blocks + db_blocks == 0) return cudaSuccess;
   return launch_pdl(k_route_sums<T>, dim3(dw_blocks + db_blocks), dim3(128), 0, st, dw_part, pieces,
-                    n, static_cast<T *>(a.dw), dw_blocks, db_part, dlogits_blocks(a.T), a.E, a.db);
+                    n, static_cast<T *>(a.dw), dw_blocks, db_part, dlogits_blocks(a.T, lanes), a.E,
+                    a.db);
 }
 
 template <typename T>
 cudaError_t route_bwd_few(const RouteBwdArgs &a, cudaStream_t st) {
   float *db_part = static_cast<float *>(a.part);
-  cudaError_t e = dlogits<false>(a, a.db ? db_part : nullptr, RouteTcArgs{}, st);
+  cudaError_t e = dlogits<false>(a, a.db ? db_part : nullptr, RouteTcArgs{}, dz_lanes(a.E), st);
   if (e != cudaSuccess) return e;
   const int pieces = proj_pieces(a.T, a.d, a.E);
   float *dw_part = db_part + (size_t)kMaxBlocks * a.E;
@@ -384,14 +481,14 @@ cudaError_t route_bwd_few(const RouteBwdArgs &a, cudaStream_t st) {
                  : (a.E <= 16 ? run(k_route_proj<T, 16, 4>) : run(k_route_proj<T, 32, 2>));
     if (e != cudaSuccess) return e;
   }
-  return sums<T>(a, dw_part, pieces, db_part, st);
+  return sums<T>(a, dw_part, pieces, db_part, dz_lanes(a.E), st);
 }
 
 // fp32, more experts: tiles on CUDA cores
 cudaError_t route_bwd_simt(const RouteBwdArgs &a, cudaStream_t st) {
   float *db_part = static_cast<float *>(a.part);
   const dim3 b(256);
-  cudaError_t e = dlogits<false>(a, a.db ? db_part : nullptr, RouteTcArgs{}, st);
+  cudaError_t e = dlogits<false>(a, a.db ? db_part : nullptr, RouteTcArgs{}, dz_lanes(a.E), st);
   if (e != cudaSuccess) return e;
   const float *x = static_cast<const float *>(a.x), *w = static_cast<const float *>(a.w);
   if (a.dx) {
@@ -426,7 +523,7 @@ cudaError_t route_bwd_simt(const RouteBwdArgs &a, cudaStream_t st) {
                    dim3(ceil_div(a.d, simt::BN), ceil_div(a.E, simt::BM), pieces), b, 0, st, m);
     if (e != cudaSuccess) return e;
   }
-  return sums<float>(a, dw_part, pieces, db_part, st);
+  return sums<float>(a, dw_part, pieces, db_part, dz_lanes(a.E), st);
 }
 
 // bf16 scratch: tables | db partials | dW partials | terms
@@ -466,8 +563,9 @@ cudaError_t route_bwd_tc(const RouteBwdArgs &a, cudaStream_t st) {
   tc.Ep = e_padded(a.E);
   tc.pieces = dw_pieces_tc(a.T, a.d);
   tc.err = a.err;
-  cudaError_t e = terms ? dlogits<true>(a, a.db ? db_part : nullptr, tc, st)
-                        : dlogits<false>(a, a.db ? db_part : nullptr, tc, st);
+  const int lanes = dz_lanes(terms ? tc.Ep : a.E);
+  cudaError_t e = terms ? dlogits<true>(a, a.db ? db_part : nullptr, tc, lanes, st)
+                        : dlogits<false>(a, a.db ? db_part : nullptr, tc, lanes, st);
   if (e != cudaSuccess) return e;
   if (a.dx) {
     e = launch_route_dx_tc(tc, st);
@@ -477,7 +575,7 @@ cudaError_t route_bwd_tc(const RouteBwdArgs &a, cudaStream_t st) {
     e = launch_route_dw_tc(tc, st);
     if (e != cudaSuccess) return e;
   }
-  return sums<__nv_bfloat16>(a, tc.dw_part, tc.pieces, db_part, st);
+  return sums<__nv_bfloat16>(a, tc.dw_part, tc.pieces, db_part, lanes, st);
 }
 
 }  // namespace
