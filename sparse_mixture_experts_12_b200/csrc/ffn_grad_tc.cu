@@ -462,8 +462,7 @@ struct GemmArgs {
   const int32_t *poff, *offsets;
   const int32_t *dx_off;  // first row of each expert in dx
   int G;
-  // dx: N = d, K = F, nseg pairs (A, B) added. Weights: njobs products of M x N, each the
-  // sum of nseg pairs.
+  // dx: N = d, K = F, nseg pairs (A, B) added. Weights: njobs products of M x N.
   int N, K, nseg;
   int M[3], Ns[3], njobs;
   void *out;              // dx; fp32 weights' gradients
@@ -508,7 +507,7 @@ k_pair_gemm(const __grid_constant__ GemmMaps maps, GemmArgs a) {
       const int mt = ceil_div(a.M[r.job], kPairM);
       r.m0 = (rem % mt) * kPairM;
       r.n0 = (rem / mt) * 256;
-      r.nkb = a.nseg * ((a.poff[r.g + 1] - a.poff[r.g]) / kBlockK);
+      r.nkb = (a.poff[r.g + 1] - a.poff[r.g]) / kBlockK;
     } else {
       int n, m;
       decode_tile(t, ctl->pre, a.G, n_tiles, r.g, n, m);
@@ -532,25 +531,24 @@ k_pair_gemm(const __grid_constant__ GemmMaps maps, GemmArgs a) {
       const Tile q = tile_at(t);
       const int row0 = a.poff[q.g];
       const int bcol = q.n0 + s.rank * kRowTile;
-      const int nk = DW ? (a.poff[q.g + 1] - row0) / kBlockK : nk1;  // slices of a segment
-      int seg = 0, k = 0;
+      int seg = 0, k = 0;  // pair of operands, slice of it
       for (int kb = 0; kb < q.nkb; ++kb) {
         if (!(ok = wait_on(s, &ctl->empty[ring.stage], ring.phase ^ 1u, a.err, 31))) break;
         if (s.rank == 0) mbar_expect_tx(&ctl->full[ring.stage], 2 * kStageBytes);
         uint8_t *st = s.smem + (size_t)ring.stage * kStageBytes;
         const uint32_t bar = full0 + (uint32_t)(ring.stage * sizeof(uint64_t));
         if (DW) {
-          const int r = row0 + k * kBlockK, j = q.job + seg;
-          load_mn(&maps.a[j], bar, st, q.m0 + s.rank * kRowTile, r);
-          load_mn(&maps.b[j], bar, st + kOperand, bcol, r);
+          const int r = row0 + kb * kBlockK;
+          load_mn(&maps.a[q.job], bar, st, q.m0 + s.rank * kRowTile, r);
+          load_mn(&maps.b[q.job], bar, st + kOperand, bcol, r);
         } else {
           const int k0 = k * kBlockK;
           tma_load_2d_pair(&maps.a[seg], bar, st, k0, row0 + q.m0 + s.rank * kRowTile);
           load_mn(&maps.b[seg], bar, st + kOperand, bcol, q.g * a.K + k0);
-        }
-        if (++k == nk) {
-          k = 0;
-          ++seg;
+          if (++k == nk1) {
+            k = 0;
+            ++seg;
+          }
         }
         ring.mark();
         ring.next();
@@ -826,7 +824,6 @@ cudaError_t launch_dw_tc(const FfnGradArgs &f, cudaStream_t st) {
   a.poff = f.poff;
   a.offsets = f.offsets;
   a.G = f.G;
-  a.nseg = 1;
   a.err = f.err;
   return launch_pairs(k_pair_gemm<true>, 3, tiles, st, m, a);
 }
@@ -835,7 +832,8 @@ cudaError_t launch_route_dx_tc(const RouteTcArgs &r, cudaStream_t st) {
   GemmMaps m;
   GemmArgs a{};
   for (int j = 0; j < kSplit; ++j)
-    if (!make_map(&m.a[j], r.term[j], (uint64_t)r.T, (uint64_t)r.Ep, kRowTile) ||
+    if (!make_map(&m.a[j], r.terms + (size_t)j * r.Ep, (uint64_t)r.T, (uint64_t)r.Ep, kRowTile,
+                  (uint64_t)kSplit * r.Ep) ||
         !make_map(&m.b[j], r.w, (uint64_t)r.E, (uint64_t)r.d, kBlockK))
       return cudaErrorInvalidValue;
   if (!make_f32_map(&m.o[0], r.dx, (uint64_t)r.T, (uint64_t)r.d)) return cudaErrorInvalidValue;
@@ -856,22 +854,22 @@ cudaError_t launch_route_dx_tc(const RouteTcArgs &r, cudaStream_t st) {
 cudaError_t launch_route_dw_tc(const RouteTcArgs &r, cudaStream_t st) {
   GemmMaps m;
   GemmArgs a{};
-  for (int j = 0; j < kSplitDw; ++j)
-    if (!make_map(&m.a[j], r.term[j], (uint64_t)r.T, (uint64_t)r.Ep, kBlockK) ||
-        !make_map(&m.b[j], r.x, (uint64_t)r.T, (uint64_t)r.d, kBlockK))
-      return cudaErrorInvalidValue;
-  if (!make_f32_map(&m.o[0], r.dw_part, (uint64_t)r.pieces * r.E, (uint64_t)r.d))
+  // the terms side by side are the rows of one product: x is read once for both
+  const int M = kSplitDw * r.Ep;
+  if (!make_map(&m.a[0], r.terms, (uint64_t)r.T, (uint64_t)M, kBlockK, (uint64_t)kSplit * r.Ep) ||
+      !make_map(&m.b[0], r.x, (uint64_t)r.T, (uint64_t)r.d, kBlockK) ||
+      !make_f32_map(&m.o[0], r.dw_part, (uint64_t)r.pieces * M, (uint64_t)r.d))
     return cudaErrorInvalidValue;
   a.poff = a.offsets = r.piece;
   a.G = r.pieces;
-  a.nseg = kSplitDw;
   a.njobs = 1;
-  a.M[0] = r.E;
+  a.M[0] = M;
   a.Ns[0] = r.d;
   a.out = r.dw_part;
   a.out_f32 = 1;
   a.err = r.err;
-  return launch_pairs(k_pair_gemm<true>, 3, (long long)r.pieces * ceil_div(r.d, 256), st, m, a);
+  return launch_pairs(k_pair_gemm<true>, 3,
+                      (long long)r.pieces * ceil_div(M, kPairM) * ceil_div(r.d, 256), st, m, a);
 }
 
 }  // namespace moe

@@ -74,10 +74,10 @@ struct RouteBwdArgs {
 constexpr int kSplit = 3, kSplitDw = 2;
 struct RouteTcArgs {
   const void *x, *w;           // [T, d], [E, d]
-  __nv_bfloat16 *term[kSplit]; // [T, Ep] each, Ep = E rounded up to 64 (zeros behind E)
+  __nv_bfloat16 *terms;        // [T, kSplit, Ep], Ep = E rounded up to 64 (zeros behind E)
   int32_t *all, *all_rows;     // {0, T rounded up to 64}, {0, T}
   int32_t *piece;              // [pieces + 1] first tokens (multiples of 64) of the pieces of dW
-  float *dx, *dw_part;         // [T, d]; [pieces, E, d]
+  float *dx, *dw_part;         // [T, d]; [pieces, kSplitDw, Ep, d]: a sum for each term
   int T, d, E, Ep, pieces;
   int32_t *err;
 };

@@ -54,7 +54,7 @@ __device__ __forceinline__ float group_sum(float v) {
 }
 
 template <int LPT, bool TC>
-__global__ void __launch_bounds__(kDzThreads) k_dlogits(RouteBwdArgs a, float *db_part,
+__global__ void __launch_bounds__(kDzThreads, 8) k_dlogits(RouteBwdArgs a, float *db_part,
                                                         RouteTcArgs tc) {
   constexpr int kTokens = kDzThreads / LPT, kWarps = kDzThreads / 32;
   __shared__ float red[kWarps][LPT * kEpl];
@@ -228,9 +228,8 @@ __global__ void __launch_bounds__(kDzThreads) k_dlogits(RouteBwdArgs a, float *d
       }
 #pragma unroll
       for (int i = 0; i < kSplit; ++i)
-        if (tc.term[i])
-          *reinterpret_cast<uint4 *>(tc.term[i] + (size_t)t * tc.Ep + e0) =
-              *reinterpret_cast<const uint4 *>(part[i]);
+        *reinterpret_cast<uint4 *>(tc.terms + ((size_t)t * kSplit + i) * tc.Ep + e0) =
+            *reinterpret_cast<const uint4 *>(part[i]);
     }
   }
   if (db_part == nullptr) return;
@@ -367,38 +366,58 @@ __global__ void __launch_bounds__(kProjThreads) k_route_proj(const T *x, const T
   }
 }
 
-// dw[i] = sum over the pieces of part [pieces, n], and (the last E blocks) db[e] = the
-// sum of the blocks' partials, each in a fixed order
+// dw [E, d] = the sum of the `parts` partials (each `rows` x d, its first E rows), and (the
+// last blocks) db[e] = the sum of the blocks' partials. Eight (32) groups of threads take
+// every eighth (32nd) partial, so that few loads follow one another; the groups are added
+// in order.
 template <typename T>
-__global__ void __launch_bounds__(128) k_route_sums(const float *part, int pieces, size_t n, T *dw,
-                                                    int dw_blocks, const float *db_part, int blocks,
-                                                    int E, float *db) {
-  __shared__ float red[4];
+__global__ void __launch_bounds__(256) k_route_sums(const float *part, int parts, int rows, int d,
+                                                    T *dw, int dw_blocks, const float *db_part,
+                                                    int blocks, int E, float *db) {
+  __shared__ float4 red4[8][32];
+  __shared__ float red[32][8];
+  const int tid = threadIdx.x;
   pdl_wait();
   pdl_trigger();
-  if ((int)blockIdx.x < dw_blocks) {  // n is a multiple of 4
-    const size_t i = ((size_t)blockIdx.x * 128 + threadIdx.x) * 4;
-    if (i >= n) return;
+  if ((int)blockIdx.x < dw_blocks) {  // d is a multiple of 4
+    const int x = tid & 31, g = tid >> 5;
+    const size_t i = ((size_t)blockIdx.x * 32 + x) * 4;
+    const bool in = i < (size_t)E * d;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-    for (int s = 0; s < pieces; ++s) {
-      const float4 p = __ldg(reinterpret_cast<const float4 *>(part + (size_t)s * n + i));
+    if (in) {
+#pragma unroll 4
+      for (int s = g; s < parts; s += 8) {
+        const float4 p = __ldg(reinterpret_cast<const float4 *>(part + (size_t)s * rows * d + i));
+        v.x += p.x; v.y += p.y; v.z += p.z; v.w += p.w;
+      }
+    }
+    red4[g][x] = v;
+    __syncthreads();
+    if (g > 0 || !in) return;
+#pragma unroll
+    for (int q = 1; q < 8; ++q) {
+      const float4 p = red4[q][x];
       v.x += p.x; v.y += p.y; v.z += p.z; v.w += p.w;
     }
-    dw[i] = Elem<T>::from_f(v.x);
-    dw[i + 1] = Elem<T>::from_f(v.y);
-    dw[i + 2] = Elem<T>::from_f(v.z);
-    dw[i + 3] = Elem<T>::from_f(v.w);
+    if constexpr (sizeof(T) == 4)
+      *reinterpret_cast<float4 *>(dw + i) = v;
+    else
+      *reinterpret_cast<uint2 *>(dw + i) =
+          make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
     return;
   }
-  const int e = blockIdx.x - dw_blocks;
+  const int e = ((int)blockIdx.x - dw_blocks) * 8 + (tid & 7), g = tid >> 3;
   float v = 0.f;
-#pragma unroll 4
-  for (int i = threadIdx.x; i < blocks; i += 128) v += db_part[(size_t)i * E + e];
-  v = warp_sum(v);
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+  if (e < E) {
+#pragma unroll 8
+    for (int s = g; s < blocks; s += 32) v += db_part[(size_t)s * E + e];
+  }
+  red[g][tid & 7] = v;
   __syncthreads();
-  if (threadIdx.x == 0) db[e] = (red[0] + red[1]) + (red[2] + red[3]);
+  if (tid >= 8 || e >= E) return;
+#pragma unroll
+  for (int q = 1; q < 32; ++q) v += red[q][tid];
+  db[e] = v;
 }
 
 // lanes per token of k_dlogits: eight experts each, the tensor-core terms' padding too
@@ -452,14 +471,14 @@ cudaError_t dlogits(const RouteBwdArgs &a, float *db_part, const RouteTcArgs &tc
 }
 
 template <typename T>
-cudaError_t sums(const RouteBwdArgs &a, const float *dw_part, int pieces, const float *db_part,
-                 int lanes, cudaStream_t st) {
-  const size_t n = a.dw ? (size_t)a.E * a.d : 0;
-  const int dw_blocks = (int)((n / 4 + 127) / 128), db_blocks = a.db ? a.E : 0;
+cudaError_t sums(const RouteBwdArgs &a, const float *dw_part, int parts, int rows,
+                 const float *db_part, int lanes, cudaStream_t st) {
+  const int dw_blocks = a.dw ? (int)(((size_t)a.E * a.d / 4 + 31) / 32) : 0;
+  const int db_blocks = a.db ? ceil_div(a.E, 8) : 0;
   if (dw_blocks + db_blocks == 0) return cudaSuccess;
-  return launch_pdl(k_route_sums<T>, dim3(dw_blocks + db_blocks), dim3(128), 0, st, dw_part, pieces,
-                    n, static_cast<T *>(a.dw), dw_blocks, db_part, dlogits_blocks(a.T, lanes), a.E,
-                    a.db);
+  return launch_pdl(k_route_sums<T>, dim3(dw_blocks + db_blocks), dim3(256), 0, st, dw_part, parts,
+                    rows, a.d, static_cast<T *>(a.dw), dw_blocks, db_part,
+                    dlogits_blocks(a.T, lanes), a.E, a.db);
 }
 
 template <typename T>
@@ -481,7 +500,7 @@ cudaError_t route_bwd_few(const RouteBwdArgs &a, cudaStream_t st) {
                  : (a.E <= 16 ? run(k_route_proj<T, 16, 4>) : run(k_route_proj<T, 32, 2>));
     if (e != cudaSuccess) return e;
   }
-  return sums<T>(a, dw_part, pieces, db_part, dz_lanes(a.E), st);
+  return sums<T>(a, dw_part, pieces, a.E, db_part, dz_lanes(a.E), st);
 }
 
 // fp32, more experts: tiles on CUDA cores
@@ -523,22 +542,20 @@ cudaError_t route_bwd_simt(const RouteBwdArgs &a, cudaStream_t st) {
                    dim3(ceil_div(a.d, simt::BN), ceil_div(a.E, simt::BM), pieces), b, 0, st, m);
     if (e != cudaSuccess) return e;
   }
-  return sums<float>(a, dw_part, pieces, db_part, dz_lanes(a.E), st);
+  return sums<float>(a, dw_part, pieces, a.E, db_part, dz_lanes(a.E), st);
 }
 
 // bf16 scratch: tables | db partials | dW partials | terms
 struct TcScratch {
-  size_t tables, db, dw, term, term_bytes, total;
+  size_t db, dw, terms, total;
 };
 TcScratch tc_scratch(int T, int d, int E) {
   auto up = [](size_t v) { return (v + 255) & ~(size_t)255; };
   TcScratch s;
-  s.tables = 0;
   s.db = up((kMaxExperts + 1 + 4) * 4);
   s.dw = s.db + up((size_t)kMaxBlocks * E * 4);
-  s.term = s.dw + up((size_t)dw_pieces_tc(T, d) * E * d * 4);
-  s.term_bytes = up((size_t)T * e_padded(E) * 2);
-  s.total = s.term + kSplit * s.term_bytes;
+  s.terms = s.dw + up((size_t)dw_pieces_tc(T, d) * kSplitDw * e_padded(E) * d * 4);
+  s.total = s.terms + up((size_t)T * kSplit * e_padded(E) * 2);
   return s;
 }
 
@@ -549,9 +566,8 @@ cudaError_t route_bwd_tc(const RouteBwdArgs &a, cudaStream_t st) {
   RouteTcArgs tc{};
   tc.x = a.x;
   tc.w = a.w;
-  const int terms = a.dx ? kSplit : (a.dw ? kSplitDw : 0);
-  for (int i = 0; i < terms; ++i)
-    tc.term[i] = reinterpret_cast<__nv_bfloat16 *>(base + s.term + i * s.term_bytes);
+  const bool terms = a.dx || a.dw;
+  tc.terms = reinterpret_cast<__nv_bfloat16 *>(base + s.terms);
   tc.all = reinterpret_cast<int32_t *>(base);
   tc.all_rows = tc.all + 2;
   tc.piece = tc.all + 4;
@@ -575,7 +591,7 @@ cudaError_t route_bwd_tc(const RouteBwdArgs &a, cudaStream_t st) {
     e = launch_route_dw_tc(tc, st);
     if (e != cudaSuccess) return e;
   }
-  return sums<__nv_bfloat16>(a, tc.dw_part, tc.pieces, db_part, lanes, st);
+  return sums<__nv_bfloat16>(a, tc.dw_part, tc.pieces * kSplitDw, tc.Ep, db_part, lanes, st);
 }
 
 }  // namespace

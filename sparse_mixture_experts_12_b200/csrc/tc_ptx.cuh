@@ -362,14 +362,14 @@ inline PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   return fn;
 }
 
-// 2-D bf16 map over a row-major [rows, cols] matrix; box = [box_rows, 64 cols],
-// 128-byte swizzle (the K-major operand layout of the MMAs).
+// 2-D bf16 map over a row-major [rows, cols] matrix (rows `ld` elements apart, 0: cols);
+// box = [box_rows, 64 cols], 128-byte swizzle (the operand layout of the MMAs).
 inline bool make_map(CUtensorMap *map, const void *ptr, uint64_t rows, uint64_t cols,
-                     uint32_t box_rows) {
+                     uint32_t box_rows, uint64_t ld = 0) {
   auto fn = encode_fn();
   if (fn == nullptr) return false;
   cuuint64_t dims[2] = {cols, rows};
-  cuuint64_t strides[1] = {cols * 2};
+  cuuint64_t strides[1] = {(ld ? ld : cols) * 2};
   cuuint32_t box[2] = {(cuuint32_t)kBlockK, box_rows};
   cuuint32_t estr[2] = {1, 1};
   CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(ptr), dims, strides,
