@@ -13,6 +13,7 @@ import math
 import os
 from typing import Optional
 
+import numpy as np
 import torch
 
 from . import synth
@@ -210,11 +211,23 @@ def check_tensor(t: Optional[torch.Tensor], shape, dtype: torch.dtype, name: str
         if optional:
             return
         raise ValueError(f"{name} is missing")
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+    if t.shape != shape or t.dtype is not dtype or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {tuple(shape)} {dtype} tensor, not "
                          f"{tuple(t.shape)} {t.dtype}")
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, not on {device}")
+
+
+def _addr(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+def _on_device(index: int, call, *args):
+    """call(*args, stream) with device `index` current and its current stream."""
+    if torch._C._cuda_getDevice() == index:
+        return call(*args, torch._C._cuda_getCurrentRawStream(index))
+    with torch.cuda.device(index):
+        return call(*args, torch._C._cuda_getCurrentRawStream(index))
 
 
 def _stream():
@@ -469,9 +482,10 @@ class MoELayer:
         """lib.name(cfg, *args, workspace, its size, stream) on this layer's device, on
         that device's current stream."""
         bws = self.bws
-        with torch.cuda.device(bws.device):
-            _check(getattr(self.lib, name)(ctypes.byref(self.cfg), *args, _ptr(bws),
-                                           bws.numel(), _stream()), name)
+        st = _on_device(bws.get_device(), getattr(self.lib, name), ctypes.byref(self.cfg), *args,
+                        bws.data_ptr(), bws.numel())
+        if st:
+            _check(st, name)
 
     def _want(self, t, shape, name, dtype=None, optional=False):
         check_tensor(t, shape, dtype or self.w.torch_dtype, name, self.ws.device, optional)
@@ -518,8 +532,8 @@ class MoELayer:
         self._want(topk_gate, (T, k), "topk_gate", f32, optional=dy_perm is None)
         self._want(dy_perm, (T * k, d), "dy_perm", optional=True)
         self._want(dgate, (T, k), "dgate", f32, optional=True)
-        self._call("moe_combine_backward", _ptr(dy), _ptr(y_perm), _ptr(inv), _ptr(topk_gate),
-                   _ptr(dy_perm), _ptr(dgate))
+        self._call("moe_combine_backward", _addr(dy), _addr(y_perm), _addr(inv), _addr(topk_gate),
+                   _addr(dy_perm), _addr(dgate))
 
     def permute_backward(self, dx_perm: torch.Tensor, inv: torch.Tensor,
                          dx_add: Optional[torch.Tensor], dx: torch.Tensor):
@@ -529,7 +543,7 @@ class MoELayer:
         self._want(inv, (T * k,), "inv", torch.int32)
         self._want(dx_add, (T, d), "dx_add", torch.float32, optional=True)
         self._want(dx, (T, d), "dx")
-        self._call("moe_permute_backward", _ptr(dx_perm), _ptr(inv), _ptr(dx_add), _ptr(dx))
+        self._call("moe_permute_backward", _addr(dx_perm), _addr(inv), _addr(dx_add), _addr(dx))
 
     def route_backward(self, x: Optional[torch.Tensor], logits: torch.Tensor,
                        topk_idx: torch.Tensor, counts: Optional[torch.Tensor],
@@ -550,9 +564,9 @@ class MoELayer:
         self._want(d_losses, (2,), "d_losses", f32, optional=True)
         self._want(dlogits, (T, E), "dlogits", f32, optional=True)
         self._want(dx, (T, d), "dx", f32, optional=True)
-        self._call("moe_route_backward", ctypes.byref(self.weights), _ptr(x), _ptr(logits),
-                   _ptr(topk_idx), _ptr(counts), _ptr(dgate), _ptr(d_losses), _ptr(dlogits),
-                   _ptr(dx), ctypes.byref(g))
+        self._call("moe_route_backward", ctypes.byref(self.weights), _addr(x), _addr(logits),
+                   _addr(topk_idx), _addr(counts), _addr(dgate), _addr(d_losses), _addr(dlogits),
+                   _addr(dx), ctypes.byref(g))
 
     def expert_ffn_backward(self, x_perm: torch.Tensor, offsets: torch.Tensor,
                             dy_perm: torch.Tensor, dx_perm: Optional[torch.Tensor],
@@ -565,8 +579,8 @@ class MoELayer:
         self._want(dy_perm, (R, d), "dy_perm")
         self._want(dx_perm, (R, d), "dx_perm", optional=True)
         g = self._grads(grads, ("w1", "w3", "w2", "b1", "b2"))
-        self._call("moe_expert_ffn_backward", ctypes.byref(self.weights), _ptr(x_perm),
-                   _ptr(offsets), _ptr(dy_perm), _ptr(dx_perm), ctypes.byref(g))
+        self._call("moe_expert_ffn_backward", ctypes.byref(self.weights), _addr(x_perm),
+                   _addr(offsets), _addr(dy_perm), _addr(dx_perm), ctypes.byref(g))
 
     def backward(self, x: torch.Tensor, dy: torch.Tensor, taps: dict,
                  dx: Optional[torch.Tensor] = None, grads: Optional[dict] = None,
@@ -591,8 +605,8 @@ class MoELayer:
             grads = self.new_grads()
         g = self._grads(grads, tuple(self.grad_shapes()) + tuple(grads))
         tp = _taps(taps)
-        self._call("moe_backward", ctypes.byref(self.weights), _ptr(x), ctypes.byref(tp),
-                   _ptr(dy), _ptr(d_losses), _ptr(dx), ctypes.byref(g))
+        self._call("moe_backward", ctypes.byref(self.weights), _addr(x), ctypes.byref(tp),
+                   _addr(dy), _addr(d_losses), _addr(dx), ctypes.byref(g))
         return dx, grads
 
     def last_backward_error(self):
@@ -663,13 +677,14 @@ class AdamW:
             self.bits = 32 if self.exp_avg_scale is None else 8
             self.master = list(state.get("master") or [None] * len(self.params))
         self._lib = load()
-        self._batch = (MoeAdamWTensor * len(self.params))()
+        n_params = len(self.params)
         dt = torch.float32 if self.bits == 32 else torch.float8_e4m3fn
         lists = [self.exp_avg, self.exp_avg_sq, self.master]
         if self.bits == 8:
             lists += [self.exp_avg_scale, self.exp_avg_sq_scale]
-        if any(x is None or len(x) != len(self.params) for x in lists):
+        if any(x is None or len(x) != n_params for x in lists):
             raise ValueError("the state has not one entry for each parameter")
+        self._batch = (MoeAdamWTensor * n_params)()
         for i, p in enumerate(self.params):
             if p.dtype not in _ADAMW_DTYPES:
                 raise ValueError(f"parameter {i} is {p.dtype}: fp32 or bf16 are supported")
@@ -684,7 +699,7 @@ class AdamW:
             e.n, e.param, e.exp_avg, e.exp_avg_sq = (p.numel(), p.data_ptr(),
                                                      self.exp_avg[i].data_ptr(),
                                                      self.exp_avg_sq[i].data_ptr())
-            e.master = None if self.master[i] is None else self.master[i].data_ptr()
+            e.master = _addr(self.master[i])
             if self.bits == 8:
                 n = (-(-p.numel() // ADAMW_BLOCK),)
                 for name, x in (("exp_avg_scale", self.exp_avg_scale[i]),
@@ -692,6 +707,14 @@ class AdamW:
                     check_tensor(x, n, torch.float32, f"{name}[{i}]", self.device)
                     setattr(e, name, x.data_ptr())
             e.param_dtype, e.state_bits = _ADAMW_DTYPES[p.dtype], self.bits
+        # views of the two members that every step sets, all tensors at once
+        self._grad_ptrs = np.ndarray((n_params,), np.uint64, self._batch, MoeAdamWTensor.grad.offset,
+                                     (ctypes.sizeof(MoeAdamWTensor),))
+        self._grad_types = np.ndarray((n_params,), np.int32, self._batch,
+                                      MoeAdamWTensor.grad_dtype.offset,
+                                      (ctypes.sizeof(MoeAdamWTensor),))
+        self._shapes = [p.shape for p in self.params]
+        self._index = self.params[0].get_device()
 
     def step(self, grads, grad_scale: Optional[torch.Tensor] = None,
              found_inf: Optional[torch.Tensor] = None, step: Optional[torch.Tensor] = None,
@@ -704,13 +727,17 @@ class AdamW:
         grads = list(grads.values() if isinstance(grads, dict) else grads)
         if len(grads) != len(self.params):
             raise ValueError(f"{len(grads)} gradients for {len(self.params)} parameters")
-        for i, (g, p, e) in enumerate(zip(grads, self.params, self._batch)):
-            if g.dtype not in _ADAMW_DTYPES:
-                raise ValueError(f"gradient {i} is {g.dtype}: fp32 or bf16 are supported")
-            check_tensor(g, p.shape, g.dtype, f"gradient {i}", self.device)
-            e.grad, e.grad_dtype = g.data_ptr(), _ADAMW_DTYPES[g.dtype]
-        o = MoeAdamW(beta1=self.betas[0], beta2=self.betas[1], lr=self.lr, eps=self.eps,
-                     weight_decay=self.weight_decay, step=self.t + 1)
+        if ([g.shape for g in grads] != self._shapes
+                or not all([g.is_contiguous() and g.get_device() == self._index for g in grads])):
+            for i, (g, p) in enumerate(zip(grads, self.params)):  # which one
+                check_tensor(g, p.shape, g.dtype, f"gradient {i}", self.device)
+        types = [_ADAMW_DTYPES.get(g.dtype, -1) for g in grads]
+        if -1 in types:
+            raise ValueError(f"gradient {types.index(-1)} is {grads[types.index(-1)].dtype}: fp32 "
+                             "or bf16 are supported")
+        self._grad_ptrs[:] = [g.data_ptr() for g in grads]
+        self._grad_types[:] = types
+        o = MoeAdamW(self.betas[0], self.betas[1], self.lr, self.eps, self.weight_decay, self.t + 1)
         for name, t, dt in (("grad_scale", grad_scale, torch.float32),
                             ("found_inf", found_inf, torch.float32),
                             ("step_dev", step, torch.int64), ("lr_dev", lr, torch.float32)):
@@ -719,9 +746,10 @@ class AdamW:
                     raise ValueError(f"{name} must hold one value")
                 check_tensor(t, t.shape, dt, name, self.device)
                 setattr(o, name, t.data_ptr())
-        with torch.cuda.device(self.device):
-            _check(self._lib.moe_adamw_step(self._batch, len(self.params), ctypes.byref(o),
-                                            _stream()), "moe_adamw_step")
+        st = _on_device(self._index, self._lib.moe_adamw_step, self._batch, len(self.params),
+                        ctypes.byref(o))
+        if st:
+            _check(st, "moe_adamw_step")
         self.t += 1
 
     def state_dict(self) -> dict:

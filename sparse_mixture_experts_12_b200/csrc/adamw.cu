@@ -13,6 +13,8 @@
 #include <cuda_fp8.h>
 #include <math.h>
 
+#include <type_traits>
+
 #include "api.cuh"
 
 namespace moe {
@@ -41,69 +43,76 @@ struct Batch {
   const float *lr_dev, *grad_scale, *found_inf;
 };
 
-__device__ __forceinline__ void load8(const float *p, float (&f)[8]) {
-  const float4 a = *reinterpret_cast<const float4 *>(p), b = *reinterpret_cast<const float4 *>(p + 4);
-  f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
-  f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
-}
-__device__ __forceinline__ void load8(const __nv_bfloat16 *p, float (&f)[8]) {
-  unpack16(*reinterpret_cast<const uint4 *>(p), f);
-}
+// Eight elements as they lie in memory: raw(p) of any of the types, values by get()
+template <typename T>
+struct Raw8 {
+  static constexpr int kWords = 8 * (int)sizeof(T) / 4;
+  uint32_t u[kWords];
+  __device__ __forceinline__ void load(const T *p, int n) {
+    if (n >= 8) {
+      if constexpr (kWords == 2) {
+        const uint2 q = __ldcs(reinterpret_cast<const uint2 *>(p));
+        u[0] = q.x; u[1] = q.y;
+      } else {
+#pragma unroll
+        for (int i = 0; i < kWords; i += 4) {
+          const uint4 q = __ldcs(reinterpret_cast<const uint4 *>(p) + i / 4);
+          u[i] = q.x; u[i + 1] = q.y; u[i + 2] = q.z; u[i + 3] = q.w;
+        }
+      }
+      return;
+    }
+    // a tensor's end
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) {
+      uint32_t w = 0;
+      constexpr int per = 4 / (int)sizeof(T);
+#pragma unroll
+      for (int j = 0; j < per; ++j) {
+        const int e = i * per + j;
+        if (e < n) w |= bits(p[e]) << (8 * (int)sizeof(T) * j);
+      }
+      u[i] = w;
+    }
+  }
+  static __device__ __forceinline__ uint32_t bits(float v) { return __float_as_uint(v); }
+  static __device__ __forceinline__ uint32_t bits(__nv_bfloat16 v) { return __bfloat16_as_ushort(v); }
+  static __device__ __forceinline__ uint32_t bits(uint8_t v) { return v; }
+  __device__ __forceinline__ void get(float (&f)[8]) const {
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) {
+      if constexpr (sizeof(T) == 4) {
+        f[i] = __uint_as_float(u[i]);
+        f[i + 1] = __uint_as_float(u[i + 1]);
+      } else if constexpr (sizeof(T) == 2) {
+        f[i] = __uint_as_float(u[i / 2] << 16);
+        f[i + 1] = __uint_as_float(u[i / 2] & 0xffff0000u);
+      } else {  // e4m3: exact in half precision
+        const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(
+            (__nv_fp8x2_storage_t)(u[i / 4] >> (8 * (i & 2))), __NV_E4M3);
+        const float2 q = __half22float2(__half2(h));
+        f[i] = q.x;
+        f[i + 1] = q.y;
+      }
+    }
+  }
+};
 __device__ __forceinline__ void store8(float *p, const float (&f)[8]) {
-  reinterpret_cast<float4 *>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
-  reinterpret_cast<float4 *>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
+  __stcs(reinterpret_cast<float4 *>(p), make_float4(f[0], f[1], f[2], f[3]));
+  __stcs(reinterpret_cast<float4 *>(p) + 1, make_float4(f[4], f[5], f[6], f[7]));
 }
 __device__ __forceinline__ void store8(__nv_bfloat16 *p, const float (&f)[8]) {
   *reinterpret_cast<uint4 *>(p) = pack16(f);
 }
-// n < 8 elements of a tensor's end
 template <typename T>
-__device__ __forceinline__ void load_n(const T *p, int n, float (&f)[8]) {
-#pragma unroll
-  for (int i = 0; i < 8; ++i) f[i] = i < n ? Elem<T>::to_f(p[i]) : 0.f;
-}
-template <typename T>
-__device__ __forceinline__ void store_n(T *p, int n, const float (&f)[8]) {
+__device__ __forceinline__ void store_any(T *p, int n, const float (&f)[8]) {
+  if (n >= 8) {
+    store8(p, f);
+    return;
+  }
 #pragma unroll
   for (int i = 0; i < 8; ++i)
     if (i < n) p[i] = Elem<T>::from_f(f[i]);
-}
-template <typename T>
-__device__ __forceinline__ void load_any(const T *p, int n, float (&f)[8]) {
-  if (n >= 8) load8(p, f);
-  else load_n(p, n, f);
-}
-template <typename T>
-__device__ __forceinline__ void store_any(T *p, int n, const float (&f)[8]) {
-  if (n >= 8) store8(p, f);
-  else store_n(p, n, f);
-}
-__device__ __forceinline__ void load_codes(const uint8_t *p, int n, float scale, float (&f)[8]) {
-  uint8_t c[8];
-  if (n >= 8) {
-    *reinterpret_cast<uint2 *>(c) = *reinterpret_cast<const uint2 *>(p);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) c[i] = i < n ? p[i] : 0;
-  }
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    __nv_fp8_e4m3 q;
-    q.__x = c[i];
-    f[i] = (float)q * scale;
-  }
-}
-__device__ __forceinline__ void store_codes(uint8_t *p, int n, const float (&f)[8]) {
-  uint8_t c[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) c[i] = __nv_fp8_e4m3(f[i]).__x;  // nearest even, saturating
-  if (n >= 8) {
-    *reinterpret_cast<uint2 *>(p) = *reinterpret_cast<const uint2 *>(c);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (i < n) p[i] = c[i];
-  }
 }
 // A block's (a warp's 256 elements) codes and scale
 template <bool ROOT>
@@ -112,74 +121,110 @@ __device__ __forceinline__ void quantise(uint8_t *codes, float *scale, int n, fl
 #pragma unroll
   for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(f[i]));
   top = warp_max(top);
-  const float up = kE4M3Max / top;
+  const float up = __fmul_rn(__frcp_rn(top), kE4M3Max);
+  uint32_t c[2] = {0, 0};
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float y = f[i] * up;
-    f[i] = (ROOT && f[i] > 0.f) ? fmaxf(y, kE4M3Tiny) : y;
+  for (int i = 0; i < 8; i += 2) {
+    float2 y = make_float2(__fmul_rn(f[i], up), __fmul_rn(f[i + 1], up));
+    if (ROOT) {
+      y.x = f[i] > 0.f ? fmaxf(y.x, kE4M3Tiny) : y.x;
+      y.y = f[i + 1] > 0.f ? fmaxf(y.y, kE4M3Tiny) : y.y;
+    }
+    // nearest even, saturating
+    c[i / 4] |= (uint32_t)__nv_cvt_float2_to_fp8x2(y, __NV_SATFINITE, __NV_E4M3) << (8 * (i & 2));
   }
-  store_codes(codes, n, f);
-  if ((threadIdx.x & 31) == 0 && n > 0) *scale = top / kE4M3Max;
+  if (n >= 8) {
+    *reinterpret_cast<uint2 *>(codes) = make_uint2(c[0], c[1]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < n) codes[i] = (uint8_t)(c[i / 4] >> (8 * (i & 3)));
+  }
+  if ((threadIdx.x & 31) == 0 && n > 0) *scale = __fmul_rn(top, 1.f / kE4M3Max);
 }
 
 struct Step {
   float b1, b2, e1, e2, keep, size, root2, eps, gs;
-  // e1 = 1 - b1, e2 = 1 - b2; keep = 1 - lr wd; size = lr / c1; root2 = sqrt(c2)
+  // e1 = 1 - b1, e2 = 1 - b2; keep = 1 - lr wd; size = lr / c1; root2 = 1 / sqrt(c2)
 };
 
-// n <= 8 elements at element i of the tensor; with 8-bit states the whole warp calls
-// it together (lanes past the end with n <= 0)
+// What a lane reads for 8 elements at element i of the tensor (n <= 8 of them exist; none
+// or less: nothing)
 template <typename P, typename G, bool Q>
-__device__ __forceinline__ void update(const moe_adamw_tensor_t &t, size_t i, int n,
-                                       const Step &s) {
-  float p[8], g[8], m[8], v[8];
-  float *w32 = t.master ? t.master + i : nullptr;
-  P *pw = static_cast<P *>(t.param) + i;
-  if (!Q && n <= 0) return;
-  load_any(static_cast<const G *>(t.grad) + i, n, g);
-  if (w32) load_any(w32, n, p);
-  else load_any(pw, n, p);
-  const size_t blk = i / kQBlock;
-  if (Q) {
-    load_codes(static_cast<const uint8_t *>(t.exp_avg) + i, n, n > 0 ? t.exp_avg_scale[blk] : 0.f, m);
-    load_codes(static_cast<const uint8_t *>(t.exp_avg_sq) + i, n,
-               n > 0 ? t.exp_avg_sq_scale[blk] : 0.f, v);
+struct Lane {
+  using S = typename std::conditional<Q, uint8_t, float>::type;
+  Raw8<P> p;
+  Raw8<float> w;
+  Raw8<G> g;
+  Raw8<S> m, v;
+  float ms, vs;
+  __device__ __forceinline__ void load(const moe_adamw_tensor_t &t, size_t i, int n) {
+    g.load(static_cast<const G *>(t.grad) + i, n);
+    if (sizeof(P) == 2 && t.master) w.load(t.master + i, n);
+    else p.load(static_cast<const P *>(t.param) + i, n);
+    m.load(static_cast<const S *>(t.exp_avg) + i, n);
+    v.load(static_cast<const S *>(t.exp_avg_sq) + i, n);
+    if (Q) {
+      ms = n > 0 ? t.exp_avg_scale[i / kQBlock] : 0.f;
+      vs = n > 0 ? t.exp_avg_sq_scale[i / kQBlock] : 0.f;
+    }
+  }
+  // The moments' sums are rounded product by product: a contraction that differs from one
+  // build or element to the next would move 8-bit codes that lie at a border.
+  __device__ __forceinline__ void update(const moe_adamw_tensor_t &t, size_t i, int n,
+                                         const Step &s) {
+    const bool copy = sizeof(P) == 2 && t.master;
+    float pf[8], gf[8], mf[8], vf[8], r[8];
+    g.get(gf);
+    m.get(mf);
+    v.get(vf);
+    if (copy) w.get(pf);
+    else p.get(pf);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] *= v[j];
-  } else {
-    load_any(static_cast<const float *>(t.exp_avg) + i, n, m);
-    load_any(static_cast<const float *>(t.exp_avg_sq) + i, n, v);
+    for (int j = 0; j < 8; ++j) {
+      if (Q) {
+        mf[j] = __fmul_rn(mf[j], ms);
+        vf[j] = __fmul_rn(vf[j], vs);
+        vf[j] = __fmul_rn(vf[j], vf[j]);
+      }
+      const float gr = __fmul_rn(gf[j], s.gs);
+      mf[j] = __fadd_rn(__fmul_rn(s.b1, mf[j]), __fmul_rn(s.e1, gr));
+      vf[j] = __fadd_rn(__fmul_rn(s.b2, vf[j]), __fmul_rn(__fmul_rn(s.e2, gr), gr));
+      r[j] = __fsqrt_rn(vf[j]);
+      // a quotient good to two units: far below what a step moves a weight
+      pf[j] = fmaf(pf[j], s.keep, -s.size * __fdividef(mf[j], fmaf(r[j], s.root2, s.eps)));
+    }
+    if (copy) store_any(t.master + i, n, pf);
+    store_any(static_cast<P *>(t.param) + i, n, pf);
+    if constexpr (Q) {
+      quantise<false>(static_cast<uint8_t *>(t.exp_avg) + i, t.exp_avg_scale + i / kQBlock, n, mf);
+      quantise<true>(static_cast<uint8_t *>(t.exp_avg_sq) + i, t.exp_avg_sq_scale + i / kQBlock, n,
+                     r);
+    } else {
+      store_any(static_cast<float *>(t.exp_avg) + i, n, mf);
+      store_any(static_cast<float *>(t.exp_avg_sq) + i, n, vf);
+    }
   }
-  float r[8];
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const float gr = g[j] * s.gs;
-    m[j] = fmaf(s.b1, m[j], s.e1 * gr);
-    v[j] = fmaf(s.b2, v[j], s.e2 * gr * gr);
-    r[j] = sqrtf(v[j]);
-    p[j] = fmaf(p[j], s.keep, -s.size * (m[j] / (r[j] / s.root2 + s.eps)));
-  }
-  if (w32) store_any(w32, n, p);
-  store_any(pw, n, p);
-  if (Q) {
-    quantise<false>(static_cast<uint8_t *>(t.exp_avg) + i, t.exp_avg_scale + blk, n, m);
-    quantise<true>(static_cast<uint8_t *>(t.exp_avg_sq) + i, t.exp_avg_sq_scale + blk, n, r);
-  } else {
-    store_any(static_cast<float *>(t.exp_avg) + i, n, m);
-    store_any(static_cast<float *>(t.exp_avg_sq) + i, n, v);
-  }
-}
+};
 
+// The chunk's steps: all are requested before the first is worked on. With 8-bit states a
+// warp stays together (its 256 elements share a scale); a warp past the end leaves.
 template <typename P, typename G, bool Q>
 __device__ __forceinline__ void chunk(const moe_adamw_tensor_t &t, size_t base, const Step &s) {
+  Lane<P, G, Q> lane[kSteps];
+  size_t at[kSteps];
+  int n[kSteps];
 #pragma unroll
   for (int j = 0; j < kSteps; ++j) {
-    const size_t i = base + (size_t)j * kThreads * kVec + (size_t)threadIdx.x * kVec;
-    const long long left = (long long)t.n - (long long)i;
-    const int n = left >= 8 ? 8 : (int)(left > 0 ? left : 0);
-    // a whole warp past the end has nothing to do
-    if ((long long)t.n <= (long long)(i - (threadIdx.x & 31) * kVec)) return;
-    update<P, G, Q>(t, i, n, s);
+    at[j] = base + (size_t)j * kThreads * kVec + (size_t)threadIdx.x * kVec;
+    const long long left = (long long)t.n - (long long)at[j];
+    n[j] = left >= 8 ? 8 : (int)(left > 0 ? left : 0);
+    lane[j].load(t, at[j], n[j]);
+  }
+#pragma unroll
+  for (int j = 0; j < kSteps; ++j) {
+    if (Q ? (long long)t.n <= (long long)(at[j] - (threadIdx.x & 31) * kVec) : n[j] == 0) return;
+    lane[j].update(t, at[j], n[j], s);
   }
 }
 
@@ -204,7 +249,7 @@ __global__ void __launch_bounds__(kThreads) k_adamw(const __grid_constant__ Batc
     sh.e2 = (float)(1.0 - b.beta2_d);
     sh.keep = (float)(1.0 - lr * (double)b.decay);
     sh.size = (float)(lr / c1);
-    sh.root2 = (float)sqrt(c2);
+    sh.root2 = (float)(1.0 / sqrt(c2));
     sh.eps = b.eps;
     sh.gs = b.grad_scale ? *b.grad_scale : 1.f;
   }
