@@ -15,7 +15,7 @@
 //
 // A CTA pair's roles, barriers and bounded waits are those of the forward's GEMM
 // (ffn_tc.cu): warp 0 of each CTA loads its operand halves, warp 1 of the leader issues
-// the MMAs, warps 4-19 drain tensor memory; a wait that runs out records
+// the MMAs, warps 4.. drain tensor memory; a wait that runs out records
 // MOE_DEVERR_WAIT_TIMEOUT and ends both CTAs.
 #include <algorithm>
 #include <mutex>
@@ -30,33 +30,25 @@ namespace {
 using namespace tc;
 
 constexpr int kPairM = 2 * kRowTile;
-constexpr int kStages = 5;
 constexpr int kOperand = kRowTile * kBlockK * 2;  // 16 KB: a CTA's half of a 256-wide operand
-constexpr int kStageBytes = 2 * kOperand;
 constexpr int kMnBlock = kBlockK * kBlockK * 2;   // 8 KB: 64 K rows x 64 contiguous elements
-// Sixteen epilogue warps, four to a lane quarter of tensor memory: the activations'
-// derivatives take some 25 instructions an element in long dependent chains, and the
-// output stores wait for shared memory to be read; eight warps did not keep up.
-constexpr int kEpiWarps = 16;
-constexpr int kThreads = 128 + 32 * kEpiWarps;
-constexpr int kStageOut = 4096;  // output staging of an epilogue warp
 constexpr int kTmemCols = 512;
+constexpr int kMaxStages = 8;
+constexpr int kStageOutBytes = kStoreBox * kStoreBox * 2;  // 2 KB: a 32 x 32 output chunk
 constexpr uint64_t kDrainNs = 50000000ull;
 
 struct Ctl {
-  uint64_t full[kStages];   // leader: both CTAs' copies of the stage landed
-  uint64_t empty[kStages];  // each CTA: the pair's MMAs are done with the stage
-  uint64_t tfull[2];        // each CTA: the tile's accumulators are complete
-  uint64_t tempty[2];       // leader: both epilogues have drained them
-  uint64_t drain;
+  uint64_t full[kMaxStages];   // leader: both CTAs' copies of the stage landed
+  uint64_t empty[kMaxStages];  // each CTA: the pair's MMAs are done with the stage
+  uint64_t tfull[2];           // each CTA: the tile's accumulators are complete
+  uint64_t tempty[2];          // leader: both epilogues have drained them
+  uint64_t drain[2];
   uint32_t tmem_base;
   int abort_flag;
   int pre[kMaxExperts + 1];  // prefix of the experts' 256-row tiles
 };
-constexpr size_t kRing = (size_t)kStages * kStageBytes;
-constexpr size_t kSmemBytes = kRing + (size_t)kEpiWarps * kStageOut + sizeof(Ctl) + 1024;
 
-// what both kernels do before their roles split up; returns the tensor memory's base
+// what both kernels do before their roles split up
 struct Setup {
   uint8_t *smem;
   Ctl *ctl;
@@ -64,24 +56,27 @@ struct Setup {
   int rank, c0, cstep;
 };
 
-__device__ __forceinline__ Setup set_up(uint8_t *raw, const int32_t *poff, int G) {
+// `bytes` of operand stages and output staging come before the control block; `issuers`
+// threads complete a tile's accumulators, `drainers` threads of both CTAs drain them.
+__device__ __forceinline__ Setup set_up(uint8_t *raw, size_t bytes, int issuers, int drainers,
+                                        const int32_t *poff, int G) {
   Setup s;
   s.smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) &
                                        ~static_cast<uintptr_t>(1023));
-  s.ctl = reinterpret_cast<Ctl *>(s.smem + kRing + kEpiWarps * kStageOut);
+  s.ctl = reinterpret_cast<Ctl *>(s.smem + bytes);
   Ctl *ctl = s.ctl;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   s.rank = (int)cluster_ctarank();
   if (tid == 0) {
-    for (int i = 0; i < kStages; ++i) {
+    for (int i = 0; i < kMaxStages; ++i) {
       mbar_init(&ctl->full[i], 1);
       mbar_init(&ctl->empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&ctl->tfull[i], 1);
-      mbar_init(&ctl->tempty[i], 2 * kEpiWarps * 32);
+      mbar_init(&ctl->tfull[i], issuers);
+      mbar_init(&ctl->tempty[i], drainers);
+      mbar_init(&ctl->drain[i], 1);
     }
-    mbar_init(&ctl->drain, 1);
     ctl->abort_flag = 0;
     fence_mbar_init();
   }
@@ -123,29 +118,58 @@ __device__ __forceinline__ Setup set_up(uint8_t *raw, const int32_t *poff, int G
 __device__ __forceinline__ bool wait_on(const Setup &s, uint64_t *bar, uint32_t parity,
                                         int32_t *err, int site, bool honour_abort = true,
                                         uint64_t limit_ns = kWaitLimitNs) {
+  if (mbar_try_wait(bar, parity)) return true;
   return wait_mbar(bar, parity, &s.ctl->abort_flag, s.peer_abort, err, site, honour_abort,
                    limit_ns);
 }
 
-// the ring's position, and (producer) which stages were filled and when
+// A ring of N operand stages of BYTES each, from stage FIRST of the barriers on; producer
+// and MMA issuer hold one each and walk through it in step.
+template <int N, int FIRST, int BYTES>
 struct Ring {
+  uint8_t *base;
   int stage = 0;
   uint32_t phase = 0, issued = 0, last_phase = 0;
-  __device__ __forceinline__ void mark() {
+  __device__ __forceinline__ explicit Ring(uint8_t *b) : base(b) {}
+  // producer: the next stage, free to be filled with `bytes` by each CTA, or nullptr
+  __device__ __forceinline__ uint8_t *acquire(const Setup &s, int bytes, int32_t *err, int site) {
+    if (!wait_on(s, &s.ctl->empty[FIRST + stage], phase ^ 1u, err, site)) return nullptr;
+    if (s.rank == 0) mbar_expect_tx(&s.ctl->full[FIRST + stage], 2 * bytes);
     issued |= 1u << stage;
     last_phase = (last_phase & ~(1u << stage)) | (phase << stage);
+    return base + (size_t)stage * BYTES;
+  }
+  // ... its barrier (full0: the leader's first)
+  __device__ __forceinline__ uint32_t bar(uint32_t full0) const {
+    return full0 + (uint32_t)((FIRST + stage) * sizeof(uint64_t));
+  }
+  // issuer: the next stage, filled
+  __device__ __forceinline__ bool filled(const Setup &s, int32_t *err, int site) const {
+    const bool ok = wait_on(s, &s.ctl->full[FIRST + stage], phase, err, site);
+    tc_fence_after();
+    return ok;
+  }
+  __device__ __forceinline__ uint32_t addr() const { return smem_u32(base) + stage * BYTES; }
+  // ... handed back once the MMAs issued so far are done
+  __device__ __forceinline__ void release(const Setup &s) const {
+    umma_commit_pair_both(&s.ctl->empty[FIRST + stage]);
   }
   __device__ __forceinline__ void next() {
-    if (++stage == kStages) { stage = 0; phase ^= 1u; }
+    if (++stage == N) { stage = 0; phase ^= 1u; }
+  }
+  // producer, at its end: the MMAs have released every stage this CTA filled
+  __device__ __forceinline__ void drain(const Setup &s, bool ok) const {
+    for (int i = 0; i < N; ++i)
+      if (issued & (1u << i))
+        wait_on(s, &s.ctl->empty[FIRST + i], (last_phase >> i) & 1u, nullptr, 0, false,
+                ok ? kWaitLimitNs : kDrainNs);
   }
 };
 
-// the pair's MMAs have released every stage this CTA filled
-__device__ __forceinline__ void drain_ring(const Setup &s, const Ring &r, bool ok) {
-  for (int i = 0; i < kStages; ++i)
-    if (r.issued & (1u << i))
-      wait_on(s, &s.ctl->empty[i], (r.last_phase >> i) & 1u, nullptr, 0, false,
-              ok ? kWaitLimitNs : kDrainNs);
+// issuer, at its end: the MMAs in flight retire before tensor memory is released
+__device__ __forceinline__ void retire(const Setup &s, uint64_t *bar) {
+  umma_commit_pair_own(bar);
+  wait_on(s, bar, 0, nullptr, 0, false, kDrainNs);
 }
 
 __device__ __forceinline__ void tear_down(const Setup &s) {
@@ -166,33 +190,26 @@ __device__ __forceinline__ void load_mn(const CUtensorMap *map, uint32_t bar, ui
   tma_load_2d_pair(map, bar, dst + kMnBlock, c + kBlockK, row);
 }
 
-// The output path of an epilogue warp: 4 KB of shared memory that TMA stores read, as two
-// 32 x 32 chunks in turn or one of 32 x 64. One lane issues the stores and, before a
-// buffer is written again, waits until they have read it.
-struct Stage {
-  uint8_t *buf;
-  int turn = 0;
-  // 32 rows (a lane each) x 32 columns: the lane's 64 bytes, 16-byte pieces swizzled
-  __device__ __forceinline__ void put32(const CUtensorMap *map, const uint32_t *p, int col0,
-                                        int row0) {
-    const int lane = threadIdx.x & 31;
-    if (lane == 0) bulk_wait_read<1>();
-    __syncwarp();
-    uint8_t *b = buf + turn * (kStageOut / 2);
-    uint4 *row = reinterpret_cast<uint4 *>(b + lane * 64);
-    const int sw = (lane >> 1) & 3;
+// One 32-row x 32-column chunk (a lane's row of 64 bytes) through the warp's 2 KB of
+// shared memory: 16-byte pieces swizzled, one TMA store. The buffer is written again once
+// the store before has read it.
+__device__ __forceinline__ void put32(uint8_t *buf, const CUtensorMap *map, const uint32_t *p,
+                                      int col0, int row0) {
+  const int lane = threadIdx.x & 31;
+  if (lane == 0) bulk_wait_read_all();
+  __syncwarp();
+  uint4 *row = reinterpret_cast<uint4 *>(buf + lane * 64);
+  const int sw = (lane >> 1) & 3;
 #pragma unroll
-    for (int q = 0; q < 4; ++q)
-      row[q ^ sw] = make_uint4(p[4 * q], p[4 * q + 1], p[4 * q + 2], p[4 * q + 3]);
-    fence_proxy_async_smem();
-    __syncwarp();
-    if (lane == 0) {
-      tma_store_2d(map, b, col0, row0);
-      bulk_commit();
-    }
-    turn ^= 1;
+  for (int q = 0; q < 4; ++q)
+    row[q ^ sw] = make_uint4(p[4 * q], p[4 * q + 1], p[4 * q + 2], p[4 * q + 3]);
+  fence_proxy_async_smem();
+  __syncwarp();
+  if (lane == 0) {
+    tma_store_2d(map, buf, col0, row0);
+    bulk_commit();
   }
-};
+}
 
 // ================================================================= activations
 struct ActArgs {
@@ -238,217 +255,237 @@ __device__ __forceinline__ void gelu_and_slope(float v, float &h, float &s) {
   s = fmaf(v * 0.39894228040143268f, e, c);
 }
 
-// One tile: 256 rows x 128 columns of F (32 to an epilogue warp). Tensor memory: a | u at columns 0-255 (SwiGLU) or
-// a at 0 / 128 (alternating, MLP); q at 256 / 384 (alternating). With SwiGLU the a | u
-// region is single: the next tile's first kLead slices of q run while it is drained.
+// One tile: 256 rows x 128 columns of F. Tensor memory: a | u at columns 0-255 (SwiGLU) or
+// a at 0 / 128 (alternating, MLP); q at 256 / 384 (alternating). q and a (| u) have a ring,
+// a loading and an issuing thread of their own: one thread for both spent more time on
+// issuing (about 400 clocks a slice and thread) than the MMAs took, and q of the next tile
+// runs while the epilogue drains the one a | u region of SwiGLU.
 constexpr int kTileN = 128;
-constexpr int kLead = 24;
+template <bool GLU>
+struct ActCfg {
+  static constexpr int kEpiWarps = GLU ? 8 : 16;  // MLP tiles are shorter, their epilogue longer
+  static constexpr int kThreads = 128 + 32 * kEpiWarps;
+  static constexpr int kBytesQ = kOperand + kMnBlock;
+  static constexpr int kBytesA = GLU ? 2 * kOperand : kOperand + kMnBlock;
+  static constexpr int kStagesQ = GLU ? 3 : 4, kStagesA = 4;
+  static constexpr size_t kRings = (size_t)kStagesQ * kBytesQ + (size_t)kStagesA * kBytesA;
+  static constexpr size_t kBytes = kRings + (size_t)kEpiWarps * kStageOutBytes;
+  static constexpr size_t kSmem = kBytes + sizeof(Ctl) + 1024;
+};
 
 template <bool GLU>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(ActCfg<GLU>::kThreads, 1)
 k_act_grad(const __grid_constant__ ActMaps maps, ActArgs a) {
+  using C = ActCfg<GLU>;
+  using RingQ = Ring<C::kStagesQ, 0, C::kBytesQ>;
+  using RingA = Ring<C::kStagesA, C::kStagesQ, C::kBytesA>;
   extern __shared__ uint8_t smem_raw[];
-  const Setup s = set_up(smem_raw, a.poff, a.G);
+  const Setup s = set_up(smem_raw, C::kBytes, 2, 2 * C::kEpiWarps * 32, a.poff, a.G);
   Ctl *ctl = s.ctl;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int total = ctl->pre[a.G] * a.n_tiles;
   const int nkb = ceil_div(a.d, kBlockK);
-  const int lead = GLU ? min(kLead, nkb) : 0;
-  constexpr int kBytesQ = kOperand + kMnBlock;
-  constexpr int kBytesA = GLU ? 2 * kOperand : kOperand + kMnBlock;
+  uint8_t *const ring_q = s.smem, *const ring_a = s.smem + C::kStagesQ * C::kBytesQ;
 
   if (warp == 0 && lane == 0) {
-    // ------------------------------------------------------------ TMA producer
-    prefetch_map(&maps.x);
+    // ----------------------------------------------- TMA producer of dy and W2
     prefetch_map(&maps.dy);
-    prefetch_map(&maps.w1);
     prefetch_map(&maps.w2);
-    if (GLU) prefetch_map(&maps.w3);
     const uint32_t full0 = mapa_rank(smem_u32(&ctl->full[0]), 0);
-    Ring ring;
+    RingQ ring(ring_q);
     bool ok = true;
     for (int t = s.c0; ok && t < total; t += s.cstep) {
       int g, n, m;
       decode_tile(t, ctl->pre, a.G, a.n_tiles, g, n, m);
       const int arow = a.poff[g] + m * kPairM + s.rank * kRowTile;
-      const int n0 = n * kTileN;
-      auto stage_for = [&](int bytes) -> uint8_t * {
-        if (!wait_on(s, &ctl->empty[ring.stage], ring.phase ^ 1u, a.err, 21)) return nullptr;
-        if (s.rank == 0) mbar_expect_tx(&ctl->full[ring.stage], 2 * bytes);
-        return s.smem + (size_t)ring.stage * kStageBytes;
-      };
-      for (int i = 0; i < nkb + lead; ++i) {
-        if (i < nkb) {
-          uint8_t *st = stage_for(kBytesQ);
-          if (!(ok = st != nullptr)) break;
-          const uint32_t bar = full0 + (uint32_t)(ring.stage * sizeof(uint64_t));
-          tma_load_2d_pair(&maps.dy, bar, st, i * kBlockK, arow);
-          tma_load_2d_pair(&maps.w2, bar, st + kOperand, n0 + s.rank * kBlockK,
-                           g * a.d + i * kBlockK);
-          ring.mark();
-          ring.next();
-        }
-        if (i >= lead) {
-          uint8_t *st = stage_for(kBytesA);
-          if (!(ok = st != nullptr)) break;
-          const uint32_t bar = full0 + (uint32_t)(ring.stage * sizeof(uint64_t));
-          const int k0 = (i - lead) * kBlockK;
-          tma_load_2d_pair(&maps.x, bar, st, k0, arow);
-          if (GLU)
-            tma_load_2d_pair(s.rank ? &maps.w3 : &maps.w1, bar, st + kOperand, k0, g * a.F + n0);
-          else
-            tma_load_2d_pair(&maps.w1, bar, st + kOperand, k0, g * a.F + n0 + s.rank * kBlockK);
-          ring.mark();
-          ring.next();
-        }
+      const int col = n * kTileN + s.rank * kBlockK, brow = g * a.d;
+      for (int i = 0; i < nkb; ++i) {
+        uint8_t *st = ring.acquire(s, C::kBytesQ, a.err, 21);
+        if (!(ok = st != nullptr)) break;
+        const uint32_t bar = ring.bar(full0);
+        tma_load_2d_pair(&maps.dy, bar, st, i * kBlockK, arow);
+        tma_load_2d_pair(&maps.w2, bar, st + kOperand, col, brow + i * kBlockK);
+        ring.next();
       }
     }
-    drain_ring(s, ring, ok);
+    ring.drain(s, ok);
+  } else if (warp == 3 && lane == 0) {
+    // ----------------------------------------- TMA producer of x and W1 (| W3)
+    const CUtensorMap *w = GLU && s.rank ? &maps.w3 : &maps.w1;
+    prefetch_map(&maps.x);
+    prefetch_map(w);
+    const uint32_t full0 = mapa_rank(smem_u32(&ctl->full[0]), 0);
+    RingA ring(ring_a);
+    bool ok = true;
+    for (int t = s.c0; ok && t < total; t += s.cstep) {
+      int g, n, m;
+      decode_tile(t, ctl->pre, a.G, a.n_tiles, g, n, m);
+      const int arow = a.poff[g] + m * kPairM + s.rank * kRowTile;
+      const int brow = g * a.F + n * kTileN + (GLU ? 0 : s.rank * kBlockK);
+      for (int i = 0; i < nkb; ++i) {
+        uint8_t *st = ring.acquire(s, C::kBytesA, a.err, 21);
+        if (!(ok = st != nullptr)) break;
+        const uint32_t bar = ring.bar(full0);
+        tma_load_2d_pair(&maps.x, bar, st, i * kBlockK, arow);
+        tma_load_2d_pair(w, bar, st + kOperand, i * kBlockK, brow);
+        ring.next();
+      }
+    }
+    ring.drain(s, ok);
   } else if (warp == 1 && lane == 0 && s.rank == 0) {
-    // --------------------------------------------------------------- MMA issuer
-    constexpr uint32_t idesc_q = make_idesc(kPairM, kTileN) | kIdescMnB;
-    constexpr uint32_t idesc_a = make_idesc(kPairM, GLU ? 2 * kTileN : kTileN);
-    Ring ring;
+    // ------------------------------------------------------------ MMAs of q
+    constexpr uint32_t idesc = make_idesc(kPairM, kTileN) | kIdescMnB;
+    RingQ ring(ring_q);
     bool ok = true, any = false;
     int it = 0;
     for (int t = s.c0; ok && t < total; t += s.cstep, ++it) {
       const int buf = it & 1;
-      const uint32_t dq = s.tmem + 256u + (uint32_t)(buf * kTileN);
-      const uint32_t da = s.tmem + (GLU ? 0u : (uint32_t)(buf * kTileN));
-      // tile it - 2, which used the same buffers, has been drained
+      const uint32_t acc = s.tmem + 256u + (uint32_t)(buf * kTileN);
+      // tile it - 2, which used the same buffer, has been drained
       if (!(ok = wait_on(s, &ctl->tempty[buf], ((it >> 1) & 1) ^ 1u, a.err, 22))) break;
       tc_fence_after();
-      for (int i = 0; i < nkb + lead; ++i) {
-        if (i < nkb) {
-          if (!(ok = wait_on(s, &ctl->full[ring.stage], ring.phase, a.err, 23))) break;
-          tc_fence_after();
-          const uint32_t sa = smem_u32(s.smem + (size_t)ring.stage * kStageBytes);
-          const uint64_t xa = sw128_desc(sa), xb = sw128_desc_mn(sa + kOperand, kMnBlock);
+      for (int i = 0; i < nkb; ++i) {
+        if (!(ok = ring.filled(s, a.err, 23))) break;
+        const uint64_t xa = sw128_desc(ring.addr());
+        const uint64_t xb = sw128_desc_mn(ring.addr() + kOperand, kMnBlock);
 #pragma unroll
-          for (int kk = 0; kk < kBlockK / 16; ++kk)
-            umma_bf16_pair(dq, xa + 2 * kk, xb + 128 * kk, idesc_q, (i | kk) != 0);
-          any = true;
-          umma_commit_pair_both(&ctl->empty[ring.stage]);
-          ring.next();
-        }
-        if (i >= lead) {
-          // the one a | u region: tile it - 1 has been drained
-          if (GLU && i == lead && it > 0 &&
-              !(ok = wait_on(s, &ctl->tempty[buf ^ 1], ((it - 1) >> 1) & 1, a.err, 22)))
-            break;
-          if (!(ok = wait_on(s, &ctl->full[ring.stage], ring.phase, a.err, 23))) break;
-          tc_fence_after();
-          const uint32_t sa = smem_u32(s.smem + (size_t)ring.stage * kStageBytes);
-          const uint64_t xa = sw128_desc(sa), xb = sw128_desc(sa + kOperand);
-#pragma unroll
-          for (int kk = 0; kk < kBlockK / 16; ++kk)
-            umma_bf16_pair(da, xa + 2 * kk, xb + 2 * kk, idesc_a, ((i - lead) | kk) != 0);
-          any = true;
-          umma_commit_pair_both(&ctl->empty[ring.stage]);
-          ring.next();
-        }
+        for (int kk = 0; kk < kBlockK / 16; ++kk)
+          umma_bf16_pair(acc, xa + 2 * kk, xb + 128 * kk, idesc, (i | kk) != 0);
+        any = true;
+        ring.release(s);
+        ring.next();
       }
-      if (!ok) break;
-      umma_commit_pair_both(&ctl->tfull[buf]);
+      if (ok) umma_commit_pair_both(&ctl->tfull[buf]);
     }
-    if (!ok && any) {  // retire the MMAs in flight before TMEM is released
-      umma_commit_pair_own(&ctl->drain);
-      wait_on(s, &ctl->drain, 0, nullptr, 0, false, kDrainNs);
+    if (!ok && any) retire(s, &ctl->drain[0]);
+  } else if (warp == 2 && lane == 0 && s.rank == 0) {
+    // ------------------------------------------------------- MMAs of a (| u)
+    constexpr uint32_t idesc = make_idesc(kPairM, GLU ? 2 * kTileN : kTileN);
+    RingA ring(ring_a);
+    bool ok = true, any = false;
+    int it = 0;
+    for (int t = s.c0; ok && t < total; t += s.cstep, ++it) {
+      const int buf = it & 1;
+      const uint32_t acc = s.tmem + (GLU ? 0u : (uint32_t)(buf * kTileN));
+      // SwiGLU has one a | u region: tile it - 1 has been drained
+      const int old = GLU ? it - 1 : it - 2;
+      if (old >= 0 && !(ok = wait_on(s, &ctl->tempty[old & 1], (old >> 1) & 1, a.err, 22))) break;
+      tc_fence_after();
+      for (int i = 0; i < nkb; ++i) {
+        if (!(ok = ring.filled(s, a.err, 23))) break;
+        const uint64_t xa = sw128_desc(ring.addr()), xb = sw128_desc(ring.addr() + kOperand);
+#pragma unroll
+        for (int kk = 0; kk < kBlockK / 16; ++kk)
+          umma_bf16_pair(acc, xa + 2 * kk, xb + 2 * kk, idesc, (i | kk) != 0);
+        any = true;
+        ring.release(s);
+        ring.next();
+      }
+      if (ok) umma_commit_pair_both(&ctl->tfull[buf]);
     }
+    if (!ok && any) retire(s, &ctl->drain[1]);
   } else if (warp >= 4) {
     // ----------------------------------------------------------------- epilogue
-    const int ew = warp & 3, part = (warp - 4) >> 2;  // lanes 32 ew.., columns 32 part..
+    const int ew = warp & 3, part = (warp - 4) >> 2;  // lanes 32 ew.., column chunks part..
+    constexpr int kParts = C::kEpiWarps / 4;
     const uint32_t tempty0 = mapa_rank(smem_u32(&ctl->tempty[0]), 0);
-    Stage out{s.smem + kRing + (warp - 4) * kStageOut};
+    uint8_t *stage = s.smem + C::kRings + (warp - 4) * kStageOutBytes;
     int it = 0;
     for (int t = s.c0; t < total; t += s.cstep, ++it) {
       int g, n, m;
       decode_tile(t, ctl->pre, a.G, a.n_tiles, g, n, m);
       const int buf = it & 1;
       const int lrow = m * kPairM + s.rank * kRowTile + ew * 32;  // the warp's first row
-      const int prow = a.poff[g] + lrow, col0 = n * kTileN + part * 32;
+      const int prow = a.poff[g] + lrow;
       // padded groups of 32 rows belong to the expert as a whole or not at all; F is a
       // multiple of 64
-      const bool mine = prow < a.poff[g + 1] && col0 < a.F;
+      const bool rows_mine = prow < a.poff[g + 1];
       const bool valid = lrow + lane < a.offsets[g + 1] - a.offsets[g];
-      const float w = (a.row_w && mine) ? a.row_w[prow + lane] : 1.f;
+      const float w = (a.row_w && rows_mine) ? a.row_w[prow + lane] : 1.f;
       bool ok = wait_on(s, &ctl->tfull[buf], (it >> 1) & 1, a.err, 24);
       __syncwarp();
       if (!__all_sync(0xffffffffu, ok)) break;
       tc_fence_after();
-      const uint32_t lane_base = s.tmem + ((uint32_t)(ew * 32) << 16) + (uint32_t)(part * 32);
-      const uint32_t tq = lane_base + 256u + (uint32_t)(buf * kTileN);
-      const uint32_t ta = lane_base + (GLU ? 0u : (uint32_t)(buf * kTileN));
-      float dot = 0.f;
-      uint32_t hp[16], gp[16], up[GLU ? 16 : 1];  // packed pairs of columns
-      if (mine) {
+#pragma unroll 1
+      for (int c = part; c < kTileN / 32; c += kParts) {
+        const int col0 = n * kTileN + c * 32;
+        const bool mine = rows_mine && col0 < a.F;
+        const uint32_t lane_base = s.tmem + ((uint32_t)(ew * 32) << 16) + (uint32_t)(c * 32);
+        const uint32_t tq = lane_base + 256u + (uint32_t)(buf * kTileN);
+        const uint32_t ta = lane_base + (GLU ? 0u : (uint32_t)(buf * kTileN));
+        float dot = 0.f;
+        uint32_t hp[16], gp[16], up[GLU ? 16 : 1];  // packed pairs of columns
+        if (mine) {
 #pragma unroll
-        for (int j2 = 0; j2 < 2; ++j2) {
-          uint32_t av[16], uv[GLU ? 16 : 1], qv[16];
-          tmem_ld16(ta + j2 * 16, av);
-          if constexpr (GLU) tmem_ld16(ta + kTileN + j2 * 16, uv);
-          tmem_ld16(tq + j2 * 16, qv);
-          float bias[GLU ? 1 : 16];
-          if constexpr (!GLU) {
+          for (int j2 = 0; j2 < 2; ++j2) {
+            uint32_t av[16], uv[GLU ? 16 : 1], qv[16];
+            tmem_ld16(ta + j2 * 16, av);
+            if constexpr (GLU) tmem_ld16(ta + kTileN + j2 * 16, uv);
+            tmem_ld16(tq + j2 * 16, qv);
+            float bias[GLU ? 1 : 16];
+            if constexpr (!GLU) {
 #pragma unroll
-            for (int j = 0; j < 16; j += 4) {  // the same for every lane
-              const float4 b = a.b1 ? __ldg(reinterpret_cast<const float4 *>(
-                                          a.b1 + (size_t)g * a.F + col0 + j2 * 16 + j))
-                                    : make_float4(0.f, 0.f, 0.f, 0.f);
-              bias[j] = b.x; bias[j + 1] = b.y; bias[j + 2] = b.z; bias[j + 3] = b.w;
-            }
-          }
-          tmem_ld_wait();
-          float da[16];
-#pragma unroll
-          for (int j = 0; j < 16; j += 2) {
-            float h[2], du[2];
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const float q = __uint_as_float(qv[j + i]);
-              float v = __uint_as_float(av[j + i]), x;
-              if constexpr (GLU) {
-                const float u = __uint_as_float(uv[j + i]);
-                const float sg = __fdividef(1.f, 1.f + __expf(-v));
-                const float si = v * sg;
-                h[i] = si * u;
-                du[i] = q * si;
-                x = q * u * fmaf(si, 1.f - sg, sg);
-              } else {
-                v += bias[j + i];
-                float sl;
-                if (a.act == MOE_ACT_RELU) {
-                  h[i] = fmaxf(v, 0.f);
-                  sl = v > 0.f ? 1.f : 0.f;
-                } else {
-                  gelu_and_slope(v, h[i], sl);
-                }
-                x = q * sl;
+              for (int j = 0; j < 16; j += 4) {  // the same for every lane
+                const float4 b = a.b1 ? __ldg(reinterpret_cast<const float4 *>(
+                                            a.b1 + (size_t)g * a.F + col0 + j2 * 16 + j))
+                                      : make_float4(0.f, 0.f, 0.f, 0.f);
+                bias[j] = b.x; bias[j + 1] = b.y; bias[j + 2] = b.z; bias[j + 3] = b.w;
               }
-              dot = fmaf(q, h[i], dot);
-              // rows past the expert's: zeros, whatever the weights hold
-              h[i] = valid ? w * h[i] : 0.f;
-              da[j + i] = valid ? w * x : 0.f;
-              if constexpr (GLU) du[i] = valid ? w * du[i] : 0.f;
             }
-            hp[j2 * 8 + j / 2] = pack_bf16x2(h[0], h[1]);
-            gp[j2 * 8 + j / 2] = pack_bf16x2(da[j], da[j + 1]);
-            if constexpr (GLU) up[j2 * 8 + j / 2] = pack_bf16x2(du[0], du[1]);
-          }
-          if (!GLU && a.col_part) {
-            const float v = column_sum16(da, lane);
-            if (lane < 16)
-              a.col_part[(size_t)(prow >> 5) * a.F + col0 + j2 * 16 + lane] = v;
+            tmem_ld_wait();
+            float da[16];
+#pragma unroll
+            for (int j = 0; j < 16; j += 2) {
+              float h[2], du[2];
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                const float q = __uint_as_float(qv[j + i]);
+                float v = __uint_as_float(av[j + i]), x;
+                if constexpr (GLU) {
+                  const float u = __uint_as_float(uv[j + i]);
+                  const float sg = __fdividef(1.f, 1.f + __expf(-v));
+                  const float si = v * sg;
+                  h[i] = si * u;
+                  du[i] = q * si;
+                  x = q * u * fmaf(si, 1.f - sg, sg);
+                } else {
+                  v += bias[j + i];
+                  float sl;
+                  if (a.act == MOE_ACT_RELU) {
+                    h[i] = fmaxf(v, 0.f);
+                    sl = v > 0.f ? 1.f : 0.f;
+                  } else {
+                    gelu_and_slope(v, h[i], sl);
+                  }
+                  x = q * sl;
+                }
+                dot = fmaf(q, h[i], dot);
+                // rows past the expert's: zeros, whatever the weights hold
+                h[i] = valid ? w * h[i] : 0.f;
+                da[j + i] = valid ? w * x : 0.f;
+                if constexpr (GLU) du[i] = valid ? w * du[i] : 0.f;
+              }
+              hp[j2 * 8 + j / 2] = pack_bf16x2(h[0], h[1]);
+              gp[j2 * 8 + j / 2] = pack_bf16x2(da[j], da[j + 1]);
+              if constexpr (GLU) up[j2 * 8 + j / 2] = pack_bf16x2(du[0], du[1]);
+            }
+            if (!GLU && a.col_part) {
+              const float v = column_sum16(da, lane);
+              if (lane < 16)
+                a.col_part[(size_t)(prow >> 5) * a.F + col0 + j2 * 16 + lane] = v;
+            }
           }
         }
-      }
-      tc_fence_before();
-      mbar_arrive_cluster(tempty0 + (uint32_t)(buf * sizeof(uint64_t)));
-      if (mine) {
-        out.put32(&maps.h, hp, col0, prow);
-        out.put32(&maps.dg, gp, col0, prow);
-        if constexpr (GLU) out.put32(&maps.du, up, col0, prow);
-        if (a.dot_part && valid) a.dot_part[(size_t)(col0 / 32) * a.rows + prow + lane] = dot;
+        if (c + kParts >= kTileN / 32) {  // the warp's last chunk is in registers
+          tc_fence_before();
+          mbar_arrive_cluster(tempty0 + (uint32_t)(buf * sizeof(uint64_t)));
+        }
+        if (mine) {
+          put32(stage, &maps.h, hp, col0, prow);
+          put32(stage, &maps.dg, gp, col0, prow);
+          if constexpr (GLU) put32(stage, &maps.du, up, col0, prow);
+          if (a.dot_part && valid) a.dot_part[(size_t)(col0 / 32) * a.rows + prow + lane] = dot;
+        }
       }
     }
     if (lane == 0) bulk_wait_all();  // this warp's output stores are done
@@ -474,12 +511,19 @@ struct GemmArgs {
 struct GemmMaps {
   CUtensorMap a[3], b[3], o[3];
 };
+constexpr int kGemmStages = 5, kGemmStageBytes = 2 * kOperand;
+constexpr int kGemmEpiWarps = 16, kGemmThreads = 128 + 32 * kGemmEpiWarps;
+constexpr int kStageOut = 4096;  // output staging of an epilogue warp
+constexpr size_t kGemmRing = (size_t)kGemmStages * kGemmStageBytes;
+constexpr size_t kGemmBytes = kGemmRing + (size_t)kGemmEpiWarps * kStageOut;
+constexpr size_t kGemmSmem = kGemmBytes + sizeof(Ctl) + 1024;
+using GemmRing = Ring<kGemmStages, 0, kGemmStageBytes>;
 
 template <bool DW>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kGemmThreads, 1)
 k_pair_gemm(const __grid_constant__ GemmMaps maps, GemmArgs a) {
   extern __shared__ uint8_t smem_raw[];
-  const Setup s = set_up(smem_raw, a.poff, a.G);
+  const Setup s = set_up(smem_raw, kGemmBytes, 1, 2 * kGemmEpiWarps * 32, a.poff, a.G);
   Ctl *ctl = s.ctl;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int per = 0;  // weights: tiles of one expert
@@ -525,7 +569,7 @@ k_pair_gemm(const __grid_constant__ GemmMaps maps, GemmArgs a) {
       prefetch_map(&maps.b[j]);
     }
     const uint32_t full0 = mapa_rank(smem_u32(&ctl->full[0]), 0);
-    Ring ring;
+    GemmRing ring(s.smem);
     bool ok = true;
     for (int t = s.c0; ok && t < total; t += s.cstep) {
       const Tile q = tile_at(t);
@@ -533,10 +577,9 @@ k_pair_gemm(const __grid_constant__ GemmMaps maps, GemmArgs a) {
       const int bcol = q.n0 + s.rank * kRowTile;
       int seg = 0, k = 0;  // pair of operands, slice of it
       for (int kb = 0; kb < q.nkb; ++kb) {
-        if (!(ok = wait_on(s, &ctl->empty[ring.stage], ring.phase ^ 1u, a.err, 31))) break;
-        if (s.rank == 0) mbar_expect_tx(&ctl->full[ring.stage], 2 * kStageBytes);
-        uint8_t *st = s.smem + (size_t)ring.stage * kStageBytes;
-        const uint32_t bar = full0 + (uint32_t)(ring.stage * sizeof(uint64_t));
+        uint8_t *st = ring.acquire(s, kGemmStageBytes, a.err, 31);
+        if (!(ok = st != nullptr)) break;
+        const uint32_t bar = ring.bar(full0);
         if (DW) {
           const int r = row0 + kb * kBlockK;
           load_mn(&maps.a[q.job], bar, st, q.m0 + s.rank * kRowTile, r);
@@ -550,16 +593,15 @@ k_pair_gemm(const __grid_constant__ GemmMaps maps, GemmArgs a) {
             ++seg;
           }
         }
-        ring.mark();
         ring.next();
       }
     }
-    drain_ring(s, ring, ok);
+    ring.drain(s, ok);
   } else if (warp == 1 && lane == 0 && s.rank == 0) {
     // --------------------------------------------------------------- MMA issuer
     constexpr uint32_t idesc = make_idesc(kPairM, 256) | kIdescMnB | (DW ? kIdescMnA : 0u);
     constexpr int kStepA = DW ? 128 : 2;  // a K = 16 step in the A descriptor
-    Ring ring;
+    GemmRing ring(s.smem);
     bool ok = true, any = false;
     int it = 0;
     for (int t = s.c0; ok && t < total; t += s.cstep, ++it) {
@@ -569,30 +611,24 @@ k_pair_gemm(const __grid_constant__ GemmMaps maps, GemmArgs a) {
       tc_fence_after();
       const uint32_t acc = s.tmem + (uint32_t)(buf * 256);
       for (int kb = 0; kb < q.nkb; ++kb) {
-        if (!(ok = wait_on(s, &ctl->full[ring.stage], ring.phase, a.err, 33))) break;
-        tc_fence_after();
-        const uint32_t sa = smem_u32(s.smem + (size_t)ring.stage * kStageBytes);
-        const uint64_t xa = DW ? sw128_desc_mn(sa, kMnBlock) : sw128_desc(sa);
-        const uint64_t xb = sw128_desc_mn(sa + kOperand, kMnBlock);
+        if (!(ok = ring.filled(s, a.err, 33))) break;
+        const uint64_t xa = DW ? sw128_desc_mn(ring.addr(), kMnBlock) : sw128_desc(ring.addr());
+        const uint64_t xb = sw128_desc_mn(ring.addr() + kOperand, kMnBlock);
 #pragma unroll
         for (int kk = 0; kk < kBlockK / 16; ++kk)
           umma_bf16_pair(acc, xa + kStepA * kk, xb + 128 * kk, idesc, (kb | kk) != 0);
         any = true;
-        umma_commit_pair_both(&ctl->empty[ring.stage]);
+        ring.release(s);
         ring.next();
       }
-      if (!ok) break;
-      umma_commit_pair_both(&ctl->tfull[buf]);
+      if (ok) umma_commit_pair_both(&ctl->tfull[buf]);
     }
-    if (!ok && any) {
-      umma_commit_pair_own(&ctl->drain);
-      wait_on(s, &ctl->drain, 0, nullptr, 0, false, kDrainNs);
-    }
+    if (!ok && any) retire(s, &ctl->drain[0]);
   } else if (warp >= 4) {
     // ----------------------------------------------------------------- epilogue
     const int ew = warp & 3, part = (warp - 4) >> 2;  // lanes 32 ew.., columns 64 part..
     const uint32_t tempty0 = mapa_rank(smem_u32(&ctl->tempty[0]), 0);
-    uint8_t *stage = s.smem + kRing + (warp - 4) * kStageOut;
+    uint8_t *stage = s.smem + kGemmRing + (warp - 4) * kStageOut;
     int it = 0;
     for (int t = s.c0; t < total; t += s.cstep, ++it) {
       const Tile q = tile_at(t);
@@ -698,8 +734,8 @@ std::mutex g_mu;
 // A persistent grid of CTA pairs, at most `tiles` of them; `slot` names the kernel in the
 // per-device table of grid sizes.
 template <typename... KArgs, typename... Args>
-cudaError_t launch_pairs(void (*kernel)(KArgs...), int slot, long long tiles, cudaStream_t st,
-                         const Args &...args) {
+cudaError_t launch_pairs(void (*kernel)(KArgs...), int slot, int threads, size_t smem,
+                         long long tiles, cudaStream_t st, const Args &...args) {
   static int max_pairs[64][4] = {};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -712,8 +748,8 @@ cudaError_t launch_pairs(void (*kernel)(KArgs...), int slot, long long tiles, cu
   attr[0].val.clusterDim.z = 1;
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = 1;
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = kSmemBytes;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
@@ -722,7 +758,7 @@ cudaError_t launch_pairs(void (*kernel)(KArgs...), int slot, long long tiles, cu
     std::lock_guard<std::mutex> lock(g_mu);
     if (most == 0) {
       e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               (int)kSmemBytes);
+                               (int)smem);
       if (e != cudaSuccess) return e;
       cfg.gridDim = dim3(2 * (sm_count() / 2));
       int n = 0;
@@ -768,8 +804,10 @@ cudaError_t launch_act_grad_tc(const FfnGradArgs &f, cudaStream_t st) {
   a.rows = f.rows;
   a.err = f.err;
   const long long tiles = (long long)f.pair_tiles_ub * a.n_tiles;
-  return glu ? launch_pairs(k_act_grad<true>, 0, tiles, st, m, a)
-             : launch_pairs(k_act_grad<false>, 1, tiles, st, m, a);
+  return glu ? launch_pairs(k_act_grad<true>, 0, ActCfg<true>::kThreads, ActCfg<true>::kSmem,
+                            tiles, st, m, a)
+             : launch_pairs(k_act_grad<false>, 1, ActCfg<false>::kThreads, ActCfg<false>::kSmem,
+                            tiles, st, m, a);
 }
 
 cudaError_t launch_dx_tc(const FfnGradArgs &f, cudaStream_t st) {
@@ -795,7 +833,8 @@ cudaError_t launch_dx_tc(const FfnGradArgs &f, cudaStream_t st) {
   a.out_f32 = f.dx_f32;
   a.clipped = f.dx_off == f.poff;  // the rows behind an expert's are its own padding
   a.err = f.err;
-  return launch_pairs(k_pair_gemm<false>, 2, (long long)f.pair_tiles_ub * ceil_div(f.d, 256), st,
+  return launch_pairs(k_pair_gemm<false>, 2, kGemmThreads, kGemmSmem,
+                      (long long)f.pair_tiles_ub * ceil_div(f.d, 256), st,
                       m, a);
 }
 
@@ -825,7 +864,7 @@ cudaError_t launch_dw_tc(const FfnGradArgs &f, cudaStream_t st) {
   a.offsets = f.offsets;
   a.G = f.G;
   a.err = f.err;
-  return launch_pairs(k_pair_gemm<true>, 3, tiles, st, m, a);
+  return launch_pairs(k_pair_gemm<true>, 3, kGemmThreads, kGemmSmem, tiles, st, m, a);
 }
 
 cudaError_t launch_route_dx_tc(const RouteTcArgs &r, cudaStream_t st) {
@@ -847,7 +886,7 @@ cudaError_t launch_route_dx_tc(const RouteTcArgs &r, cudaStream_t st) {
   a.out = r.dx;
   a.out_f32 = 1;
   a.err = r.err;
-  return launch_pairs(k_pair_gemm<false>, 2,
+  return launch_pairs(k_pair_gemm<false>, 2, kGemmThreads, kGemmSmem,
                       (long long)ceil_div(r.T, kPairM) * ceil_div(r.d, 256), st, m, a);
 }
 
@@ -868,7 +907,7 @@ cudaError_t launch_route_dw_tc(const RouteTcArgs &r, cudaStream_t st) {
   a.out = r.dw_part;
   a.out_f32 = 1;
   a.err = r.err;
-  return launch_pairs(k_pair_gemm<true>, 3,
+  return launch_pairs(k_pair_gemm<true>, 3, kGemmThreads, kGemmSmem,
                       (long long)r.pieces * ceil_div(M, kPairM) * ceil_div(r.d, 256), st, m, a);
 }
 
