@@ -57,7 +57,8 @@ struct Setup {
 };
 
 // `bytes` of operand stages and output staging come before the control block; `issuers`
-// threads complete a tile's accumulators, `drainers` threads of both CTAs drain them.
+// threads complete a tile's accumulators, `drainers` warps of both CTAs drain them (one
+// arrival each: one for every thread took 2000 clocks a tile).
 __device__ __forceinline__ Setup set_up(uint8_t *raw, size_t bytes, int issuers, int drainers,
                                         const int32_t *poff, int G) {
   Setup s;
@@ -280,7 +281,7 @@ k_act_grad(const __grid_constant__ ActMaps maps, ActArgs a) {
   using RingQ = Ring<C::kStagesQ, 0, C::kBytesQ>;
   using RingA = Ring<C::kStagesA, C::kStagesQ, C::kBytesA>;
   extern __shared__ uint8_t smem_raw[];
-  const Setup s = set_up(smem_raw, C::kBytes, 2, 2 * C::kEpiWarps * 32, a.poff, a.G);
+  const Setup s = set_up(smem_raw, C::kBytes, 2, 2 * C::kEpiWarps, a.poff, a.G);
   Ctl *ctl = s.ctl;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int total = ctl->pre[a.G] * a.n_tiles;
@@ -478,7 +479,8 @@ k_act_grad(const __grid_constant__ ActMaps maps, ActArgs a) {
         }
         if (c + kParts >= kTileN / 32) {  // the warp's last chunk is in registers
           tc_fence_before();
-          mbar_arrive_cluster(tempty0 + (uint32_t)(buf * sizeof(uint64_t)));
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(tempty0 + (uint32_t)(buf * sizeof(uint64_t)));
         }
         if (mine) {
           put32(stage, &maps.h, hp, col0, prow);
@@ -523,43 +525,62 @@ template <bool DW>
 __global__ void __launch_bounds__(kGemmThreads, 1)
 k_pair_gemm(const __grid_constant__ GemmMaps maps, GemmArgs a) {
   extern __shared__ uint8_t smem_raw[];
-  const Setup s = set_up(smem_raw, kGemmBytes, 1, 2 * kGemmEpiWarps * 32, a.poff, a.G);
+  const Setup s = set_up(smem_raw, kGemmBytes, 1, 2 * kGemmEpiWarps, a.poff, a.G);
   Ctl *ctl = s.ctl;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  int per = 0;  // weights: tiles of one expert
-  if (DW)
-    for (int j = 0; j < a.njobs; ++j) per += ceil_div(a.M[j], kPairM) * ceil_div(a.Ns[j], 256);
+  // weights: an expert's tiles are those of job 0, then 1, then 2 (ends: their prefix)
+  int mt[3] = {1, 1, 1}, end[3] = {0, 0, 0};
+  if (DW) {
+#pragma unroll
+    for (int j = 0; j < 3; ++j) {
+      if (j > 0) end[j] = end[j - 1];
+      if (j < a.njobs) {
+        mt[j] = ceil_div(a.M[j], kPairM);
+        end[j] += mt[j] * ceil_div(a.Ns[j], 256);
+      }
+    }
+  }
+  const int per = end[2];
   const int n_tiles = ceil_div(a.N, 256);
   const int total = DW ? a.G * per : ctl->pre[a.G] * n_tiles;
-  // a tile: expert, job (weights), first row and column, K slices
+  // a tile: expert, job (weights), first row and column, K slices; and the walk over
+  // every cstep-th of them
   struct Tile {
-    int g, job, m0, n0, nkb;
+    int t, g, in, job, m0, n0, nkb;
   };
   const int nk1 = ceil_div(a.K, kBlockK);
-  auto tile_at = [&](int t) -> Tile {
-    Tile r;
-    r.job = 0;
+  auto place = [&](Tile &r) {
     if (DW) {
-      r.g = t / per;
-      int rem = t % per;
-      while (true) {
-        const int cnt = ceil_div(a.M[r.job], kPairM) * ceil_div(a.Ns[r.job], 256);
-        if (rem < cnt) break;
-        rem -= cnt;
-        ++r.job;
+      while (r.in >= per) {
+        r.in -= per;
+        ++r.g;
       }
-      const int mt = ceil_div(a.M[r.job], kPairM);
-      r.m0 = (rem % mt) * kPairM;
-      r.n0 = (rem / mt) * 256;
+      if (r.g >= a.G) return;
+      r.job = (r.in >= end[0]) + (r.in >= end[1]);
+      const int first = r.job == 0 ? 0 : (r.job == 1 ? end[0] : end[1]);
+      const int mts = r.job == 0 ? mt[0] : (r.job == 1 ? mt[1] : mt[2]);
+      const int n = (r.in - first) / mts;
+      r.m0 = (r.in - first - n * mts) * kPairM;
+      r.n0 = n * 256;
       r.nkb = (a.poff[r.g + 1] - a.poff[r.g]) / kBlockK;
     } else {
+      if (r.t >= total) return;
       int n, m;
-      decode_tile(t, ctl->pre, a.G, n_tiles, r.g, n, m);
+      decode_tile(r.t, ctl->pre, a.G, n_tiles, r.g, n, m);
       r.m0 = m * kPairM;
       r.n0 = n * 256;
       r.nkb = a.nseg * nk1;
     }
+  };
+  auto first_tile = [&]() {
+    Tile r{s.c0, 0, s.c0, 0, 0, 0, 0};
+    place(r);
     return r;
+  };
+  auto next_tile = [&](Tile &r) {
+    r.t += s.cstep;
+    r.in += s.cstep;
+    place(r);
   };
 
   if (warp == 0 && lane == 0) {
@@ -571,8 +592,7 @@ k_pair_gemm(const __grid_constant__ GemmMaps maps, GemmArgs a) {
     const uint32_t full0 = mapa_rank(smem_u32(&ctl->full[0]), 0);
     GemmRing ring(s.smem);
     bool ok = true;
-    for (int t = s.c0; ok && t < total; t += s.cstep) {
-      const Tile q = tile_at(t);
+    for (Tile q = first_tile(); ok && q.t < total; next_tile(q)) {
       const int row0 = a.poff[q.g];
       const int bcol = q.n0 + s.rank * kRowTile;
       int seg = 0, k = 0;  // pair of operands, slice of it
@@ -604,8 +624,7 @@ k_pair_gemm(const __grid_constant__ GemmMaps maps, GemmArgs a) {
     GemmRing ring(s.smem);
     bool ok = true, any = false;
     int it = 0;
-    for (int t = s.c0; ok && t < total; t += s.cstep, ++it) {
-      const Tile q = tile_at(t);
+    for (Tile q = first_tile(); ok && q.t < total; next_tile(q), ++it) {
       const int buf = it & 1;
       if (!(ok = wait_on(s, &ctl->tempty[buf], ((it >> 1) & 1) ^ 1u, a.err, 32))) break;
       tc_fence_after();
@@ -630,15 +649,14 @@ k_pair_gemm(const __grid_constant__ GemmMaps maps, GemmArgs a) {
     const uint32_t tempty0 = mapa_rank(smem_u32(&ctl->tempty[0]), 0);
     uint8_t *stage = s.smem + kGemmRing + (warp - 4) * kStageOut;
     int it = 0;
-    for (int t = s.c0; t < total; t += s.cstep, ++it) {
-      const Tile q = tile_at(t);
+    for (Tile q = first_tile(); q.t < total; next_tile(q), ++it) {
       const int buf = it & 1;
       const int lrow = q.m0 + s.rank * kRowTile + ew * 32, col0 = q.n0 + part * 64;
       int rows, N;      // the output's valid rows from q's first, its width
       size_t orow;      // output row of lane 0
       if (DW) {
-        rows = a.M[q.job];
-        N = a.Ns[q.job];
+        rows = q.job == 0 ? a.M[0] : (q.job == 1 ? a.M[1] : a.M[2]);
+        N = q.job == 0 ? a.Ns[0] : (q.job == 1 ? a.Ns[1] : a.Ns[2]);
         orow = (size_t)q.g * rows + lrow;
       } else {
         rows = a.offsets[q.g + 1] - a.offsets[q.g];
@@ -712,7 +730,8 @@ k_pair_gemm(const __grid_constant__ GemmMaps maps, GemmArgs a) {
         }
       }
       tc_fence_before();
-      mbar_arrive_cluster(tempty0 + (uint32_t)(buf * sizeof(uint64_t)));
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(tempty0 + (uint32_t)(buf * sizeof(uint64_t)));
       if (mine && staged && !a.out_f32) {
         fence_proxy_async_smem();
         __syncwarp();
