@@ -58,7 +58,7 @@ struct Setup {
 
 // `bytes` of operand stages and output staging come before the control block; `issuers`
 // threads complete a tile's accumulators, `drainers` warps of both CTAs drain them (one
-// arrival each: one for every thread took 2000 clocks a tile).
+// arrival each).
 __device__ __forceinline__ Setup set_up(uint8_t *raw, size_t bytes, int issuers, int drainers,
                                         const int32_t *poff, int G) {
   Setup s;
@@ -480,7 +480,7 @@ k_act_grad(const __grid_constant__ ActMaps maps, ActArgs a) {
         if (c + kParts >= kTileN / 32) {  // the warp's last chunk is in registers
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(tempty0 + (uint32_t)(buf * sizeof(uint64_t)));
+          if (lane == 0) mbar_arrive_remote(tempty0 + (uint32_t)(buf * sizeof(uint64_t)));
         }
         if (mine) {
           put32(stage, &maps.h, hp, col0, prow);
@@ -731,7 +731,7 @@ k_pair_gemm(const __grid_constant__ GemmMaps maps, GemmArgs a) {
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(tempty0 + (uint32_t)(buf * sizeof(uint64_t)));
+      if (lane == 0) mbar_arrive_remote(tempty0 + (uint32_t)(buf * sizeof(uint64_t)));
       if (mine && staged && !a.out_f32) {
         fence_proxy_async_smem();
         __syncwarp();
