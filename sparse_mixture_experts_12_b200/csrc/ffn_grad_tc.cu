@@ -45,7 +45,7 @@ struct Ctl {
   uint64_t drain[2];
   uint32_t tmem_base;
   int abort_flag;
-  int pre[kMaxExperts + 1];  // prefix of the experts' 256-row tiles
+  int pre[kMaxExperts + 1];  // prefix of the experts' 256-row tiles, or their first rows
 };
 
 // what both kernels do before their roles split up
@@ -59,8 +59,9 @@ struct Setup {
 // `bytes` of operand stages and output staging come before the control block; `issuers`
 // threads complete a tile's accumulators, `drainers` warps of both CTAs drain them (one
 // arrival each).
+// `unit`: rows of a tile whose prefix over the experts goes to pre[] (0: their first rows).
 __device__ __forceinline__ Setup set_up(uint8_t *raw, size_t bytes, int issuers, int drainers,
-                                        const int32_t *poff, int G) {
+                                        const int32_t *poff, int G, int unit) {
   Setup s;
   s.smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) &
                                        ~static_cast<uintptr_t>(1023));
@@ -86,11 +87,13 @@ __device__ __forceinline__ Setup set_up(uint8_t *raw, size_t bytes, int issuers,
     tmem_relinquish_pair();
   }
   pdl_wait();
-  if (warp == 1) {
+  if (unit == 0) {
+    for (int i = tid; i <= G; i += blockDim.x) ctl->pre[i] = poff[i];
+  } else if (warp == 1) {
     const int per = ceil_div(G, 32);
     const int j0 = min(G, lane * per), j1 = min(G, j0 + per);
     int sum = 0;
-    for (int j = j0; j < j1; ++j) sum += ceil_div(poff[j + 1] - poff[j], kPairM);
+    for (int j = j0; j < j1; ++j) sum += ceil_div(poff[j + 1] - poff[j], unit);
     int incl = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -100,7 +103,7 @@ __device__ __forceinline__ Setup set_up(uint8_t *raw, size_t bytes, int issuers,
     int run = incl - sum;
     for (int j = j0; j < j1; ++j) {
       ctl->pre[j] = run;
-      run += ceil_div(poff[j + 1] - poff[j], kPairM);
+      run += ceil_div(poff[j + 1] - poff[j], unit);
     }
     if (lane == 31) ctl->pre[G] = incl;
   }
@@ -182,13 +185,6 @@ __device__ __forceinline__ void tear_down(const Setup &s) {
     tc_fence_after();
     tmem_dealloc_pair(s.tmem, kTmemCols);
   }
-}
-
-// 64 K rows x 128 contiguous elements, as two 64-element blocks
-__device__ __forceinline__ void load_mn(const CUtensorMap *map, uint32_t bar, uint8_t *dst, int c,
-                                        int row) {
-  tma_load_2d_pair(map, bar, dst, c, row);
-  tma_load_2d_pair(map, bar, dst + kMnBlock, c + kBlockK, row);
 }
 
 // One 32-row x 32-column chunk (a lane's row of 64 bytes) through the warp's 2 KB of
@@ -281,7 +277,7 @@ k_act_grad(const __grid_constant__ ActMaps maps, ActArgs a) {
   using RingQ = Ring<C::kStagesQ, 0, C::kBytesQ>;
   using RingA = Ring<C::kStagesA, C::kStagesQ, C::kBytesA>;
   extern __shared__ uint8_t smem_raw[];
-  const Setup s = set_up(smem_raw, C::kBytes, 2, 2 * C::kEpiWarps, a.poff, a.G);
+  const Setup s = set_up(smem_raw, C::kBytes, 2, 2 * C::kEpiWarps, a.poff, a.G, kPairM);
   Ctl *ctl = s.ctl;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int total = ctl->pre[a.G] * a.n_tiles;
@@ -525,17 +521,19 @@ template <bool DW>
 __global__ void __launch_bounds__(kGemmThreads, 1)
 k_pair_gemm(const __grid_constant__ GemmMaps maps, GemmArgs a) {
   extern __shared__ uint8_t smem_raw[];
-  const Setup s = set_up(smem_raw, kGemmBytes, 1, 2 * kGemmEpiWarps, a.poff, a.G);
+  const Setup s = set_up(smem_raw, kGemmBytes, 1, 2 * kGemmEpiWarps, a.poff, a.G, DW ? 0 : kPairM);
   Ctl *ctl = s.ctl;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // weights: an expert's tiles are those of job 0, then 1, then 2 (ends: their prefix)
   int mt[3] = {1, 1, 1}, end[3] = {0, 0, 0};
+  float inv[3] = {1.f, 1.f, 1.f};
   if (DW) {
 #pragma unroll
     for (int j = 0; j < 3; ++j) {
       if (j > 0) end[j] = end[j - 1];
       if (j < a.njobs) {
         mt[j] = ceil_div(a.M[j], kPairM);
+        inv[j] = 1.f / (float)mt[j];
         end[j] += mt[j] * ceil_div(a.Ns[j], 256);
       }
     }
@@ -546,7 +544,7 @@ k_pair_gemm(const __grid_constant__ GemmMaps maps, GemmArgs a) {
   // a tile: expert, job (weights), first row and column, K slices; and the walk over
   // every cstep-th of them
   struct Tile {
-    int t, g, in, job, m0, n0, nkb;
+    int t, g, in, job, m0, n0, nkb, row0;
   };
   const int nk1 = ceil_div(a.K, kBlockK);
   auto place = [&](Tile &r) {
@@ -559,10 +557,14 @@ k_pair_gemm(const __grid_constant__ GemmMaps maps, GemmArgs a) {
       r.job = (r.in >= end[0]) + (r.in >= end[1]);
       const int first = r.job == 0 ? 0 : (r.job == 1 ? end[0] : end[1]);
       const int mts = r.job == 0 ? mt[0] : (r.job == 1 ? mt[1] : mt[2]);
-      const int n = (r.in - first) / mts;
+      // n = in / mts (single-thread roles pay for a division in full): exact, since in is
+      // below 2^20 and half a tile is more than the product's error
+      const float by = r.job == 0 ? inv[0] : (r.job == 1 ? inv[1] : inv[2]);
+      const int n = __float2int_rd(((float)(r.in - first) + 0.5f) * by);
       r.m0 = (r.in - first - n * mts) * kPairM;
       r.n0 = n * 256;
-      r.nkb = (a.poff[r.g + 1] - a.poff[r.g]) / kBlockK;
+      r.row0 = ctl->pre[r.g];
+      r.nkb = (ctl->pre[r.g + 1] - r.row0) / kBlockK;
     } else {
       if (r.t >= total) return;
       int n, m;
@@ -570,10 +572,11 @@ k_pair_gemm(const __grid_constant__ GemmMaps maps, GemmArgs a) {
       r.m0 = m * kPairM;
       r.n0 = n * 256;
       r.nkb = a.nseg * nk1;
+      r.row0 = a.poff[r.g];
     }
   };
   auto first_tile = [&]() {
-    Tile r{s.c0, 0, s.c0, 0, 0, 0, 0};
+    Tile r{s.c0, 0, s.c0, 0, 0, 0, 0, 0};
     place(r);
     return r;
   };
@@ -593,8 +596,7 @@ k_pair_gemm(const __grid_constant__ GemmMaps maps, GemmArgs a) {
     GemmRing ring(s.smem);
     bool ok = true;
     for (Tile q = first_tile(); ok && q.t < total; next_tile(q)) {
-      const int row0 = a.poff[q.g];
-      const int bcol = q.n0 + s.rank * kRowTile;
+      const int row0 = q.row0, bblk = q.n0 / kBlockK + 2 * s.rank;
       int seg = 0, k = 0;  // pair of operands, slice of it
       for (int kb = 0; kb < q.nkb; ++kb) {
         uint8_t *st = ring.acquire(s, kGemmStageBytes, a.err, 31);
@@ -602,12 +604,12 @@ k_pair_gemm(const __grid_constant__ GemmMaps maps, GemmArgs a) {
         const uint32_t bar = ring.bar(full0);
         if (DW) {
           const int r = row0 + kb * kBlockK;
-          load_mn(&maps.a[q.job], bar, st, q.m0 + s.rank * kRowTile, r);
-          load_mn(&maps.b[q.job], bar, st + kOperand, bcol, r);
+          tma_load_3d_pair(&maps.a[q.job], bar, st, 0, r, q.m0 / kBlockK + 2 * s.rank);
+          tma_load_3d_pair(&maps.b[q.job], bar, st + kOperand, 0, r, bblk);
         } else {
           const int k0 = k * kBlockK;
           tma_load_2d_pair(&maps.a[seg], bar, st, k0, row0 + q.m0 + s.rank * kRowTile);
-          load_mn(&maps.b[seg], bar, st + kOperand, bcol, q.g * a.K + k0);
+          tma_load_3d_pair(&maps.b[seg], bar, st + kOperand, 0, q.g * a.K + k0, bblk);
           if (++k == nk1) {
             k = 0;
             ++seg;
@@ -833,10 +835,10 @@ cudaError_t launch_dx_tc(const FfnGradArgs &f, cudaStream_t st) {
   const bool glu = f.act == MOE_ACT_SWIGLU;
   const uint64_t R = (uint64_t)f.rows, d = (uint64_t)f.d, F = (uint64_t)f.F, G = (uint64_t)f.G;
   GemmMaps m;
-  bool ok = make_map(&m.a[0], f.dg, R, F, kRowTile) && make_map(&m.b[0], f.w1, G * F, d, kBlockK);
+  bool ok = make_map(&m.a[0], f.dg, R, F, kRowTile) && make_mn_map(&m.b[0], f.w1, G * F, d);
   if (glu)
     ok = ok && make_map(&m.a[1], f.du, R, F, kRowTile) &&
-         make_map(&m.b[1], f.w3, G * F, d, kBlockK);
+         make_mn_map(&m.b[1], f.w3, G * F, d);
   ok = ok && (f.dx_f32 ? make_f32_map(&m.o[0], f.dx, (uint64_t)f.dx_rows, d)
                        : make_map(&m.o[0], f.dx, (uint64_t)f.dx_rows, d, 32));
   if (!ok) return cudaErrorInvalidValue;
@@ -867,8 +869,8 @@ cudaError_t launch_dw_tc(const FfnGradArgs &f, cudaStream_t st) {
                  int N) {
     if (out == nullptr) return;
     const int j = a.njobs++;
-    ok = ok && make_map(&m.a[j], p, prows, (uint64_t)M, kBlockK) &&
-         make_map(&m.b[j], q, qrows, (uint64_t)N, kBlockK) &&
+    ok = ok && make_mn_map(&m.a[j], p, prows, (uint64_t)M) &&
+         make_mn_map(&m.b[j], q, qrows, (uint64_t)N) &&
          make_map(&m.o[j], out, G * (uint64_t)M, (uint64_t)N, 32);
     a.M[j] = M;
     a.Ns[j] = N;
@@ -892,7 +894,7 @@ cudaError_t launch_route_dx_tc(const RouteTcArgs &r, cudaStream_t st) {
   for (int j = 0; j < kSplit; ++j)
     if (!make_map(&m.a[j], r.terms + (size_t)j * r.Ep, (uint64_t)r.T, (uint64_t)r.Ep, kRowTile,
                   (uint64_t)kSplit * r.Ep) ||
-        !make_map(&m.b[j], r.w, (uint64_t)r.E, (uint64_t)r.d, kBlockK))
+        !make_mn_map(&m.b[j], r.w, (uint64_t)r.E, (uint64_t)r.d))
       return cudaErrorInvalidValue;
   if (!make_f32_map(&m.o[0], r.dx, (uint64_t)r.T, (uint64_t)r.d)) return cudaErrorInvalidValue;
   a.clipped = 1;
@@ -914,8 +916,8 @@ cudaError_t launch_route_dw_tc(const RouteTcArgs &r, cudaStream_t st) {
   GemmArgs a{};
   // the terms side by side are the rows of one product: x is read once for both
   const int M = kSplitDw * r.Ep;
-  if (!make_map(&m.a[0], r.terms, (uint64_t)r.T, (uint64_t)M, kBlockK, (uint64_t)kSplit * r.Ep) ||
-      !make_map(&m.b[0], r.x, (uint64_t)r.T, (uint64_t)r.d, kBlockK) ||
+  if (!make_mn_map(&m.a[0], r.terms, (uint64_t)r.T, (uint64_t)M, (uint64_t)kSplit * r.Ep) ||
+      !make_mn_map(&m.b[0], r.x, (uint64_t)r.T, (uint64_t)r.d) ||
       !make_f32_map(&m.o[0], r.dw_part, (uint64_t)r.pieces * M, (uint64_t)r.d))
     return cudaErrorInvalidValue;
   a.poff = a.offsets = r.piece;
