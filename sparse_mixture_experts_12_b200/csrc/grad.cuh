@@ -99,8 +99,9 @@ struct FfnGradArgs {
                              // expert g has offsets[g+1] - offsets[g] rows
   const int32_t *poff;       // [G+1] its first row in all arrays but dx
   const int32_t *dx_off;     // [G+1] its first row in dx: offsets or poff
-  const int32_t *mprefix;    // [G+1] prefix of the experts' 128-row tiles
-  int G, m_tiles_ub, pair_tiles_ub;  // bounds of the 128-row and the 256-row tiles
+  const int32_t *mprefix;    // [G+1] prefix of the experts' tile_rows-row tiles
+  int tile_rows;             // 32 or 128, see grad_tile_rows()
+  int G, m_tiles_ub, pair_tiles_ub;  // bounds of those tiles and of the 256-row tiles
   int d, F, act;
   const void *w1, *w3, *w2;
   const float *b1, *b2;
@@ -112,7 +113,7 @@ struct FfnGradArgs {
   int dx_f32, dx_rows;
   void *dw1, *dw3, *dw2;     // [G, F, d], [G, F, d], [G, d, F] dtype, or nullptr
   float *db1, *db2;          // [G, F], [G, d] fp32, or nullptr
-  float *col_part;           // scratch of col_part_rows() x max(F, d) (with db1 or db2)
+  float *col_part, *part2;   // scratch of col_part_rows() x F (with db1), m_tiles_ub x d (db2)
   int32_t *err;
 };
 cudaError_t launch_ffn_bwd(const FfnGradArgs &a, int dtype, cudaStream_t st);
@@ -129,17 +130,22 @@ inline long long padded_rows_ub(long long R, int G, int pad) {
   const long long r = R + (long long)(pad - 1) * (R < G ? R : G);
   return (r + pad - 1) / pad * pad;
 }
-// column-sum partials: one per 128-row tile, and (bf16) one per 32 rows
+// Rows of a tile of the CUDA-core products (and of a partial of db2): 32 where experts
+// average fewer than 64 rows, so that small experts do not pay for empty ones.
+inline int grad_tile_rows(long long rows, int G) { return rows < 64LL * G ? 32 : 128; }
+inline int grad_tiles_ub(long long rows, int G, int unit) {
+  return (int)(rows / unit + (rows < G ? rows : G));
+}
+// partials of db1: one per row tile, or (bf16) one per 32 padded rows
 inline long long col_part_rows(long long rows, int m_tiles, int dtype) {
-  const long long g = dtype == MOE_DTYPE_F32 ? 0 : (rows + 31) / 32;
-  return g > m_tiles ? g : m_tiles;
+  return dtype == MOE_DTYPE_F32 ? m_tiles : rows / 32;
 }
 // offsets -> checked copy, tile prefix and the padded first rows
-cudaError_t launch_grad_tables(const int32_t *offsets, int G, int max_rows, int pad,
+cudaError_t launch_grad_tables(const int32_t *offsets, int G, int max_rows, int unit, int pad,
                                int32_t *checked, int32_t *mprefix, int32_t *poff, int32_t *err,
                                cudaStream_t st);
 // the tables of one group of n rows
-cudaError_t launch_one_group(int n, int pad, int32_t *offsets, int32_t *mprefix, int32_t *poff,
+cudaError_t launch_one_group(int n, int unit, int pad, int32_t *offsets, int32_t *mprefix, int32_t *poff,
                              cudaStream_t st);
 
 }  // namespace moe

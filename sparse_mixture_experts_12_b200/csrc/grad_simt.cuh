@@ -1,12 +1,9 @@
-// fp32 matrix products of the gradients on CUDA cores (FFMA): 128 x 64 tiles of
-// C = A B with B row-major [K, N], A row-major [M, K] or (AT) [K, M].
+// fp32 tiles on CUDA cores (FFMA) shared by the gradients: 256 threads compute a
+// BM x 64 tile of C = A B with B row-major [K, N], A row-major [M, K] or (AT) [K, M], from
+// K slices in shared memory while the next slice is fetched into registers.
 //
-// Two groupings:
-//  * rows:  the rows of A and C are expert-contiguous (or one plain matrix); B is
-//           the expert's own. Up to two (A, B) pairs add into the same C.
-//  * k:     the reduction runs over an expert's rows (or over one of `chunk`-row
-//           pieces of a plain matrix), and C is the expert's (the piece's) own. Up
-//           to three independent (A, B, C) jobs share a launch.
+// BM 128 (8 x 4 values a thread, 16-wide slices) is for experts with many rows; BM 32 (2 x
+// 4, 32-wide) for few: a 128-row tile of 16 rows took 22 us where the 32-row one takes 5.
 #pragma once
 
 #include "kernels.cuh"
@@ -14,11 +11,16 @@
 namespace moe {
 namespace simt {
 
-constexpr int BM = kRowTile, BN = 64, BK = 32;
-constexpr int TM = 8, TN = 4;  // per-thread micro tile; (BM/TM)*(BN/TN) = 256 threads
-constexpr int kAPer = BM * BK / 256, kBPer = BN * BK / 256;
+constexpr int BN = 64, kThreads = 256;
+template <int BM_>
+struct Tile {
+  static constexpr int BM = BM_, BK = BM == 128 ? 16 : 32;
+  static constexpr int TM = BM / 16, TN = 4;       // per thread; 16 x 16 threads
+  static constexpr int LDA = BM + (BM == 128 ? 4 : 2), LDB = BN + 4;
+  static constexpr int A4 = BM * BK / 4 / kThreads, B4 = BN * BK / 4 / kThreads;
+};
 
-// the expert of 128-row tile mt (mprefix [G+1]), or -1 past the last tile
+// the expert of row tile mt (mprefix [G+1]), or -1 past the last tile
 __device__ __forceinline__ int group_of_tile(const int32_t *mprefix, int G, int mt) {
   if (mt >= mprefix[G]) return -1;
   int lo = 0, hi = G - 1;  // last g with mprefix[g] <= mt
@@ -29,126 +31,147 @@ __device__ __forceinline__ int group_of_tile(const int32_t *mprefix, int G, int 
   return lo;
 }
 
-template <typename TA, typename TB, typename TO>
-struct Gemm {
-  const TA *a[3];
-  const TB *b[3];
-  TO *c[3];
-  int M[3], N[3];       // k grouping: per job; rows: M[0] = rows, N[0]
-  int lda[3], ldb[3];
-  int nseg;             // rows: (A, B) pairs added; k: jobs
-  int K;                // rows: reduction length; k: rows of the plain matrix
-  int chunk;            // k, plain matrix: rows per piece
-  int G;                // experts (k, plain matrix: pieces)
-  const int32_t *offsets, *mprefix;  // nullptr: a plain matrix
+// up to four consecutive values, n of them inside (n <= 0: none). VEC: 16-byte aligned,
+// and all dimensions are multiples of 4.
+template <bool VEC>
+__device__ __forceinline__ float4 ld4(const float *p, int n) {
+  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (VEC) {
+    if (n > 0) v = __ldg(reinterpret_cast<const float4 *>(p));
+  } else {
+    if (n > 0) v.x = __ldg(p);
+    if (n > 1) v.y = __ldg(p + 1);
+    if (n > 2) v.z = __ldg(p + 2);
+    if (n > 3) v.w = __ldg(p + 3);
+  }
+  return v;
+}
+
+// A slice of an operand with ROWS rows (of M or N), BK wide, in registers and then in
+// shared memory as [BK][LD]. KMAJOR: the reduction's index is the contiguous one.
+template <int ROWS, int BK, int LD, bool KMAJOR, bool VEC>
+struct Slice {
+  static constexpr int N4 = ROWS * BK / 4 / kThreads;
+  float4 r[N4];
+  __device__ __forceinline__ void fetch(const float *p, size_t ld, int rows, int k0, int K) {
+#pragma unroll
+    for (int j = 0; j < N4; ++j) {
+      const int i = threadIdx.x + kThreads * j;
+      if (KMAJOR) {
+        const int m = i / (BK / 4), k = k0 + (i % (BK / 4)) * 4;
+        r[j] = ld4<VEC>(p + (size_t)m * ld + k, m < rows ? K - k : 0);
+      } else {
+        const int k = k0 + i / (ROWS / 4), m = (i % (ROWS / 4)) * 4;
+        r[j] = ld4<VEC>(p + (size_t)k * ld + m, k < K ? rows - m : 0);
+      }
+    }
+  }
+  __device__ __forceinline__ void put(float (*s)[LD]) const {
+#pragma unroll
+    for (int j = 0; j < N4; ++j) {
+      const int i = threadIdx.x + kThreads * j;
+      if (KMAJOR) {
+        const int m = i / (BK / 4), k = (i % (BK / 4)) * 4;
+        s[k][m] = r[j].x;
+        s[k + 1][m] = r[j].y;
+        s[k + 2][m] = r[j].z;
+        s[k + 3][m] = r[j].w;
+      } else {
+        const int k = i / (ROWS / 4), m = (i % (ROWS / 4)) * 4;
+        if (LD % 4 == 0) {
+          *reinterpret_cast<float4 *>(&s[k][m]) = r[j];
+        } else {
+          *reinterpret_cast<float2 *>(&s[k][m]) = make_float2(r[j].x, r[j].y);
+          *reinterpret_cast<float2 *>(&s[k][m + 2]) = make_float2(r[j].z, r[j].w);
+        }
+      }
+    }
+  }
 };
 
-template <typename TA, typename TB, typename TO, bool KGROUP>
-__global__ void __launch_bounds__(256) k_gemm(Gemm<TA, TB, TO> s) {
-  __shared__ __align__(16) float As[BK][BM + 4];
-  __shared__ __align__(16) float Bs[BK][BN + 4];
-  const int tid = threadIdx.x;
-  pdl_wait();
-  pdl_trigger();
-  int job = 0, g = 0, row0, nrows, K;  // row0: first row of A and C (rows) or of the reduction (k)
-  const int n0 = blockIdx.x * BN;
-  int m0;
-  if (KGROUP) {
-    job = blockIdx.z / s.G;
-    g = blockIdx.z % s.G;
-    m0 = blockIdx.y * BM;
-    if (m0 >= s.M[job] || n0 >= s.N[job]) return;
-    nrows = min(BM, s.M[job] - m0);
-    const int e0 = s.offsets ? s.offsets[g] : g * s.chunk;
-    const int e1 = s.offsets ? s.offsets[g + 1] : min(s.K, e0 + s.chunk);
-    row0 = e0;
-    K = max(0, e1 - e0);
+template <int TM>
+__device__ __forceinline__ void row_values(const float *p, float (&v)[TM]) {
+  if constexpr (TM == 8) {
+#pragma unroll
+    for (int i = 0; i < TM; i += 4) {
+      const float4 q = *reinterpret_cast<const float4 *>(p + i);
+      v[i] = q.x; v[i + 1] = q.y; v[i + 2] = q.z; v[i + 3] = q.w;
+    }
   } else {
-    m0 = blockIdx.y * BM;
-    if (s.offsets) {
-      g = group_of_tile(s.mprefix, s.G, blockIdx.y);
-      if (g < 0) return;
-      m0 = s.offsets[g] + ((int)blockIdx.y - s.mprefix[g]) * BM;
-      nrows = min(BM, s.offsets[g + 1] - m0);
-    } else {
-      nrows = min(BM, s.M[0] - m0);
-    }
-    row0 = m0;
-    K = s.K;
+    const float2 q = *reinterpret_cast<const float2 *>(p);
+    v[0] = q.x; v[1] = q.y;
   }
-  const int N = s.N[job];
-  const int tx = tid % (BN / TN), ty = tid / (BN / TN);
-  float acc[TM][TN];
-#pragma unroll
-  for (int i = 0; i < TM; ++i)
-#pragma unroll
-    for (int j = 0; j < TN; ++j) acc[i][j] = 0.f;
-  const int nseg = KGROUP ? 1 : s.nseg;
-  for (int seg = 0; seg < nseg; ++seg) {
-    const int q = KGROUP ? job : seg;
-    const int lda = s.lda[q], ldb = s.ldb[q];
-    const TA *ap = s.a[q] + (size_t)row0 * lda + (KGROUP ? m0 : 0);
-    const TB *bp = s.b[q] + (KGROUP ? (size_t)row0 : (size_t)g * s.K) * ldb + n0;
-    float ra[kAPer], rb[kBPer];
-    auto fetch = [&](int k0) {
-#pragma unroll
-      for (int j = 0; j < kAPer; ++j) {
-        const int i = tid + 256 * j;
-        const int m = KGROUP ? i % BM : i / BK, kk = KGROUP ? i / BM : i % BK;
-        const bool ok = m < nrows && k0 + kk < K;
-        ra[j] = ok ? Elem<TA>::to_f(ap[KGROUP ? (size_t)(k0 + kk) * lda + m
-                                              : (size_t)m * lda + k0 + kk])
-                   : 0.f;
-      }
-#pragma unroll
-      for (int j = 0; j < kBPer; ++j) {
-        const int i = tid + 256 * j, n = i % BN, kk = i / BN;
-        const bool ok = n0 + n < N && k0 + kk < K;
-        rb[j] = ok ? Elem<TB>::to_f(bp[(size_t)(k0 + kk) * ldb + n]) : 0.f;
-      }
-    };
-    fetch(0);
-    for (int k0 = 0; k0 < K; k0 += BK) {
-#pragma unroll
-      for (int j = 0; j < kAPer; ++j) {
-        const int i = tid + 256 * j;
-        if (KGROUP) As[i / BM][i % BM] = ra[j];
-        else As[i % BK][i / BK] = ra[j];
-      }
-#pragma unroll
-      for (int j = 0; j < kBPer; ++j) {
-        const int i = tid + 256 * j;
-        Bs[i / BN][i % BN] = rb[j];
-      }
-      __syncthreads();
-      if (k0 + BK < K) fetch(k0 + BK);
-#pragma unroll
-      for (int kk = 0; kk < BK; ++kk) {
-        float av[TM], bv[TN];
-#pragma unroll
-        for (int i = 0; i < TM; i += 4) {
-          const float4 v = *reinterpret_cast<const float4 *>(&As[kk][ty * TM + i]);
-          av[i] = v.x; av[i + 1] = v.y; av[i + 2] = v.z; av[i + 3] = v.w;
-        }
-        const float4 v = *reinterpret_cast<const float4 *>(&Bs[kk][tx * TN]);
-        bv[0] = v.x; bv[1] = v.y; bv[2] = v.z; bv[3] = v.w;
-#pragma unroll
-        for (int i = 0; i < TM; ++i)
-#pragma unroll
-          for (int j = 0; j < TN; ++j) acc[i][j] = fmaf(av[i], bv[j], acc[i][j]);
-      }
-      __syncthreads();
-    }
-  }
-  TO *c = s.c[job] + (KGROUP ? (size_t)g * s.M[job] * N : 0);
+}
+template <int TM>
+__device__ __forceinline__ void outer(float (&acc)[TM][4], const float (&a)[TM], const float *b) {
+  const float4 q = *reinterpret_cast<const float4 *>(b);
 #pragma unroll
   for (int i = 0; i < TM; ++i) {
-    const int m = ty * TM + i;
-    if (m >= nrows) continue;
+    acc[i][0] = fmaf(a[i], q.x, acc[i][0]);
+    acc[i][1] = fmaf(a[i], q.y, acc[i][1]);
+    acc[i][2] = fmaf(a[i], q.z, acc[i][2]);
+    acc[i][3] = fmaf(a[i], q.w, acc[i][3]);
+  }
+}
+template <int TM>
+__device__ __forceinline__ void clear(float (&acc)[TM][4]) {
 #pragma unroll
-    for (int j = 0; j < TN; ++j) {
-      const int n = n0 + tx * TN + j;
-      if (n < N) c[(size_t)(m0 + m) * N + n] = Elem<TO>::from_f(acc[i][j]);
+  for (int i = 0; i < TM; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
+}
+
+template <class T>
+struct GemmSmem {
+  alignas(16) float a[T::BK][T::LDA];
+  alignas(16) float b[T::BK][T::LDB];
+};
+
+// acc += A B over K for the tile whose operands begin at a and b: `rows` rows of A, `cols`
+// columns of B inside
+template <class T, bool AT, bool VEC>
+__device__ __forceinline__ void mma_tile(GemmSmem<T> &s, float (&acc)[T::TM][4], const float *a,
+                                         size_t lda, int rows, const float *b, size_t ldb, int cols,
+                                         int K) {
+  const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
+  Slice<T::BM, T::BK, T::LDA, !AT, VEC> sa;
+  Slice<BN, T::BK, T::LDB, false, VEC> sb;
+  sa.fetch(a, lda, rows, 0, K);
+  sb.fetch(b, ldb, cols, 0, K);
+  for (int k0 = 0; k0 < K; k0 += T::BK) {
+    __syncthreads();
+    sa.put(s.a);
+    sb.put(s.b);
+    __syncthreads();
+    if (k0 + T::BK < K) {
+      sa.fetch(a, lda, rows, k0 + T::BK, K);
+      sb.fetch(b, ldb, cols, k0 + T::BK, K);
+    }
+#pragma unroll
+    for (int k = 0; k < T::BK; ++k) {
+      float av[T::TM];
+      row_values<T::TM>(&s.a[k][ty * T::TM], av);
+      outer<T::TM>(acc, av, &s.b[k][tx * 4]);
+    }
+  }
+}
+
+// c: the tile's first element
+template <class T, bool VEC>
+__device__ __forceinline__ void store_tile(const float (&acc)[T::TM][4], float *c, size_t ldc,
+                                           int rows, int cols) {
+  const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
+#pragma unroll
+  for (int i = 0; i < T::TM; ++i) {
+    const int m = ty * T::TM + i;
+    if (m >= rows) continue;
+    float *p = c + (size_t)m * ldc + tx * 4;
+    const int n = cols - tx * 4;
+    if (VEC) {
+      if (n > 0)
+        *reinterpret_cast<float4 *>(p) = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (j < n) p[j] = acc[i][j];
     }
   }
 }

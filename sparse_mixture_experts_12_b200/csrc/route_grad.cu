@@ -433,7 +433,7 @@ int dlogits_blocks(int T, int lanes) {
 
 // pieces of the tokens for dW: enough tiles for two per SM
 int dw_pieces(int T, int d, int E) {
-  const int tiles = ceil_div(E, simt::BM) * ceil_div(d, simt::BN);
+  const int tiles = ceil_div(E, 128) * ceil_div(d, simt::BN);
   int s = 296 / tiles;
   if (s < 1) s = 1;
   const int most = ceil_div(T, 64);
@@ -503,43 +503,51 @@ cudaError_t route_bwd_few(const RouteBwdArgs &a, cudaStream_t st) {
   return sums<T>(a, dw_part, pieces, a.E, db_part, dz_lanes(a.E), st);
 }
 
-// fp32, more experts: tiles on CUDA cores
+// fp32, more experts: tiles on CUDA cores, those of dx = dz W and of the pieces of dW =
+// dz^T x in one launch. E need not be a multiple of 4.
+using ProjTile = simt::Tile<128>;
+template <bool VEC>
+__global__ void __launch_bounds__(simt::kThreads) k_proj_tiles(RouteBwdArgs a, float *dw_part,
+                                                               int dx_blocks, int per) {
+  using T = ProjTile;
+  __shared__ simt::GemmSmem<T> sm;
+  pdl_wait();
+  pdl_trigger();
+  const float *x = static_cast<const float *>(a.x), *w = static_cast<const float *>(a.w);
+  const int nt = ceil_div(a.d, simt::BN), E = a.E, d = a.d;
+  float acc[T::TM][4];
+  simt::clear(acc);
+  int b = blockIdx.x;
+  if (b < dx_blocks) {
+    const int m0 = b / nt * T::BM, n0 = b % nt * simt::BN;
+    simt::mma_tile<T, false, VEC>(sm, acc, a.dlogits + (size_t)m0 * E, E, a.T - m0, w + n0, d,
+                                  d - n0, E);
+    simt::store_tile<T, true>(acc, a.dx + (size_t)m0 * d + n0, d, min(T::BM, a.T - m0),
+                              min(simt::BN, d - n0));
+    return;
+  }
+  b -= dx_blocks;
+  const int mt = ceil_div(E, T::BM), piece = b / (mt * nt);
+  b -= piece * mt * nt;
+  const int m0 = b / nt * T::BM, n0 = b % nt * simt::BN;
+  const int t0 = min(a.T, piece * per), n = min(a.T - t0, per);
+  simt::mma_tile<T, true, VEC>(sm, acc, a.dlogits + (size_t)t0 * E + m0, E, E - m0,
+                               x + (size_t)t0 * d + n0, d, d - n0, n);
+  simt::store_tile<T, true>(acc, dw_part + ((size_t)piece * E + m0) * d + n0, d,
+                            min(T::BM, E - m0), min(simt::BN, d - n0));
+}
+
 cudaError_t route_bwd_simt(const RouteBwdArgs &a, cudaStream_t st) {
   float *db_part = static_cast<float *>(a.part);
-  const dim3 b(256);
   cudaError_t e = dlogits<false>(a, a.db ? db_part : nullptr, RouteTcArgs{}, dz_lanes(a.E), st);
   if (e != cudaSuccess) return e;
-  const float *x = static_cast<const float *>(a.x), *w = static_cast<const float *>(a.w);
-  if (a.dx) {
-    simt::Gemm<float, float, float> m{};
-    m.a[0] = a.dlogits;
-    m.b[0] = w;
-    m.c[0] = a.dx;
-    m.M[0] = a.T;
-    m.N[0] = m.ldb[0] = a.d;
-    m.lda[0] = a.E;
-    m.nseg = 1;
-    m.K = a.E;
-    m.G = 1;
-    e = launch_pdl(simt::k_gemm<float, float, float, false>,
-                   dim3(ceil_div(a.d, simt::BN), ceil_div(a.T, simt::BM)), b, 0, st, m);
-    if (e != cudaSuccess) return e;
-  }
-  const int pieces = dw_pieces(a.T, a.d, a.E);
+  const int pieces = dw_pieces(a.T, a.d, a.E), nt = ceil_div(a.d, simt::BN);
   float *dw_part = db_part + (size_t)kMaxBlocks * a.E;
-  if (a.dw) {
-    simt::Gemm<float, float, float> m{};
-    m.a[0] = a.dlogits;
-    m.b[0] = x;
-    m.c[0] = dw_part;
-    m.M[0] = m.lda[0] = a.E;
-    m.N[0] = m.ldb[0] = a.d;
-    m.nseg = 1;
-    m.K = a.T;
-    m.chunk = ceil_div(a.T, pieces);
-    m.G = pieces;
-    e = launch_pdl(simt::k_gemm<float, float, float, true>,
-                   dim3(ceil_div(a.d, simt::BN), ceil_div(a.E, simt::BM), pieces), b, 0, st, m);
+  const int dx = a.dx ? nt * ceil_div(a.T, ProjTile::BM) : 0;
+  const int dw = a.dw ? nt * ceil_div(a.E, ProjTile::BM) * pieces : 0;
+  if (dx + dw > 0) {
+    e = launch_pdl(a.E % 4 ? k_proj_tiles<false> : k_proj_tiles<true>, dim3(dx + dw),
+                   dim3(simt::kThreads), 0, st, a, dw_part, dx, ceil_div(a.T, pieces));
     if (e != cudaSuccess) return e;
   }
   return sums<float>(a, dw_part, pieces, a.E, db_part, dz_lanes(a.E), st);

@@ -9,7 +9,7 @@ namespace {
 
 enum Buf {
   G_ERR, G_OFFSETS, G_MPREFIX, G_POFF, G_SH_OFFSETS, G_SH_MPREFIX, G_SH_POFF, G_H, G_DG, G_DU,
-  G_COL, G_DLOGITS, G_ROUTE, G_X, G_DY, G_INV, G_DX, G_ROW_W, G_ROW_DOT, G_DOT_PART, G_DX_ROUTER,
+  G_COL, G_COL2, G_DLOGITS, G_ROUTE, G_X, G_DY, G_INV, G_DX, G_ROW_W, G_ROW_DOT, G_DOT_PART, G_DX_ROUTER,
   G_DX_SHARED, G_NBUF
 };
 
@@ -25,10 +25,7 @@ long long scratch_rows(const moe_cfg_t &c) {
   return padded_rows_ub(expert_rows(c), c.n_experts, row_pad(c.dtype));
 }
 
-// bound of the experts' 256-row tiles
-int pair_tiles_ub(long long rows, int groups) {
-  return (int)(rows / (2 * kRowTile) + (rows < groups ? rows : groups));
-}
+int tile_rows(const moe_cfg_t &c) { return grad_tile_rows(expert_rows(c), c.n_experts); }
 
 size_t larger(size_t a, size_t b) { return a > b ? a : b; }
 
@@ -43,7 +40,7 @@ Layout layout_for(const moe_cfg_t &c) {
   // h / dg / du
   const size_t R = (size_t)scratch_rows(c), Ts = (size_t)padded_rows_ub(c.n_tokens, 1, row_pad(c.dtype));
   const size_t act = larger(R * F, Ts * Fs);
-  const int tiles = m_tiles_ub(expert_rows(c), c.n_experts);
+  const int tiles = grad_tiles_ub(expert_rows(c), c.n_experts, tile_rows(c));
   const bool copies = c.dtype != MOE_DTYPE_F32 || tc;  // of x and dy rows
   size_t sz[G_NBUF];
   sz[G_ERR] = 4 * sizeof(int32_t);
@@ -52,7 +49,8 @@ Layout layout_for(const moe_cfg_t &c) {
   sz[G_H] = act * eb;
   sz[G_DG] = act * eb;
   sz[G_DU] = (glu || Fs ? act : 0) * eb;
-  sz[G_COL] = glu ? 0 : (size_t)col_part_rows((long long)R, tiles, c.dtype) * larger(F, d) * 4;
+  sz[G_COL] = glu ? 0 : (size_t)col_part_rows((long long)R, tiles, c.dtype) * F * 4;
+  sz[G_COL2] = glu ? 0 : (size_t)tiles * d * 4;
   sz[G_DLOGITS] = tc ? T * E * 4 : 0;
   sz[G_ROUTE] = tc ? route_bwd_scratch_bytes(c.n_tokens, c.d_model, c.n_experts, c.dtype) : 0;
   sz[G_X] = copies ? R * d * eb : 0;
@@ -126,8 +124,9 @@ FfnGradArgs expert_args(const moe_cfg_t &c, const moe_weights_t &w, const moe_gr
   a.mprefix = at<int32_t>(ws, L, G_MPREFIX);
   a.poff = at<int32_t>(ws, L, G_POFF);
   a.G = c.n_experts;
-  a.m_tiles_ub = m_tiles_ub(expert_rows(c), c.n_experts);
-  a.pair_tiles_ub = pair_tiles_ub(expert_rows(c), c.n_experts);
+  a.tile_rows = tile_rows(c);
+  a.m_tiles_ub = grad_tiles_ub(expert_rows(c), c.n_experts, a.tile_rows);
+  a.pair_tiles_ub = grad_tiles_ub(expert_rows(c), c.n_experts, 2 * kRowTile);
   a.d = c.d_model;
   a.F = c.d_ff;
   a.act = c.act;
@@ -140,6 +139,7 @@ FfnGradArgs expert_args(const moe_cfg_t &c, const moe_weights_t &w, const moe_gr
   a.dg = at<void>(ws, L, G_DG);
   a.du = at<void>(ws, L, G_DU);
   a.col_part = at<float>(ws, L, G_COL);
+  a.part2 = at<float>(ws, L, G_COL2);
   a.dw1 = g.w1;
   a.dw3 = g.w3;
   a.dw2 = g.w2;
@@ -152,8 +152,9 @@ FfnGradArgs expert_args(const moe_cfg_t &c, const moe_weights_t &w, const moe_gr
 moe_status_t expert_tables(const moe_cfg_t &c, const int32_t *offsets, void *ws, const Layout &L,
                            cudaStream_t st) {
   return cuda_status(launch_grad_tables(
-      offsets, c.n_experts, (int)expert_rows(c), row_pad(c.dtype), at<int32_t>(ws, L, G_OFFSETS),
-      at<int32_t>(ws, L, G_MPREFIX), at<int32_t>(ws, L, G_POFF), at<int32_t>(ws, L, G_ERR), st));
+      offsets, c.n_experts, (int)expert_rows(c), tile_rows(c), row_pad(c.dtype),
+      at<int32_t>(ws, L, G_OFFSETS), at<int32_t>(ws, L, G_MPREFIX), at<int32_t>(ws, L, G_POFF),
+      at<int32_t>(ws, L, G_ERR), st));
 }
 
 // copies of the experts' rows of x and dy, padded
@@ -380,9 +381,10 @@ MOE_API moe_status_t moe_backward(const moe_cfg_t *cfg, const moe_weights_t *w, 
   float *dx_shared = nullptr;
   if (c.n_shared > 0 && (dx || g.ws_gate || g.ws_up || g.ws_down)) {
     FfnGradArgs s{};
+    s.tile_rows = grad_tile_rows(c.n_tokens, 1);
     int32_t *so = at<int32_t>(ws, L, G_SH_OFFSETS), *sm = at<int32_t>(ws, L, G_SH_MPREFIX),
             *sp = at<int32_t>(ws, L, G_SH_POFF);
-    MOE_CUDA(launch_one_group(c.n_tokens, row_pad(c.dtype), so, sm, sp, stream));
+    MOE_CUDA(launch_one_group(c.n_tokens, s.tile_rows, row_pad(c.dtype), so, sm, sp, stream));
     s.x = x;
     s.dy = dy;
     s.x_rows = c.n_tokens;  // the padding rows lie past the operands' bounds: read as zero
@@ -391,7 +393,7 @@ MOE_API moe_status_t moe_backward(const moe_cfg_t *cfg, const moe_weights_t *w, 
     s.mprefix = sm;
     s.poff = s.dx_off = sp;
     s.G = 1;
-    s.m_tiles_ub = ceil_div(c.n_tokens, kRowTile);
+    s.m_tiles_ub = ceil_div(c.n_tokens, s.tile_rows);
     s.pair_tiles_ub = ceil_div(c.n_tokens, 2 * kRowTile);
     s.d = c.d_model;
     s.F = c.n_shared * c.d_ff_shared;
