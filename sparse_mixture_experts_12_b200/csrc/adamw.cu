@@ -24,21 +24,32 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kVec = 8;                            // elements per lane and step
 constexpr int kQBlock = MOE_ADAMW_BLOCK;           // elements of one 8-bit scale: a warp's step
-constexpr int kSteps = 2;                          // steps per thread
-constexpr int kChunk = kThreads * kVec * kSteps;   // elements per CTA
+constexpr int kChunk = kThreads * kVec;            // elements per CTA
 static_assert(kQBlock == 32 * kVec, "a warp's step is one scale block");
 constexpr float kE4M3Max = 448.f;
 constexpr float kE4M3Tiny = 0.001953125f;          // 2^-9, the smallest positive code
 constexpr float kFloor = 7.8886090522101181e-31f;  // 2^-100: keeps 448 / top finite
+
+struct Step {
+  float b1, b2, e1, e2, keep, size, root2, eps, gs;
+  // e1 = 1 - b1, e2 = 1 - b2; keep = 1 - lr wd; size = lr / c1; root2 = 1 / sqrt(c2);
+  // c1 = 1 - b1^t, c2 = 1 - b2^t
+};
+__host__ __device__ inline void set_rates(Step &s, double lr, double decay, double c1, double c2) {
+  s.keep = (float)(1.0 - lr * decay);
+  s.size = (float)(lr / c1);
+  s.root2 = (float)(1.0 / sqrt(c2));
+}
 
 template <int N>
 struct Batch {
   moe_adamw_tensor_t t[N];
   unsigned first[N + 1];  // first CTA of each tensor
   int n;
-  float beta1, beta2, lr, eps, decay;
-  double c1, c2;               // 1 - b1^t, 1 - b2^t (without step_dev)
-  double beta1_d, beta2_d;
+  Step s;                 // without the device scalars
+  // with step_dev or lr_dev the rates are worked out on the device
+  double beta1, beta2, c1, c2;
+  float lr, decay;
   const int64_t *step_dev;
   const float *lr_dev, *grad_scale, *found_inf;
 };
@@ -143,11 +154,6 @@ __device__ __forceinline__ void quantise(uint8_t *codes, float *scale, int n, fl
   if ((threadIdx.x & 31) == 0 && n > 0) *scale = __fmul_rn(top, 1.f / kE4M3Max);
 }
 
-struct Step {
-  float b1, b2, e1, e2, keep, size, root2, eps, gs;
-  // e1 = 1 - b1, e2 = 1 - b2; keep = 1 - lr wd; size = lr / c1; root2 = 1 / sqrt(c2)
-};
-
 // What a lane reads for 8 elements at element i of the tensor (n <= 8 of them exist; none
 // or less: nothing)
 template <typename P, typename G, bool Q>
@@ -207,72 +213,67 @@ struct Lane {
   }
 };
 
-// The chunk's steps: all are requested before the first is worked on. With 8-bit states a
-// warp stays together (its 256 elements share a scale); a warp past the end leaves.
-template <typename P, typename G, bool Q>
-__device__ __forceinline__ void chunk(const moe_adamw_tensor_t &t, size_t base, const Step &s) {
-  Lane<P, G, Q> lane[kSteps];
-  size_t at[kSteps];
-  int n[kSteps];
-#pragma unroll
-  for (int j = 0; j < kSteps; ++j) {
-    at[j] = base + (size_t)j * kThreads * kVec + (size_t)threadIdx.x * kVec;
-    const long long left = (long long)t.n - (long long)at[j];
-    n[j] = left >= 8 ? 8 : (int)(left > 0 ? left : 0);
-    lane[j].load(t, at[j], n[j]);
-  }
-#pragma unroll
-  for (int j = 0; j < kSteps; ++j) {
-    if (Q ? (long long)t.n <= (long long)(at[j] - (threadIdx.x & 31) * kVec) : n[j] == 0) return;
-    lane[j].update(t, at[j], n[j], s);
-  }
+// A CTA's elements: requested, then the step's scalars, then the update. With 8-bit states
+// a warp stays together (its 256 elements share a scale); a warp past the end leaves.
+// Eight elements a thread and five CTAs an SM hide the loads better than longer walks with
+// the next elements prefetched (8-bit states: 1.85 ms against 1.92 to 2.59 at
+// 805 M elements).
+template <typename P, typename G, bool Q, typename F>
+__device__ __forceinline__ void chunk(const moe_adamw_tensor_t &t, size_t base, const F &ready) {
+  const size_t at = base + (size_t)threadIdx.x * kVec;
+  const long long left = (long long)t.n - (long long)at;
+  const int n = left >= 8 ? 8 : (int)(left > 0 ? left : 0);
+  Lane<P, G, Q> lane;
+  lane.load(t, at, n);
+  const Step s = ready();
+  if (Q ? (long long)t.n <= (long long)(at - (threadIdx.x & 31) * kVec) : n == 0) return;
+  lane.update(t, at, n, s);
 }
 
 template <int N>
-__global__ void __launch_bounds__(kThreads) k_adamw(const __grid_constant__ Batch<N> b) {
+__global__ void __launch_bounds__(kThreads, 5) k_adamw(const __grid_constant__ Batch<N> b) {
   // waits for the kernels that wrote the gradients, and never lets the next kernel begin
   // early: the layer's GEMMs read weights before their own wait
-  pdl_wait();
   __shared__ Step sh;
-  if (b.found_inf && *b.found_inf != 0.f) return;  // the step is skipped
-  if (threadIdx.x == 0) {
-    double c1 = b.c1, c2 = b.c2;
-    if (b.step_dev) {
-      const double step = (double)*b.step_dev;
-      c1 = 1.0 - pow(b.beta1_d, step);
-      c2 = 1.0 - pow(b.beta2_d, step);
-    }
-    const double lr = b.lr_dev ? (double)*b.lr_dev : (double)b.lr;
-    sh.b1 = b.beta1;
-    sh.b2 = b.beta2;
-    sh.e1 = (float)(1.0 - b.beta1_d);
-    sh.e2 = (float)(1.0 - b.beta2_d);
-    sh.keep = (float)(1.0 - lr * (double)b.decay);
-    sh.size = (float)(lr / c1);
-    sh.root2 = (float)(1.0 / sqrt(c2));
-    sh.eps = b.eps;
-    sh.gs = b.grad_scale ? *b.grad_scale : 1.f;
-  }
-  __syncthreads();
-  const Step s = sh;
   int lo = 0, hi = b.n - 1;  // last tensor whose first CTA <= this one
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
     if (b.first[mid] <= blockIdx.x) lo = mid; else hi = mid - 1;
   }
+  pdl_wait();
+  if (b.found_inf && *b.found_inf != 0.f) return;  // the step is skipped
+  auto ready = [&]() {
+    Step s = b.s;
+    if (b.step_dev || b.lr_dev) {
+      if (threadIdx.x == 0) {
+        double c1 = b.c1, c2 = b.c2;
+        if (b.step_dev) {
+          const double step = (double)*b.step_dev;
+          c1 = 1.0 - pow(b.beta1, step);
+          c2 = 1.0 - pow(b.beta2, step);
+        }
+        set_rates(s, b.lr_dev ? (double)*b.lr_dev : (double)b.lr, (double)b.decay, c1, c2);
+        sh = s;
+      }
+      __syncthreads();
+      s = sh;
+    }
+    if (b.grad_scale) s.gs = *b.grad_scale;
+    return s;
+  };
   const moe_adamw_tensor_t &t = b.t[lo];
   const size_t base = (size_t)(blockIdx.x - b.first[lo]) * kChunk;
   const bool pf = t.param_dtype == MOE_DTYPE_F32, gf = t.grad_dtype == MOE_DTYPE_F32;
   const bool q = t.state_bits == 8;
   if (pf) {
-    if (gf) q ? chunk<float, float, true>(t, base, s) : chunk<float, float, false>(t, base, s);
-    else q ? chunk<float, __nv_bfloat16, true>(t, base, s)
-           : chunk<float, __nv_bfloat16, false>(t, base, s);
+    if (gf) q ? chunk<float, float, true>(t, base, ready) : chunk<float, float, false>(t, base, ready);
+    else q ? chunk<float, __nv_bfloat16, true>(t, base, ready)
+           : chunk<float, __nv_bfloat16, false>(t, base, ready);
   } else {
-    if (gf) q ? chunk<__nv_bfloat16, float, true>(t, base, s)
-              : chunk<__nv_bfloat16, float, false>(t, base, s);
-    else q ? chunk<__nv_bfloat16, __nv_bfloat16, true>(t, base, s)
-           : chunk<__nv_bfloat16, __nv_bfloat16, false>(t, base, s);
+    if (gf) q ? chunk<__nv_bfloat16, float, true>(t, base, ready)
+              : chunk<__nv_bfloat16, float, false>(t, base, ready);
+    else q ? chunk<__nv_bfloat16, __nv_bfloat16, true>(t, base, ready)
+           : chunk<__nv_bfloat16, __nv_bfloat16, false>(t, base, ready);
   }
 }
 
@@ -282,12 +283,15 @@ static_assert(sizeof(Batch<kFew>) <= 4096 && sizeof(Batch<kMany>) <= 32764, "ker
 template <int N>
 moe_status_t launch(const moe_adamw_tensor_t *ts, int n, const moe_adamw_t &o, cudaStream_t st) {
   Batch<N> b{};
-  b.beta1 = (float)o.beta1;
-  b.beta2 = (float)o.beta2;
-  b.beta1_d = o.beta1;
-  b.beta2_d = o.beta2;
+  b.s.b1 = (float)o.beta1;
+  b.s.b2 = (float)o.beta2;
+  b.s.e1 = (float)(1.0 - o.beta1);
+  b.s.e2 = (float)(1.0 - o.beta2);
+  b.s.eps = o.eps;
+  b.s.gs = 1.f;
+  b.beta1 = o.beta1;
+  b.beta2 = o.beta2;
   b.lr = o.lr;
-  b.eps = o.eps;
   b.decay = o.weight_decay;
   b.step_dev = o.step_dev;
   b.lr_dev = o.lr_dev;
@@ -296,6 +300,7 @@ moe_status_t launch(const moe_adamw_tensor_t *ts, int n, const moe_adamw_t &o, c
   if (!o.step_dev) {
     b.c1 = 1.0 - pow(o.beta1, (double)o.step);
     b.c2 = 1.0 - pow(o.beta2, (double)o.step);
+    set_rates(b.s, o.lr, o.weight_decay, b.c1, b.c2);
   }
   unsigned ctas = 0;
   for (int i = 0; i < n; ++i) {

@@ -126,24 +126,32 @@ __global__ void __launch_bounds__(kThreads) k_combine_bwd(CombineBwdArgs a, int 
   }
 }
 
-// 8 fp32 values (or 4) at a row's vector v: VE of them, from 16-byte loads
-template <int VE>
-__device__ __forceinline__ void load_f32(const float *p, float (&f)[VE]) {
+// VE values as they lie in memory: 16 bytes of bf16, 16 or 32 of fp32
+template <typename TI, int VE>
+struct RawVec {
+  static constexpr int N = VE * (int)sizeof(TI) / 16;
+  uint4 u[N];
+  __device__ __forceinline__ void load(const TI *p) {
 #pragma unroll
-  for (int i = 0; i < VE; i += 4) {
-    const float4 q = __ldg(reinterpret_cast<const float4 *>(p + i));
-    f[i] = q.x; f[i + 1] = q.y; f[i + 2] = q.z; f[i + 3] = q.w;
+    for (int i = 0; i < N; ++i) u[i] = __ldg(reinterpret_cast<const uint4 *>(p) + i);
   }
-}
-__device__ __forceinline__ void load_row(const __nv_bfloat16 *p, float (&f)[8]) {
-  unpack16(__ldg(reinterpret_cast<const uint4 *>(p)), f);
-}
-template <int VE>
-__device__ __forceinline__ void load_row(const float *p, float (&f)[VE]) { load_f32(p, f); }
+  __device__ __forceinline__ void add_to(float (&o)[VE]) const {
+    constexpr int per = VE / N;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      float f[per];
+      unpack16(u[i], f);
+#pragma unroll
+      for (int j = 0; j < per; ++j) o[i * per + j] += f[j];
+    }
+  }
+};
 
 // dx[t] = the kept slots' rows in slot order, then the addends; summed in fp32 and
-// rounded once. TI: the rows' type.
-template <typename T, typename TI, int KMAX, int NB>
+// rounded once. TI: the rows' type. NB vectors of each row and addend are requested before
+// any is used; one slot alone leaves room for four of them (32 -> 24 us on the top-1
+// layer, whose rows are four vectors to a lane).
+template <typename T, typename TI, int KMAX, int NB, int ADDS>
 __global__ void __launch_bounds__(kThreads) k_permute_bwd(PermuteBwdArgs a, int wpt) {
   constexpr int VE = Elem<T>::kPerVec;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -152,6 +160,20 @@ __global__ void __launch_bounds__(kThreads) k_permute_bwd(PermuteBwdArgs a, int 
   pdl_wait();
   pdl_trigger();
   if (t >= a.T) return;
+  const float *add[2] = {a.add0 ? a.add0 + (size_t)t * a.d : nullptr,
+                         a.add1 ? a.add1 + (size_t)t * a.d : nullptr};
+  const int nvec = a.d / VE;
+  RawVec<float, VE> av[ADDS][NB];
+  auto request = [&](int v0) {  // the addends do not wait for the slots' rows to be known
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      const int v = v0 + 32 * wpt * b;
+#pragma unroll
+      for (int i = 0; i < ADDS; ++i)
+        if (add[i] && v < nvec) av[i][b].load(add[i] + (size_t)v * VE);
+    }
+  };
+  request(sub * 32 + lane);
   int row[KMAX];
 #pragma unroll
   for (int s = 0; s < KMAX; ++s)
@@ -159,18 +181,14 @@ __global__ void __launch_bounds__(kThreads) k_permute_bwd(PermuteBwdArgs a, int 
                      : -1;
   const TI *xp = static_cast<const TI *>(a.dx_perm);
   T *dx = static_cast<T *>(a.dx) + (size_t)t * a.d;
-  const int nvec = a.d / VE;
   for (int v0 = sub * 32 + lane; v0 < nvec; v0 += 32 * wpt * NB) {
-    float f[KMAX][NB][VE], add[2][NB][VE];
+    RawVec<TI, VE> f[KMAX][NB];
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
       const int v = v0 + 32 * wpt * b;
-      const bool in = v < nvec;
 #pragma unroll
       for (int s = 0; s < KMAX; ++s)
-        if (row[s] >= 0 && in) load_row(xp + (size_t)row[s] * a.d + (size_t)v * VE, f[s][b]);
-      if (a.add0 && in) load_f32(a.add0 + (size_t)t * a.d + (size_t)v * VE, add[0][b]);
-      if (a.add1 && in) load_f32(a.add1 + (size_t)t * a.d + (size_t)v * VE, add[1][b]);
+        if (row[s] >= 0 && v < nvec) f[s][b].load(xp + (size_t)row[s] * a.d + (size_t)v * VE);
     }
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
@@ -181,20 +199,13 @@ __global__ void __launch_bounds__(kThreads) k_permute_bwd(PermuteBwdArgs a, int 
       for (int i = 0; i < VE; ++i) o[i] = 0.f;
 #pragma unroll
       for (int s = 0; s < KMAX; ++s)
-        if (row[s] >= 0) {
+        if (row[s] >= 0) f[s][b].add_to(o);
 #pragma unroll
-          for (int i = 0; i < VE; ++i) o[i] += f[s][b][i];
-        }
-      if (a.add0) {
-#pragma unroll
-        for (int i = 0; i < VE; ++i) o[i] += add[0][b][i];
-      }
-      if (a.add1) {
-#pragma unroll
-        for (int i = 0; i < VE; ++i) o[i] += add[1][b][i];
-      }
+      for (int i = 0; i < ADDS; ++i)
+        if (add[i]) av[i][b].add_to(o);
       reinterpret_cast<uint4 *>(dx)[v] = pack16(o);
     }
+    request(v0 + 32 * wpt * NB);
   }
 }
 
@@ -331,8 +342,17 @@ template <typename T, typename TI>
 cudaError_t permute_bwd(const PermuteBwdArgs &a, cudaStream_t st) {
   const int wpt = warps_per_token(a.T, a.d / Elem<T>::kPerVec);
   const dim3 g(ceil_div(a.T, kWarps / wpt)), b(kThreads);
-  if (a.k <= 2) return launch_pdl(k_permute_bwd<T, TI, 2, 2>, g, b, 0, st, a, wpt);
-  return launch_pdl(k_permute_bwd<T, TI, kMaxTopK, 1>, g, b, 0, st, a, wpt);
+  auto run = [&](auto kernel) { return launch_pdl(kernel, g, b, 0, st, a, wpt); };
+  if constexpr (sizeof(TI) == 4) {  // the second addend comes with fp32 rows only
+    if (a.add1) {
+      if (a.k == 1) return run(k_permute_bwd<T, TI, 1, 2, 2>);
+      if (a.k == 2) return run(k_permute_bwd<T, TI, 2, 2, 2>);
+      return run(k_permute_bwd<T, TI, kMaxTopK, 1, 2>);
+    }
+  }
+  if (a.k == 1) return run(k_permute_bwd<T, TI, 1, 4, 1>);
+  if (a.k == 2) return run(k_permute_bwd<T, TI, 2, 2, 1>);
+  return run(k_permute_bwd<T, TI, kMaxTopK, 1, 1>);
 }
 
 }  // namespace
