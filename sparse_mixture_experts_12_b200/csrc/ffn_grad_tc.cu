@@ -187,6 +187,15 @@ __device__ __forceinline__ void tear_down(const Setup &s) {
   }
 }
 
+// First row of this CTA's half of row tile m of expert g, or `rows` (past the operand's
+// bounds: zeros, no traffic) when the expert ends before it. The MMAs of such a half take
+// their time all the same, but on zeros, which cost less of the power that limits long
+// grids.
+__device__ __forceinline__ int first_row(const int32_t *poff, int g, int m, int rank, int rows) {
+  const int r = poff[g] + m * kPairM + rank * kRowTile;
+  return r < poff[g + 1] ? r : rows;
+}
+
 // One 32-row x 32-column chunk (a lane's row of 64 bytes) through the warp's 2 KB of
 // shared memory: 16-byte pieces swizzled, one TMA store. The buffer is written again once
 // the store before has read it.
@@ -215,8 +224,7 @@ struct ActArgs {
   const float *b1, *row_w;
   float *dot_part;  // [F / 32, rows] or nullptr
   float *col_part;  // [rows / 32, F] or nullptr
-  void *h, *dg, *du;
-  int rows;
+  int rows, x_rows;
   int32_t *err;
 };
 struct ActMaps {
@@ -294,7 +302,7 @@ k_act_grad(const __grid_constant__ ActMaps maps, ActArgs a) {
     for (int t = s.c0; ok && t < total; t += s.cstep) {
       int g, n, m;
       decode_tile(t, ctl->pre, a.G, a.n_tiles, g, n, m);
-      const int arow = a.poff[g] + m * kPairM + s.rank * kRowTile;
+      const int arow = first_row(a.poff, g, m, s.rank, a.x_rows);
       const int col = n * kTileN + s.rank * kBlockK, brow = g * a.d;
       for (int i = 0; i < nkb; ++i) {
         uint8_t *st = ring.acquire(s, C::kBytesQ, a.err, 21);
@@ -317,7 +325,7 @@ k_act_grad(const __grid_constant__ ActMaps maps, ActArgs a) {
     for (int t = s.c0; ok && t < total; t += s.cstep) {
       int g, n, m;
       decode_tile(t, ctl->pre, a.G, a.n_tiles, g, n, m);
-      const int arow = a.poff[g] + m * kPairM + s.rank * kRowTile;
+      const int arow = first_row(a.poff, g, m, s.rank, a.x_rows);
       const int brow = g * a.F + n * kTileN + (GLU ? 0 : s.rank * kBlockK);
       for (int i = 0; i < nkb; ++i) {
         uint8_t *st = ring.acquire(s, C::kBytesA, a.err, 21);
@@ -498,7 +506,7 @@ struct GemmArgs {
   const int32_t *dx_off;  // first row of each expert in dx
   int G;
   // dx: N = d, K = F, nseg pairs (A, B) added. Weights: njobs products of M x N.
-  int N, K, nseg;
+  int N, K, nseg, a_rows;
   int M[3], Ns[3], njobs;
   void *out;              // dx; fp32 weights' gradients
   int out_f32;
@@ -544,7 +552,8 @@ k_pair_gemm(const __grid_constant__ GemmMaps maps, GemmArgs a) {
   // a tile: expert, job (weights), first row and column, K slices; and the walk over
   // every cstep-th of them
   struct Tile {
-    int t, g, in, job, m0, n0, nkb, row0;
+    int t, g, in, job, m0, n0, nkb;
+    int row0;  // weights: the reduction's first row; dx: this CTA's first row of A
   };
   const int nk1 = ceil_div(a.K, kBlockK);
   auto place = [&](Tile &r) {
@@ -572,7 +581,7 @@ k_pair_gemm(const __grid_constant__ GemmMaps maps, GemmArgs a) {
       r.m0 = m * kPairM;
       r.n0 = n * 256;
       r.nkb = a.nseg * nk1;
-      r.row0 = a.poff[r.g];
+      r.row0 = first_row(a.poff, r.g, m, s.rank, a.a_rows);
     }
   };
   auto first_tile = [&]() {
@@ -608,7 +617,7 @@ k_pair_gemm(const __grid_constant__ GemmMaps maps, GemmArgs a) {
           tma_load_3d_pair(&maps.b[q.job], bar, st + kOperand, 0, r, bblk);
         } else {
           const int k0 = k * kBlockK;
-          tma_load_2d_pair(&maps.a[seg], bar, st, k0, row0 + q.m0 + s.rank * kRowTile);
+          tma_load_2d_pair(&maps.a[seg], bar, st, k0, row0);
           tma_load_3d_pair(&maps.b[seg], bar, st + kOperand, 0, q.g * a.K + k0, bblk);
           if (++k == nk1) {
             k = 0;
@@ -823,6 +832,7 @@ cudaError_t launch_act_grad_tc(const FfnGradArgs &f, cudaStream_t st) {
   a.dot_part = f.row_dot ? f.dot_part : nullptr;
   a.col_part = f.db1 ? f.col_part : nullptr;
   a.rows = f.rows;
+  a.x_rows = f.x_rows;
   a.err = f.err;
   const long long tiles = (long long)f.pair_tiles_ub * a.n_tiles;
   return glu ? launch_pairs(k_act_grad<true>, 0, ActCfg<true>::kThreads, ActCfg<true>::kSmem,
@@ -850,6 +860,7 @@ cudaError_t launch_dx_tc(const FfnGradArgs &f, cudaStream_t st) {
   a.N = f.d;
   a.K = f.F;
   a.nseg = glu ? 2 : 1;
+  a.a_rows = f.rows;
   a.out = f.dx;
   a.out_f32 = f.dx_f32;
   a.clipped = f.dx_off == f.poff;  // the rows behind an expert's are its own padding
@@ -904,6 +915,7 @@ cudaError_t launch_route_dx_tc(const RouteTcArgs &r, cudaStream_t st) {
   a.N = r.d;
   a.K = r.Ep;
   a.nseg = kSplit;
+  a.a_rows = r.T;
   a.out = r.dx;
   a.out_f32 = 1;
   a.err = r.err;
