@@ -310,10 +310,11 @@ __global__ void __launch_bounds__(kThreads) k_products(FfnGradArgs s, Products p
 }
 
 // One warp: offsets -> checked copy (all zero when they are no partition of at most
-// max_rows rows), the tile prefix, and the prefix of the row counts rounded up to
+// max_rows rows), the prefixes of their tiles, and the prefix of the row counts rounded up to
 // multiples of `pad`.
 __global__ void k_grad_tables(const int32_t *offsets, int G, int max_rows, int unit,
-                              int pad, int32_t *checked, int32_t *mprefix, int32_t *poff, int32_t *err) {
+                              int pad, int32_t *checked, int32_t *mprefix, int32_t *pre256,
+                              int32_t *poff, int32_t *err) {
   pdl_wait();
   pdl_trigger();
   const int lane = threadIdx.x;
@@ -325,51 +326,60 @@ __global__ void k_grad_tables(const int32_t *offsets, int G, int max_rows, int u
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) bad = min(bad, __shfl_xor_sync(0xffffffffu, bad, o));
   const bool ok = bad == G;
-  int sm = 0, sp = 0, mt[8], pr[8];
+  int sm = 0, s2 = 0, sp = 0, mt[8], m2[8], pr[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) {  // G <= 256: eight groups per lane
     const int g = lane * 8 + j;
     const int n = (ok && g < G) ? offsets[g + 1] - offsets[g] : 0;
     mt[j] = ceil_div(n, unit);
     pr[j] = ceil_div(n, pad) * pad;
+    m2[j] = ceil_div(n, 2 * kRowTile);
     sm += mt[j];
+    s2 += m2[j];
     sp += pr[j];
   }
-  int im = sm, ip = sp;
+  int im = sm, i2 = s2, ip = sp;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int v = __shfl_up_sync(0xffffffffu, im, o), u = __shfl_up_sync(0xffffffffu, ip, o);
+    const int w = __shfl_up_sync(0xffffffffu, i2, o);
     if (lane >= o) {
       im += v;
+      i2 += w;
       ip += u;
     }
   }
-  int rm = im - sm, rp = ip - sp;
+  int rm = im - sm, r2 = i2 - s2, rp = ip - sp;
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     const int g = lane * 8 + j;
     if (g < G) {
       mprefix[g] = rm;
+      pre256[g] = r2;
       poff[g] = rp;
       checked[g] = ok ? offsets[g] : 0;
     }
     rm += mt[j];
+    r2 += m2[j];
     rp += pr[j];
   }
   if (lane == 31) {
     mprefix[G] = im;
+    pre256[G] = i2;
     poff[G] = ip;
     checked[G] = ok ? offsets[G] : 0;
   }
   if (!ok && lane == 0) report_error(err, MOE_DEVERR_OFFSETS, bad);
 }
 
-__global__ void k_one_group(int n, int unit, int pad, int32_t *offsets, int32_t *mprefix, int32_t *poff) {
+__global__ void k_one_group(int n, int unit, int pad, int32_t *offsets, int32_t *mprefix, int32_t *pre256,
+                            int32_t *poff) {
   pdl_wait();
   pdl_trigger();
-  offsets[0] = mprefix[0] = poff[0] = 0;
+  offsets[0] = mprefix[0] = pre256[0] = poff[0] = 0;
   offsets[1] = n;
   mprefix[1] = ceil_div(n, unit);
+  pre256[1] = ceil_div(n, 2 * kRowTile);
   poff[1] = ceil_div(n, pad) * pad;
 }
 
@@ -408,7 +418,7 @@ cudaError_t ffn_bwd_f32(const FfnGradArgs &a, cudaStream_t st) {
   return launch_pdl(k_products<T, VEC>, dim3(blocks), b, 0, st, a, p, q);
 }
 
-// bf16: the three steps on the tensor cores
+// bf16: the steps on the tensor cores
 cudaError_t ffn_bwd_tc(const FfnGradArgs &a, cudaStream_t st) {
   cudaError_t e = cudaSuccess;
   if (a.db2) {
@@ -427,25 +437,22 @@ cudaError_t ffn_bwd_tc(const FfnGradArgs &a, cudaStream_t st) {
                    q);
     if (e != cudaSuccess) return e;
   }
-  if (a.dx) {
-    e = launch_dx_tc(a, st);
-    if (e != cudaSuccess) return e;
-  }
-  return launch_dw_tc(a, st);
+  return launch_products_tc(a, st);
 }
 
 }  // namespace
 
 cudaError_t launch_grad_tables(const int32_t *offsets, int G, int max_rows, int unit, int pad,
-                               int32_t *checked, int32_t *mprefix, int32_t *poff, int32_t *err,
-                               cudaStream_t st) {
+                               int32_t *checked, int32_t *mprefix, int32_t *pre256, int32_t *poff,
+                               int32_t *err, cudaStream_t st) {
   return launch_pdl(k_grad_tables, dim3(1), dim3(32), 0, st, offsets, G, max_rows, unit, pad, checked,
-                    mprefix, poff, err);
+                    mprefix, pre256, poff, err);
 }
 
-cudaError_t launch_one_group(int n, int unit, int pad, int32_t *offsets, int32_t *mprefix, int32_t *poff,
-                             cudaStream_t st) {
-  return launch_pdl(k_one_group, dim3(1), dim3(1), 0, st, n, unit, pad, offsets, mprefix, poff);
+cudaError_t launch_one_group(int n, int unit, int pad, int32_t *offsets, int32_t *mprefix,
+                             int32_t *pre256, int32_t *poff, cudaStream_t st) {
+  return launch_pdl(k_one_group, dim3(1), dim3(1), 0, st, n, unit, pad, offsets, mprefix, pre256,
+                    poff);
 }
 
 cudaError_t launch_ffn_bwd(const FfnGradArgs &a, int dtype, cudaStream_t st) {

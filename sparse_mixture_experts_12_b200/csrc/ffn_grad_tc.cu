@@ -1,10 +1,10 @@
 // Gradient of the grouped expert FFN on the 5th-generation tensor cores (bf16 layers):
-// the formulas of ffn_grad.cu as three persistent grids of CTA pairs.
+// the formulas of ffn_grad.cu as two persistent grids of CTA pairs.
 //
 //   k_act_grad    a = x W1^T (and u = x W3^T) and q = dy W2, reduction length d, into
 //                 tensor memory together; the epilogue turns them into h, da, du
-//   k_pair_gemm   dx = da W1 (+ du W3), reduction length F (2 F)
-//   k_pair_gemm   dW1 = da^T x, dW3 = du^T x, dW2 = dy^T h, reduction over an expert's rows
+//   k_pair_gemm   dx = da W1 (+ du W3), reduction length F (2 F), and
+//                 dW1 = da^T x, dW3 = du^T x, dW2 = dy^T h, reduction over an expert's rows
 //
 // Every product is a 256-row tcgen05.mma.cta_group::2 over K slices of 64; operands whose
 // contiguous index is not the reduction's (W2 in q, W1 / W3 in dx, both in the weights'
@@ -501,21 +501,28 @@ k_act_grad(const __grid_constant__ ActMaps maps, ActArgs a) {
 }
 
 // ============================================================ dx and the weights
+// Two kinds of products in one grid, so that the last tiles of one overlap the first of the
+// other and a small layer pays for one launch: "rows" products C = sum of nseg A B over the
+// groups' rows (dx), and "sums" C = A^T B over a group's rows (the weights' gradients).
 struct GemmArgs {
-  const int32_t *poff, *offsets;
-  const int32_t *dx_off;  // first row of each expert in dx
-  int G;
-  // dx: N = d, K = F, nseg pairs (A, B) added. Weights: njobs products of M x N.
-  int N, K, nseg, a_rows;
-  int M[3], Ns[3], njobs;
-  void *out;              // dx; fp32 weights' gradients
+  // rows: groups' first (padded) rows, row counts, prefix of their 256-row tiles, first rows
+  // in the output; N columns, reduction length K
+  const int32_t *poff, *offsets, *pre, *out_off;
+  int G, N, K, nseg, a_rows;
+  void *out;
   int out_f32;
-  int clipped;            // dx: no other rows lie in an expert's last group of 32 (padding, or
-                          // the output ends and its map clips the stores)
+  int clipped;            // no other rows lie in a group's last 32 (padding, or the output
+                          // ends and its map clips the stores)
+  // sums: groups' first rows (multiples of 64); njobs products of M x N each, fp32 or bf16
+  const int32_t *first;
+  int groups, njobs;
+  int M[3], Ns[3];
+  float *sum_out;         // fp32
   int32_t *err;
 };
 struct GemmMaps {
-  CUtensorMap a[3], b[3], o[3];
+  CUtensorMap a[3], b[3], o;      // rows
+  CUtensorMap sa[3], sb[3], so[3];  // sums
 };
 constexpr int kGemmStages = 5, kGemmStageBytes = 2 * kOperand;
 constexpr int kGemmEpiWarps = 16, kGemmThreads = 128 + 32 * kGemmEpiWarps;
@@ -525,59 +532,62 @@ constexpr size_t kGemmBytes = kGemmRing + (size_t)kGemmEpiWarps * kStageOut;
 constexpr size_t kGemmSmem = kGemmBytes + sizeof(Ctl) + 1024;
 using GemmRing = Ring<kGemmStages, 0, kGemmStageBytes>;
 
-template <bool DW>
 __global__ void __launch_bounds__(kGemmThreads, 1)
 k_pair_gemm(const __grid_constant__ GemmMaps maps, GemmArgs a) {
   extern __shared__ uint8_t smem_raw[];
-  const Setup s = set_up(smem_raw, kGemmBytes, 1, 2 * kGemmEpiWarps, a.poff, a.G, DW ? 0 : kPairM);
+  // the groups' first rows of the sums stay in shared memory: their tiles can be short
+  const Setup s = set_up(smem_raw, kGemmBytes, 1, 2 * kGemmEpiWarps, a.first, a.groups, 0);
   Ctl *ctl = s.ctl;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  // weights: an expert's tiles are those of job 0, then 1, then 2 (ends: their prefix)
+  // sums: a group's tiles are those of job 0, then 1, then 2 (end: their prefix)
   int mt[3] = {1, 1, 1}, end[3] = {0, 0, 0};
   float inv[3] = {1.f, 1.f, 1.f};
-  if (DW) {
 #pragma unroll
-    for (int j = 0; j < 3; ++j) {
-      if (j > 0) end[j] = end[j - 1];
-      if (j < a.njobs) {
-        mt[j] = ceil_div(a.M[j], kPairM);
-        inv[j] = 1.f / (float)mt[j];
-        end[j] += mt[j] * ceil_div(a.Ns[j], 256);
-      }
+  for (int j = 0; j < 3; ++j) {
+    if (j > 0) end[j] = end[j - 1];
+    if (j < a.njobs) {
+      mt[j] = ceil_div(a.M[j], kPairM);
+      inv[j] = 1.f / (float)mt[j];
+      end[j] += mt[j] * ceil_div(a.Ns[j], 256);
     }
   }
-  const int per = end[2];
-  const int n_tiles = ceil_div(a.N, 256);
-  const int total = DW ? a.G * per : ctl->pre[a.G] * n_tiles;
-  // a tile: expert, job (weights), first row and column, K slices; and the walk over
-  // every cstep-th of them
+  const int per = end[2], n_tiles = ceil_div(a.N, 256);
+  const int row_tiles = n_tiles ? a.pre[a.G] * n_tiles : 0;
+  const int total = row_tiles + a.groups * per;
+  // a tile: group, job (sums), first row and column, K slices; and the walk over every
+  // cstep-th of them
   struct Tile {
-    int t, g, in, job, m0, n0, nkb;
-    int row0;  // weights: the reduction's first row; dx: this CTA's first row of A
+    int t, g, job, m0, n0, nkb;
+    int row0;   // sums: the reduction's first row; rows: this CTA's first row of A
+    bool sums;
   };
   const int nk1 = ceil_div(a.K, kBlockK);
   auto place = [&](Tile &r) {
-    if (DW) {
-      while (r.in >= per) {
-        r.in -= per;
+    if (r.t >= total) return;
+    if (r.t >= row_tiles) {
+      if (!r.sums) {
+        r.sums = true;
+        r.g = 0;
+      }
+      int in = r.t - row_tiles - r.g * per;
+      while (in >= per) {
+        in -= per;
         ++r.g;
       }
-      if (r.g >= a.G) return;
-      r.job = (r.in >= end[0]) + (r.in >= end[1]);
-      const int first = r.job == 0 ? 0 : (r.job == 1 ? end[0] : end[1]);
+      r.job = (in >= end[0]) + (in >= end[1]);
       const int mts = r.job == 0 ? mt[0] : (r.job == 1 ? mt[1] : mt[2]);
+      const float by = r.job == 0 ? inv[0] : (r.job == 1 ? inv[1] : inv[2]);
+      in -= r.job == 0 ? 0 : (r.job == 1 ? end[0] : end[1]);
       // n = in / mts (single-thread roles pay for a division in full): exact, since in is
       // below 2^20 and half a tile is more than the product's error
-      const float by = r.job == 0 ? inv[0] : (r.job == 1 ? inv[1] : inv[2]);
-      const int n = __float2int_rd(((float)(r.in - first) + 0.5f) * by);
-      r.m0 = (r.in - first - n * mts) * kPairM;
+      const int n = __float2int_rd(((float)in + 0.5f) * by);
+      r.m0 = (in - n * mts) * kPairM;
       r.n0 = n * 256;
       r.row0 = ctl->pre[r.g];
       r.nkb = (ctl->pre[r.g + 1] - r.row0) / kBlockK;
     } else {
-      if (r.t >= total) return;
       int n, m;
-      decode_tile(r.t, ctl->pre, a.G, n_tiles, r.g, n, m);
+      decode_tile(r.t, a.pre, a.G, n_tiles, r.g, n, m);
       r.m0 = m * kPairM;
       r.n0 = n * 256;
       r.nkb = a.nseg * nk1;
@@ -585,21 +595,24 @@ k_pair_gemm(const __grid_constant__ GemmMaps maps, GemmArgs a) {
     }
   };
   auto first_tile = [&]() {
-    Tile r{s.c0, 0, s.c0, 0, 0, 0, 0, 0};
+    Tile r{s.c0, 0, 0, 0, 0, 0, 0, false};
     place(r);
     return r;
   };
   auto next_tile = [&](Tile &r) {
     r.t += s.cstep;
-    r.in += s.cstep;
     place(r);
   };
 
   if (warp == 0 && lane == 0) {
     // ------------------------------------------------------------ TMA producer
-    for (int j = 0; j < max(a.njobs, a.nseg); ++j) {
+    for (int j = 0; n_tiles && j < a.nseg; ++j) {
       prefetch_map(&maps.a[j]);
       prefetch_map(&maps.b[j]);
+    }
+    for (int j = 0; j < a.njobs; ++j) {
+      prefetch_map(&maps.sa[j]);
+      prefetch_map(&maps.sb[j]);
     }
     const uint32_t full0 = mapa_rank(smem_u32(&ctl->full[0]), 0);
     GemmRing ring(s.smem);
@@ -611,10 +624,10 @@ k_pair_gemm(const __grid_constant__ GemmMaps maps, GemmArgs a) {
         uint8_t *st = ring.acquire(s, kGemmStageBytes, a.err, 31);
         if (!(ok = st != nullptr)) break;
         const uint32_t bar = ring.bar(full0);
-        if (DW) {
+        if (q.sums) {
           const int r = row0 + kb * kBlockK;
-          tma_load_3d_pair(&maps.a[q.job], bar, st, 0, r, q.m0 / kBlockK + 2 * s.rank);
-          tma_load_3d_pair(&maps.b[q.job], bar, st + kOperand, 0, r, bblk);
+          tma_load_3d_pair(&maps.sa[q.job], bar, st, 0, r, q.m0 / kBlockK + 2 * s.rank);
+          tma_load_3d_pair(&maps.sb[q.job], bar, st + kOperand, 0, r, bblk);
         } else {
           const int k0 = k * kBlockK;
           tma_load_2d_pair(&maps.a[seg], bar, st, k0, row0);
@@ -630,8 +643,6 @@ k_pair_gemm(const __grid_constant__ GemmMaps maps, GemmArgs a) {
     ring.drain(s, ok);
   } else if (warp == 1 && lane == 0 && s.rank == 0) {
     // --------------------------------------------------------------- MMA issuer
-    constexpr uint32_t idesc = make_idesc(kPairM, 256) | kIdescMnB | (DW ? kIdescMnA : 0u);
-    constexpr int kStepA = DW ? 128 : 2;  // a K = 16 step in the A descriptor
     GemmRing ring(s.smem);
     bool ok = true, any = false;
     int it = 0;
@@ -640,13 +651,16 @@ k_pair_gemm(const __grid_constant__ GemmMaps maps, GemmArgs a) {
       if (!(ok = wait_on(s, &ctl->tempty[buf], ((it >> 1) & 1) ^ 1u, a.err, 32))) break;
       tc_fence_after();
       const uint32_t acc = s.tmem + (uint32_t)(buf * 256);
+      const uint32_t idesc = make_idesc(kPairM, 256) | kIdescMnB | (q.sums ? kIdescMnA : 0u);
+      const uint64_t step_a = q.sums ? 128 : 2;  // a K = 16 step in the A descriptor
       for (int kb = 0; kb < q.nkb; ++kb) {
         if (!(ok = ring.filled(s, a.err, 33))) break;
-        const uint64_t xa = DW ? sw128_desc_mn(ring.addr(), kMnBlock) : sw128_desc(ring.addr());
+        const uint64_t xa =
+            q.sums ? sw128_desc_mn(ring.addr(), kMnBlock) : sw128_desc(ring.addr());
         const uint64_t xb = sw128_desc_mn(ring.addr() + kOperand, kMnBlock);
 #pragma unroll
         for (int kk = 0; kk < kBlockK / 16; ++kk)
-          umma_bf16_pair(acc, xa + kStepA * kk, xb + 128 * kk, idesc, (kb | kk) != 0);
+          umma_bf16_pair(acc, xa + step_a * kk, xb + 128 * kk, idesc, (kb | kk) != 0);
         any = true;
         ring.release(s);
         ring.next();
@@ -665,19 +679,23 @@ k_pair_gemm(const __grid_constant__ GemmMaps maps, GemmArgs a) {
       const int lrow = q.m0 + s.rank * kRowTile + ew * 32, col0 = q.n0 + part * 64;
       int rows, N;      // the output's valid rows from q's first, its width
       size_t orow;      // output row of lane 0
-      if (DW) {
+      if (q.sums) {
         rows = q.job == 0 ? a.M[0] : (q.job == 1 ? a.M[1] : a.M[2]);
         N = q.job == 0 ? a.Ns[0] : (q.job == 1 ? a.Ns[1] : a.Ns[2]);
         orow = (size_t)q.g * rows + lrow;
       } else {
         rows = a.offsets[q.g + 1] - a.offsets[q.g];
         N = a.N;
-        orow = (size_t)a.dx_off[q.g] + lrow;
+        orow = (size_t)a.out_off[q.g] + lrow;
       }
       const bool mine = lrow < rows && col0 < N;  // N is a multiple of 64
       const bool valid = lrow + lane < rows;
       // full groups of 32 rows leave through TMA stores, others row by row
-      const bool staged = lrow + 32 <= rows || a.clipped;
+      const bool staged = lrow + 32 <= rows || (!q.sums && a.clipped);
+      const bool f32 = q.sums ? a.sum_out != nullptr : a.out_f32;
+      const CUtensorMap *map = q.sums ? &maps.so[q.job] : &maps.o;
+      void *out = q.sums ? a.sum_out : a.out;  // (bf16 sums are always staged: M is a
+                                               // multiple of 64)
       bool ok = wait_on(s, &ctl->tfull[buf], (it >> 1) & 1, a.err, 34);
       __syncwarp();
       if (!__all_sync(0xffffffffu, ok)) break;
@@ -691,7 +709,7 @@ k_pair_gemm(const __grid_constant__ GemmMaps maps, GemmArgs a) {
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           float f[32];
-          if (DW && q.nkb == 0) {  // an expert without rows
+          if (q.nkb == 0) {  // an expert without rows
 #pragma unroll
             for (int j = 0; j < 32; ++j) f[j] = 0.f;
           } else {
@@ -701,7 +719,7 @@ k_pair_gemm(const __grid_constant__ GemmMaps maps, GemmArgs a) {
 #pragma unroll
             for (int j = 0; j < 32; ++j) f[j] = __uint_as_float(v[j]);
           }
-          if (a.out_f32 && staged) {  // 32 rows of 128 bytes, 16-byte pieces swizzled
+          if (f32 && staged) {  // 32 rows of 128 bytes, 16-byte pieces swizzled
             if (c > 0) {
               if (lane == 0) bulk_wait_read<0>();
               __syncwarp();
@@ -713,12 +731,12 @@ k_pair_gemm(const __grid_constant__ GemmMaps maps, GemmArgs a) {
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {
-              tma_store_2d(&maps.o[q.job], stage, col0 + c * 32, (int)orow);
+              tma_store_2d(map, stage, col0 + c * 32, (int)orow);
               bulk_commit();
             }
-          } else if (a.out_f32) {
+          } else if (f32) {
             if (valid) {
-              float4 *dst = reinterpret_cast<float4 *>(static_cast<float *>(a.out) +
+              float4 *dst = reinterpret_cast<float4 *>(static_cast<float *>(out) +
                                                        (orow + lane) * (size_t)N + col0 + c * 32);
 #pragma unroll
               for (int j = 0; j < 8; ++j)
@@ -727,7 +745,7 @@ k_pair_gemm(const __grid_constant__ GemmMaps maps, GemmArgs a) {
           } else if (valid) {
             // staged: the lane's row of 128 bytes, 16-byte pieces swizzled
             uint4 *dst = staged ? reinterpret_cast<uint4 *>(stage + lane * 128)
-                                : reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) +
+                                : reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(out) +
                                                             (orow + lane) * (size_t)N + col0);
             const int sw = staged ? lane & 7 : 0;
 #pragma unroll
@@ -743,11 +761,11 @@ k_pair_gemm(const __grid_constant__ GemmMaps maps, GemmArgs a) {
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive_remote(tempty0 + (uint32_t)(buf * sizeof(uint64_t)));
-      if (mine && staged && !a.out_f32) {
+      if (mine && staged && !f32) {
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
-          tma_store_2d(&maps.o[q.job], stage, col0, (int)orow);
+          tma_store_2d(map, stage, col0, (int)orow);
           bulk_commit();
         }
       }
@@ -766,7 +784,7 @@ std::mutex g_mu;
 template <typename... KArgs, typename... Args>
 cudaError_t launch_pairs(void (*kernel)(KArgs...), int slot, int threads, size_t smem,
                          long long tiles, cudaStream_t st, const Args &...args) {
-  static int max_pairs[64][4] = {};
+  static int max_pairs[64][3] = {};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
@@ -841,107 +859,98 @@ cudaError_t launch_act_grad_tc(const FfnGradArgs &f, cudaStream_t st) {
                             tiles, st, m, a);
 }
 
-cudaError_t launch_dx_tc(const FfnGradArgs &f, cudaStream_t st) {
+cudaError_t launch_products_tc(const FfnGradArgs &f, cudaStream_t st) {
   const bool glu = f.act == MOE_ACT_SWIGLU;
-  const uint64_t R = (uint64_t)f.rows, d = (uint64_t)f.d, F = (uint64_t)f.F, G = (uint64_t)f.G;
-  GemmMaps m;
-  bool ok = make_map(&m.a[0], f.dg, R, F, kRowTile) && make_mn_map(&m.b[0], f.w1, G * F, d);
-  if (glu)
-    ok = ok && make_map(&m.a[1], f.du, R, F, kRowTile) &&
-         make_mn_map(&m.b[1], f.w3, G * F, d);
-  ok = ok && (f.dx_f32 ? make_f32_map(&m.o[0], f.dx, (uint64_t)f.dx_rows, d)
-                       : make_map(&m.o[0], f.dx, (uint64_t)f.dx_rows, d, 32));
-  if (!ok) return cudaErrorInvalidValue;
-  GemmArgs a{};
-  a.poff = f.poff;
-  a.offsets = f.offsets;
-  a.dx_off = f.dx_off;
-  a.G = f.G;
-  a.N = f.d;
-  a.K = f.F;
-  a.nseg = glu ? 2 : 1;
-  a.a_rows = f.rows;
-  a.out = f.dx;
-  a.out_f32 = f.dx_f32;
-  a.clipped = f.dx_off == f.poff;  // the rows behind an expert's are its own padding
-  a.err = f.err;
-  return launch_pairs(k_pair_gemm<false>, 2, kGemmThreads, kGemmSmem,
-                      (long long)f.pair_tiles_ub * ceil_div(f.d, 256), st,
-                      m, a);
-}
-
-cudaError_t launch_dw_tc(const FfnGradArgs &f, cudaStream_t st) {
-  const uint64_t R = (uint64_t)f.rows, X = (uint64_t)f.x_rows, G = (uint64_t)f.G;
+  const uint64_t R = (uint64_t)f.rows, X = (uint64_t)f.x_rows, d = (uint64_t)f.d,
+                 F = (uint64_t)f.F, G = (uint64_t)f.G;
   GemmMaps m;
   GemmArgs a{};
   bool ok = true;
   long long tiles = 0;
+  if (f.dx) {
+    ok = make_map(&m.a[0], f.dg, R, F, kRowTile) && make_mn_map(&m.b[0], f.w1, G * F, d);
+    if (glu)
+      ok = ok && make_map(&m.a[1], f.du, R, F, kRowTile) && make_mn_map(&m.b[1], f.w3, G * F, d);
+    ok = ok && (f.dx_f32 ? make_f32_map(&m.o, f.dx, (uint64_t)f.dx_rows, d)
+                         : make_map(&m.o, f.dx, (uint64_t)f.dx_rows, d, 32));
+    a.poff = f.poff;
+    a.offsets = f.offsets;
+    a.pre = f.pre256;
+    a.out_off = f.dx_off;
+    a.G = f.G;
+    a.N = f.d;
+    a.K = f.F;
+    a.nseg = glu ? 2 : 1;
+    a.a_rows = f.rows;
+    a.out = f.dx;
+    a.out_f32 = f.dx_f32;
+    a.clipped = f.dx_off == f.poff;  // the rows behind an expert's are its own padding
+    tiles += (long long)f.pair_tiles_ub * ceil_div(f.d, 256);
+  }
   auto job = [&](const void *p, uint64_t prows, const void *q, uint64_t qrows, void *out, int M,
                  int N) {
     if (out == nullptr) return;
     const int j = a.njobs++;
-    ok = ok && make_mn_map(&m.a[j], p, prows, (uint64_t)M) &&
-         make_mn_map(&m.b[j], q, qrows, (uint64_t)N) &&
-         make_map(&m.o[j], out, G * (uint64_t)M, (uint64_t)N, 32);
+    ok = ok && make_mn_map(&m.sa[j], p, prows, (uint64_t)M) &&
+         make_mn_map(&m.sb[j], q, qrows, (uint64_t)N) &&
+         make_map(&m.so[j], out, G * (uint64_t)M, (uint64_t)N, 32);
     a.M[j] = M;
     a.Ns[j] = N;
     tiles += (long long)f.G * ceil_div(M, kPairM) * ceil_div(N, 256);
   };
   job(f.dg, R, f.x, X, f.dw1, f.F, f.d);
-  if (f.act == MOE_ACT_SWIGLU) job(f.du, R, f.x, X, f.dw3, f.F, f.d);
+  if (glu) job(f.du, R, f.x, X, f.dw3, f.F, f.d);
   job(f.dy, X, f.h, R, f.dw2, f.d, f.F);
-  if (a.njobs == 0) return cudaSuccess;
+  if (tiles == 0) return cudaSuccess;
   if (!ok) return cudaErrorInvalidValue;
-  a.poff = f.poff;
-  a.offsets = f.offsets;
-  a.G = f.G;
+  a.first = f.poff;
+  a.groups = f.G;
   a.err = f.err;
-  return launch_pairs(k_pair_gemm<true>, 3, kGemmThreads, kGemmSmem, tiles, st, m, a);
+  return launch_pairs(k_pair_gemm, 2, kGemmThreads, kGemmSmem, tiles, st, m, a);
 }
 
-cudaError_t launch_route_dx_tc(const RouteTcArgs &r, cudaStream_t st) {
+cudaError_t launch_route_tc(const RouteTcArgs &r, cudaStream_t st) {
   GemmMaps m;
   GemmArgs a{};
-  for (int j = 0; j < kSplit; ++j)
-    if (!make_map(&m.a[j], r.terms + (size_t)j * r.Ep, (uint64_t)r.T, (uint64_t)r.Ep, kRowTile,
-                  (uint64_t)kSplit * r.Ep) ||
-        !make_mn_map(&m.b[j], r.w, (uint64_t)r.E, (uint64_t)r.d))
-      return cudaErrorInvalidValue;
-  if (!make_f32_map(&m.o[0], r.dx, (uint64_t)r.T, (uint64_t)r.d)) return cudaErrorInvalidValue;
-  a.clipped = 1;
-  a.poff = r.all;
-  a.offsets = a.dx_off = r.all_rows;
-  a.G = 1;
-  a.N = r.d;
-  a.K = r.Ep;
-  a.nseg = kSplit;
-  a.a_rows = r.T;
-  a.out = r.dx;
-  a.out_f32 = 1;
+  bool ok = true;
+  long long tiles = 0;
+  const uint64_t T = (uint64_t)r.T, ld = (uint64_t)kSplit * r.Ep, d = (uint64_t)r.d;
+  if (r.dx) {
+    for (int j = 0; j < kSplit; ++j)
+      ok = ok &&
+           make_map(&m.a[j], r.terms + (size_t)j * r.Ep, T, (uint64_t)r.Ep, kRowTile, ld) &&
+           make_mn_map(&m.b[j], r.w, (uint64_t)r.E, d);
+    ok = ok && make_f32_map(&m.o, r.dx, T, d);
+    a.poff = r.all;
+    a.offsets = a.out_off = r.all_rows;
+    a.pre = r.all_tiles;
+    a.G = 1;
+    a.N = r.d;
+    a.K = r.Ep;
+    a.nseg = kSplit;
+    a.a_rows = r.T;
+    a.out = r.dx;
+    a.out_f32 = 1;
+    a.clipped = 1;
+    tiles += (long long)ceil_div(r.T, kPairM) * ceil_div(r.d, 256);
+  }
+  if (r.dw_part) {
+    // the terms side by side are the rows of one product: x is read once for both
+    const int M = kSplitDw * r.Ep;
+    ok = ok && make_mn_map(&m.sa[0], r.terms, T, (uint64_t)M, ld) &&
+         make_mn_map(&m.sb[0], r.x, T, d) &&
+         make_f32_map(&m.so[0], r.dw_part, (uint64_t)r.pieces * M, d);
+    a.groups = r.pieces;
+    a.njobs = 1;
+    a.M[0] = M;
+    a.Ns[0] = r.d;
+    a.sum_out = r.dw_part;
+    tiles += (long long)r.pieces * ceil_div(M, kPairM) * ceil_div(r.d, 256);
+  }
+  if (!ok) return cudaErrorInvalidValue;
+  a.first = r.piece;  // (read up to `groups`, which is 0 without dw)
   a.err = r.err;
-  return launch_pairs(k_pair_gemm<false>, 2, kGemmThreads, kGemmSmem,
-                      (long long)ceil_div(r.T, kPairM) * ceil_div(r.d, 256), st, m, a);
-}
-
-cudaError_t launch_route_dw_tc(const RouteTcArgs &r, cudaStream_t st) {
-  GemmMaps m;
-  GemmArgs a{};
-  // the terms side by side are the rows of one product: x is read once for both
-  const int M = kSplitDw * r.Ep;
-  if (!make_mn_map(&m.a[0], r.terms, (uint64_t)r.T, (uint64_t)M, (uint64_t)kSplit * r.Ep) ||
-      !make_mn_map(&m.b[0], r.x, (uint64_t)r.T, (uint64_t)r.d) ||
-      !make_f32_map(&m.o[0], r.dw_part, (uint64_t)r.pieces * M, (uint64_t)r.d))
-    return cudaErrorInvalidValue;
-  a.poff = a.offsets = r.piece;
-  a.G = r.pieces;
-  a.njobs = 1;
-  a.M[0] = M;
-  a.Ns[0] = r.d;
-  a.out = r.dw_part;
-  a.out_f32 = 1;
-  a.err = r.err;
-  return launch_pairs(k_pair_gemm<true>, 3, kGemmThreads, kGemmSmem,
-                      (long long)r.pieces * ceil_div(M, kPairM) * ceil_div(r.d, 256), st, m, a);
+  return launch_pairs(k_pair_gemm, 2, kGemmThreads, kGemmSmem, tiles, st, m, a);
 }
 
 }  // namespace moe

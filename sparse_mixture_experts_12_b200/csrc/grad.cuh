@@ -75,14 +75,14 @@ constexpr int kSplit = 3, kSplitDw = 2;
 struct RouteTcArgs {
   const void *x, *w;           // [T, d], [E, d]
   __nv_bfloat16 *terms;        // [T, kSplit, Ep], Ep = E rounded up to 64 (zeros behind E)
-  int32_t *all, *all_rows;     // {0, T rounded up to 64}, {0, T}
+  int32_t *all, *all_rows, *all_tiles;  // {0, T rounded up to 64}, {0, T}, {0, 256-row tiles}
   int32_t *piece;              // [pieces + 1] first tokens (multiples of 64) of the pieces of dW
-  float *dx, *dw_part;         // [T, d]; [pieces, kSplitDw, Ep, d]: a sum for each term
+  float *dx, *dw_part;         // [T, d]; [pieces, kSplitDw, Ep, d]: a sum for each term; either
+                               // may be nullptr
   int T, d, E, Ep, pieces;
   int32_t *err;
 };
-cudaError_t launch_route_dx_tc(const RouteTcArgs &a, cudaStream_t st);
-cudaError_t launch_route_dw_tc(const RouteTcArgs &a, cudaStream_t st);
+cudaError_t launch_route_tc(const RouteTcArgs &a, cudaStream_t st);
 size_t route_bwd_scratch_bytes(int T, int d, int E, int dtype);
 cudaError_t launch_route_bwd(const RouteBwdArgs &a, int dtype, cudaStream_t st);
 
@@ -100,6 +100,7 @@ struct FfnGradArgs {
   const int32_t *poff;       // [G+1] its first row in all arrays but dx
   const int32_t *dx_off;     // [G+1] its first row in dx: offsets or poff
   const int32_t *mprefix;    // [G+1] prefix of the experts' tile_rows-row tiles
+  const int32_t *pre256;     // [G+1] prefix of their 256-row tiles
   int tile_rows;             // 32 or 128, see grad_tile_rows()
   int G, m_tiles_ub, pair_tiles_ub;  // bounds of those tiles and of the 256-row tiles
   int d, F, act;
@@ -119,8 +120,7 @@ struct FfnGradArgs {
 cudaError_t launch_ffn_bwd(const FfnGradArgs &a, int dtype, cudaStream_t st);
 // its steps on the tensor cores (bf16)
 cudaError_t launch_act_grad_tc(const FfnGradArgs &a, cudaStream_t st);
-cudaError_t launch_dx_tc(const FfnGradArgs &a, cudaStream_t st);
-cudaError_t launch_dw_tc(const FfnGradArgs &a, cudaStream_t st);
+cudaError_t launch_products_tc(const FfnGradArgs &a, cudaStream_t st);
 
 // Rows to which each expert's are padded: the K slice of the tensor-core products of the
 // weights' gradients (bf16), none on CUDA cores.
@@ -142,10 +142,10 @@ inline long long col_part_rows(long long rows, int m_tiles, int dtype) {
 }
 // offsets -> checked copy, tile prefix and the padded first rows
 cudaError_t launch_grad_tables(const int32_t *offsets, int G, int max_rows, int unit, int pad,
-                               int32_t *checked, int32_t *mprefix, int32_t *poff, int32_t *err,
-                               cudaStream_t st);
+                               int32_t *checked, int32_t *mprefix, int32_t *pre256, int32_t *poff,
+                               int32_t *err, cudaStream_t st);
 // the tables of one group of n rows
-cudaError_t launch_one_group(int n, int unit, int pad, int32_t *offsets, int32_t *mprefix, int32_t *poff,
-                             cudaStream_t st);
+cudaError_t launch_one_group(int n, int unit, int pad, int32_t *offsets, int32_t *mprefix,
+                             int32_t *pre256, int32_t *poff, cudaStream_t st);
 
 }  // namespace moe

@@ -68,9 +68,10 @@ __global__ void __launch_bounds__(kDzThreads, 8) k_dlogits(RouteBwdArgs a, float
     for (int i = threadIdx.x; i <= tc.pieces; i += kDzThreads)
       tc.piece[i] = 64 * min(slices, i * per);
     if (threadIdx.x == 0) {
-      tc.all[0] = tc.all_rows[0] = 0;
+      tc.all[0] = tc.all_rows[0] = tc.all_tiles[0] = 0;
       tc.all[1] = 64 * slices;
       tc.all_rows[1] = a.T;
+      tc.all_tiles[1] = ceil_div(a.T, 256);
     }
   }
   const bool losses = a.d_losses != nullptr, raw = a.gate_mode == MOE_GATE_SOFTMAX_TOPK_RAW;
@@ -560,7 +561,7 @@ struct TcScratch {
 TcScratch tc_scratch(int T, int d, int E) {
   auto up = [](size_t v) { return (v + 255) & ~(size_t)255; };
   TcScratch s;
-  s.db = up((kMaxExperts + 1 + 4) * 4);
+  s.db = up((kMaxExperts + 1 + 6) * 4);
   s.dw = s.db + up((size_t)kMaxBlocks * E * 4);
   s.terms = s.dw + up((size_t)dw_pieces_tc(T, d) * kSplitDw * e_padded(E) * d * 4);
   s.total = s.terms + up((size_t)T * kSplit * e_padded(E) * 2);
@@ -578,9 +579,10 @@ cudaError_t route_bwd_tc(const RouteBwdArgs &a, cudaStream_t st) {
   tc.terms = reinterpret_cast<__nv_bfloat16 *>(base + s.terms);
   tc.all = reinterpret_cast<int32_t *>(base);
   tc.all_rows = tc.all + 2;
-  tc.piece = tc.all + 4;
+  tc.all_tiles = tc.all + 4;
+  tc.piece = tc.all + 6;
   tc.dx = a.dx;
-  tc.dw_part = reinterpret_cast<float *>(base + s.dw);
+  tc.dw_part = a.dw ? reinterpret_cast<float *>(base + s.dw) : nullptr;
   tc.T = a.T;
   tc.d = a.d;
   tc.E = a.E;
@@ -591,12 +593,8 @@ cudaError_t route_bwd_tc(const RouteBwdArgs &a, cudaStream_t st) {
   cudaError_t e = terms ? dlogits<true>(a, a.db ? db_part : nullptr, tc, lanes, st)
                         : dlogits<false>(a, a.db ? db_part : nullptr, tc, lanes, st);
   if (e != cudaSuccess) return e;
-  if (a.dx) {
-    e = launch_route_dx_tc(tc, st);
-    if (e != cudaSuccess) return e;
-  }
-  if (a.dw) {
-    e = launch_route_dw_tc(tc, st);
+  if (terms) {
+    e = launch_route_tc(tc, st);
     if (e != cudaSuccess) return e;
   }
   return sums<__nv_bfloat16>(a, tc.dw_part, tc.pieces * kSplitDw, tc.Ep, db_part, lanes, st);

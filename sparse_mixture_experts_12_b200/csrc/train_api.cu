@@ -8,7 +8,7 @@ namespace moe {
 namespace {
 
 enum Buf {
-  G_ERR, G_OFFSETS, G_MPREFIX, G_POFF, G_SH_OFFSETS, G_SH_MPREFIX, G_SH_POFF, G_H, G_DG, G_DU,
+  G_ERR, G_OFFSETS, G_MPREFIX, G_PRE256, G_POFF, G_SH, G_H, G_DG, G_DU,
   G_COL, G_COL2, G_DLOGITS, G_ROUTE, G_X, G_DY, G_INV, G_DX, G_ROW_W, G_ROW_DOT, G_DOT_PART, G_DX_ROUTER,
   G_DX_SHARED, G_NBUF
 };
@@ -44,8 +44,8 @@ Layout layout_for(const moe_cfg_t &c) {
   const bool copies = c.dtype != MOE_DTYPE_F32 || tc;  // of x and dy rows
   size_t sz[G_NBUF];
   sz[G_ERR] = 4 * sizeof(int32_t);
-  sz[G_OFFSETS] = sz[G_MPREFIX] = sz[G_POFF] = (E + 1) * 4;
-  sz[G_SH_OFFSETS] = sz[G_SH_MPREFIX] = sz[G_SH_POFF] = 2 * 4;
+  sz[G_OFFSETS] = sz[G_MPREFIX] = sz[G_PRE256] = sz[G_POFF] = (E + 1) * 4;
+  sz[G_SH] = 4 * 2 * 4;  // the same tables of the shared experts' one group
   sz[G_H] = act * eb;
   sz[G_DG] = act * eb;
   sz[G_DU] = (glu || Fs ? act : 0) * eb;
@@ -122,6 +122,7 @@ FfnGradArgs expert_args(const moe_cfg_t &c, const moe_weights_t &w, const moe_gr
   a.rows = a.x_rows = (int)scratch_rows(c);
   a.offsets = at<int32_t>(ws, L, G_OFFSETS);
   a.mprefix = at<int32_t>(ws, L, G_MPREFIX);
+  a.pre256 = at<int32_t>(ws, L, G_PRE256);
   a.poff = at<int32_t>(ws, L, G_POFF);
   a.G = c.n_experts;
   a.tile_rows = tile_rows(c);
@@ -153,8 +154,8 @@ moe_status_t expert_tables(const moe_cfg_t &c, const int32_t *offsets, void *ws,
                            cudaStream_t st) {
   return cuda_status(launch_grad_tables(
       offsets, c.n_experts, (int)expert_rows(c), tile_rows(c), row_pad(c.dtype),
-      at<int32_t>(ws, L, G_OFFSETS), at<int32_t>(ws, L, G_MPREFIX), at<int32_t>(ws, L, G_POFF),
-      at<int32_t>(ws, L, G_ERR), st));
+      at<int32_t>(ws, L, G_OFFSETS), at<int32_t>(ws, L, G_MPREFIX), at<int32_t>(ws, L, G_PRE256),
+      at<int32_t>(ws, L, G_POFF), at<int32_t>(ws, L, G_ERR), st));
 }
 
 // copies of the experts' rows of x and dy, padded
@@ -382,16 +383,17 @@ MOE_API moe_status_t moe_backward(const moe_cfg_t *cfg, const moe_weights_t *w, 
   if (c.n_shared > 0 && (dx || g.ws_gate || g.ws_up || g.ws_down)) {
     FfnGradArgs s{};
     s.tile_rows = grad_tile_rows(c.n_tokens, 1);
-    int32_t *so = at<int32_t>(ws, L, G_SH_OFFSETS), *sm = at<int32_t>(ws, L, G_SH_MPREFIX),
-            *sp = at<int32_t>(ws, L, G_SH_POFF);
-    MOE_CUDA(launch_one_group(c.n_tokens, s.tile_rows, row_pad(c.dtype), so, sm, sp, stream));
+    int32_t *tab = at<int32_t>(ws, L, G_SH);
+    MOE_CUDA(launch_one_group(c.n_tokens, s.tile_rows, row_pad(c.dtype), tab, tab + 2, tab + 4,
+                              tab + 6, stream));
     s.x = x;
     s.dy = dy;
     s.x_rows = c.n_tokens;  // the padding rows lie past the operands' bounds: read as zero
     s.rows = (int)padded_rows_ub(c.n_tokens, 1, row_pad(c.dtype));
-    s.offsets = so;
-    s.mprefix = sm;
-    s.poff = s.dx_off = sp;
+    s.offsets = tab;
+    s.mprefix = tab + 2;
+    s.pre256 = tab + 4;
+    s.poff = s.dx_off = tab + 6;
     s.G = 1;
     s.m_tiles_ub = ceil_div(c.n_tokens, s.tile_rows);
     s.pair_tiles_ub = ceil_div(c.n_tokens, 2 * kRowTile);
