@@ -429,7 +429,9 @@ moe_status_t moe_aux_finalize(const moe_cfg_t *cfg, long long n_tokens_total,
  * once with moe_workspace_init() and read with moe_last_device_error() like the
  * forward's (it serves every entry point below; calls that share it must not overlap).
  * Gradients of weights have cfg->dtype, of biases fp32; each given output is
- * overwritten (nothing is accumulated into it). */
+ * overwritten (nothing is accumulated into it). No output may overlap an input or
+ * another output. The results do not depend on the schedule: the same call gives the
+ * same bits. */
 
 /* The parameters' gradients: the shapes of moe_weights_t's members; a NULL member is
  * not computed. b_router is the gradient of logit_bias as well. */
@@ -493,7 +495,9 @@ moe_status_t moe_expert_ffn_backward(const moe_cfg_t *cfg, const moe_weights_t *
                                      const moe_grads_t *grads, void *ws, size_t ws_bytes,
                                      moe_stream_t stream);
 
-/* Gradient of moe_forward: from x, dy [T, d] dtype and the forward's routing (taps:
+/* Gradient of moe_forward (not of its noisy or sharded forms: the noise projection and the
+ * statistics of a batch over several shards are not differentiated): from x, dy [T, d]
+ * dtype and the forward's routing (taps:
  * logits, topk_idx, topk_gate, offsets and inv are required INPUTS, counts too with
  * d_losses; perm is not used) the gradients of x (dx [T, d] dtype, NULL: not computed)
  * and of the parameters that `grads` names. d_losses as in moe_route_backward. The
@@ -538,7 +542,7 @@ typedef struct {
 /* One AdamW step over n_tensors tensors (decoupled weight decay, bias correction):
  *   m = b1 m + (1 - b1) g;  v = b2 v + (1 - b2) g^2
  *   p = p (1 - lr wd) - lr m / (1 - b1^t) / (sqrt(v / (1 - b2^t)) + eps)
- * in fp32. state_bits 8: m = exp_avg * exp_avg_scale and sqrt(v) = exp_avg_sq *
+ * in fp32, every product and sum of m and v rounded by itself. state_bits 8: m = exp_avg * exp_avg_scale and sqrt(v) = exp_avg_sq *
  * exp_avg_sq_scale, the scale the block's largest magnitude / 448 (at least 2^-100 /
  * 448); the parameter's step uses the new m and v before their rounding to e4m3, and a
  * nonzero sqrt(v) keeps at least the smallest code. A gradient that is not finite

@@ -59,7 +59,7 @@ struct RouteBwdArgs {
   const float *row_dot;      // [R] or nullptr: dgate[t,s] = row_dot[inv[t,s]]
   const int32_t *inv;        // [T*k] (with row_dot)
   const float *d_losses;     // [2] or nullptr
-  float *dlogits;            // [T, E]
+  float *dlogits;            // [T, E]; nullptr unless route_bwd_reads_dlogits()
   float *dx;                 // [T, d] fp32 or nullptr
   void *dw;                  // [E, d] dtype or nullptr
   float *db;                 // [E] or nullptr
@@ -83,6 +83,9 @@ struct RouteTcArgs {
   int32_t *err;
 };
 cudaError_t launch_route_tc(const RouteTcArgs &a, cudaStream_t st);
+// whether the launch needs RouteBwdArgs::dlogits (else it may be nullptr: the tensor cores
+// read dz from its terms)
+bool route_bwd_reads_dlogits(int E, int dtype);
 size_t route_bwd_scratch_bytes(int T, int d, int E, int dtype);
 cudaError_t launch_route_bwd(const RouteBwdArgs &a, int dtype, cudaStream_t st);
 

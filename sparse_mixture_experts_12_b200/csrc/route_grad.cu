@@ -602,9 +602,13 @@ cudaError_t route_bwd_tc(const RouteBwdArgs &a, cudaStream_t st) {
 
 }  // namespace
 
+bool route_bwd_reads_dlogits(int E, int dtype) {
+  return E <= kFewExperts || dtype == MOE_DTYPE_F32;
+}
+
 size_t route_bwd_scratch_bytes(int T, int d, int E, int dtype) {
   if (T < 1) T = 1;
-  if (E > kFewExperts && dtype != MOE_DTYPE_F32) return tc_scratch(T, d, E).total;
+  if (!route_bwd_reads_dlogits(E, dtype)) return tc_scratch(T, d, E).total;
   const int pieces = E <= kFewExperts ? proj_pieces(T, d, E) : dw_pieces(T, d, E);
   return sizeof(float) * ((size_t)kMaxBlocks * E + (size_t)pieces * E * d);
 }

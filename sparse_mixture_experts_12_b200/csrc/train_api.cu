@@ -51,7 +51,7 @@ Layout layout_for(const moe_cfg_t &c) {
   sz[G_DU] = (glu || Fs ? act : 0) * eb;
   sz[G_COL] = glu ? 0 : (size_t)col_part_rows((long long)R, tiles, c.dtype) * F * 4;
   sz[G_COL2] = glu ? 0 : (size_t)tiles * d * 4;
-  sz[G_DLOGITS] = tc ? T * E * 4 : 0;
+  sz[G_DLOGITS] = tc && route_bwd_reads_dlogits(c.n_experts, c.dtype) ? T * E * 4 : 0;
   sz[G_ROUTE] = tc ? route_bwd_scratch_bytes(c.n_tokens, c.d_model, c.n_experts, c.dtype) : 0;
   sz[G_X] = copies ? R * d * eb : 0;
   sz[G_DY] = copies ? R * d * eb : 0;
@@ -184,7 +184,7 @@ RouteBwdArgs route_args(const moe_cfg_t &c, void *ws, const Layout &L) {
   a.R = c.n_tokens * c.top_k;
   a.gate_mode = c.gate_mode;
   a.alpha = c.aux_alpha;
-  a.dlogits = at<float>(ws, L, G_DLOGITS);
+  if (route_bwd_reads_dlogits(c.n_experts, c.dtype)) a.dlogits = at<float>(ws, L, G_DLOGITS);
   a.part = at<void>(ws, L, G_ROUTE);
   a.err = at<int32_t>(ws, L, G_ERR);
   return a;

@@ -128,7 +128,8 @@ def test_rows_outside_the_buffer_are_reported_and_skipped():
 # ------------------------------------------------------------------------ router
 ROUTES = [  # T, d, E, k
     (1, 64, 1, 1), (1, 128, 8, 2), (37, 64, 20, 3), (300, 256, 8, 2), (131, 128, 33, 8),
-    (1000, 192, 128, 1), (257, 64, 256, 8), (4100, 64, 4, 4),
+    (1000, 192, 128, 1), (257, 64, 256, 8), (4100, 64, 4, 4), (700, 1088, 64, 4), (2049, 320, 200, 2),
+    (50, 576, 16, 2), (611, 2112, 32, 3),
 ]
 
 
@@ -207,7 +208,7 @@ def test_expert_indices_out_of_range_are_reported():
 FFN = [  # d, F, rows per expert
     (64, 64, [1]), (64, 256, [5, 0, 64, 3]), (128, 320, [0, 1, 129, 300, 64, 0]), (256, 384, [65, 127, 128, 17]),
     (512, 192, [257]), (192, 640, [1, 2, 3, 4, 5, 6, 7, 8]), (64, 64, [0, 0]), (1024, 128, [31, 33]),
-    (320, 576, [700, 255, 256, 511]),
+    (320, 576, [700, 255, 256, 511]), (64, 192, [i % 5 for i in range(100)]), (576, 64, [0, 0, 90, 0]),
 ]
 ACTS = [synth.ACT_RELU, synth.ACT_GELU, synth.ACT_SWIGLU]
 
@@ -284,6 +285,32 @@ def test_invalid_offsets_are_reported_and_nothing_is_read(bad, dt):
     layer.expert_ffn_backward(x, torch.tensor(bad, dtype=torch.int32, device=DEV), dy, dx, gr)
     assert layer.last_backward_error()[0] == 2
     assert (dx == 3.0).all() and all((gr[nm] == 0).all() for nm in ("w1", "w2", "w3"))
+
+
+@pytest.mark.parametrize("dt", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("act", ACTS, ids=["relu", "gelu", "swiglu"])
+def test_experts_do_not_touch_one_another(act, dt):
+    """Infinities and NaN in one expert's rows and weights stay with it, and what the workspace
+    held before is not read."""
+    rows = [70, 3, 64, 129]
+    wl, layer, x, dy, off, n = _ffn_case(192, 320, rows, act, dt, 77)
+    dx, gr = torch.empty_like(x), layer.new_grads()
+    layer.expert_ffn_backward(x, off, dy, dx, gr)
+    x2, dy2 = x.clone(), dy.clone()
+    x2[73 + 10], dy2[73 + 20, 5] = float("nan"), float("inf")      # rows of expert 2
+    for nm in ("w1", "w2", "w3", "b1"):
+        if layer.p.get(nm) is not None:
+            layer.p[nm][2].reshape(-1)[7] = float("-inf")
+    layer.bws[64:].fill_(255)                                      # NaN in every type
+    dx2, g2 = torch.empty_like(x), layer.new_grads()
+    layer.expert_ffn_backward(x2, off, dy2, dx2, g2)
+    keep = [0, 1, 3]
+    for nm in g2:
+        if nm not in ("w_router", "b_router"):
+            assert torch.equal(g2[nm][keep], gr[nm][keep]), nm
+    assert torch.equal(dx2[:73], dx[:73]) and torch.equal(dx2[137:n], dx[137:n])
+    assert not torch.isfinite(g2["w1"][2].float()).all()
+    assert layer.last_backward_error() == (0, 0)
 
 
 def test_expert_choice_rows_have_expert_gradients():
@@ -404,6 +431,8 @@ def test_binding_refuses_what_the_library_cannot_see():
         layer.backward(x, dy.cpu(), taps)
     with pytest.raises(ValueError):
         layer.permute_backward(x, taps["inv"], None, x)
+    with pytest.raises(ValueError):
+        layer.combine_backward(dy.t(), None, taps["inv"], taps["topk_gate"], None, None)
 
 
 # ------------------------------------------------------------------------- AdamW
@@ -600,6 +629,28 @@ def test_training_steps_agree_however_they_are_launched(name, how):
     a, b = _train(wl, 3, 5, "eager"), _train(wl, 3, 5, how)
     for s, t in zip(a, b):
         assert all(torch.equal(p, q) for p, q in zip(s, t))
+
+
+@pytest.mark.parametrize("name", ["deepseek_small", "switch_small", "fp32_gelu_cap"])
+def test_two_layers_at_once_and_a_stale_workspace(name):
+    """Two layers on two streams give what each gives alone, from workspaces full of NaN."""
+    wl = _layer_workload(name)
+    made = [_forward(wl, seed) for seed in (31, 32)]
+    alone = [layer.backward(x, dy, taps) for layer, x, taps, dy in made]
+    for layer, *_ in made:
+        layer.bws[64:].fill_(255)
+    streams = [torch.cuda.Stream() for _ in made]
+    torch.cuda.synchronize()
+    out = []
+    for _ in range(3):
+        for s, (layer, x, taps, dy) in zip(streams, made):
+            with torch.cuda.stream(s):
+                out.append(layer.backward(x, dy, taps))
+    torch.cuda.synchronize()
+    for i, (dx, gr) in enumerate(out):
+        rx, rg = alone[i % 2]
+        assert torch.equal(dx, rx) and all(torch.equal(gr[n], rg[n]) for n in rg)
+    assert all(layer.last_backward_error() == (0, 0) for layer, *_ in made)
 
 
 def test_training_step_against_64_bits():
