@@ -140,7 +140,7 @@ __global__ void __launch_bounds__(kThreads) k_reduce(FfnGradArgs s, Reduce q) {
 // reduction length d; blocks behind the tiles add up db2's columns.
 template <class T, bool GLU, bool VEC>
 __global__ void __launch_bounds__(kThreads) k_dact(FfnGradArgs s, int tiles_n, int tiles) {
-  constexpr int BM = T::BM, BK = T::BK, TM = T::TM;
+  constexpr int BM = T::BM, BK = T::BK, TM = T::TM, TN = T::TN;
   struct Smem {
     alignas(16) float x[BK][T::LDA], y[BK][T::LDA];
     alignas(16) float w1[BK][T::LDB], w3[GLU ? BK : 1][T::LDB], w2[BK][T::LDB];
@@ -159,13 +159,13 @@ __global__ void __launch_bounds__(kThreads) k_dact(FfnGradArgs s, int tiles_n, i
   const int row0 = s.offsets[g] + (tile_m - s.mprefix[g]) * BM;
   const int nrows = min(BM, s.offsets[g + 1] - row0);
   const int n0 = tile_n * BN, F = s.F, d = s.d, ncols = min(BN, F - n0);
-  const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
+  const int tx = threadIdx.x % T::TX, ty = threadIdx.x / T::TX;
   const float *x = static_cast<const float *>(s.x) + (size_t)row0 * d;
   const float *dy = static_cast<const float *>(s.dy) + (size_t)row0 * d;
   const float *w1 = static_cast<const float *>(s.w1) + ((size_t)g * F + n0) * d;
   const float *w3 = GLU ? static_cast<const float *>(s.w3) + ((size_t)g * F + n0) * d : nullptr;
   const float *w2 = static_cast<const float *>(s.w2) + (size_t)g * d * F + n0;
-  float a1[TM][4], a3[GLU ? TM : 1][4], a2[TM][4];
+  float a1[TM][TN], a3[GLU ? TM : 1][TN], a2[TM][TN];
   clear(a1);
   clear(a2);
   if (GLU) clear(a3);
@@ -192,14 +192,16 @@ __global__ void __launch_bounds__(kThreads) k_dact(FfnGradArgs s, int tiles_n, i
 #pragma unroll
     for (int k = 0; k < BK; ++k) {
       float xv[TM], yv[TM];
-      row_values<TM>(&sm.x[k][ty * TM], xv);
-      row_values<TM>(&sm.y[k][ty * TM], yv);
-      outer<TM>(a1, xv, &sm.w1[k][tx * 4]);
-      if constexpr (GLU) outer<TM>(a3, xv, &sm.w3[k][tx * 4]);
-      outer<TM>(a2, yv, &sm.w2[k][tx * 4]);
+      values(&sm.x[k][ty * TM], xv);
+      values(&sm.y[k][ty * TM], yv);
+      outer(a1, xv, &sm.w1[k][tx * TN]);
+      if constexpr (GLU) outer(a3, xv, &sm.w3[k][tx * TN]);
+      outer(a2, yv, &sm.w2[k][tx * TN]);
     }
   }
-  float col[4] = {0.f, 0.f, 0.f, 0.f}, dot[TM];
+  float col[TN], dot[TM];
+#pragma unroll
+  for (int j = 0; j < TN; ++j) col[j] = 0.f;
 #pragma unroll
   for (int i = 0; i < TM; ++i) {
     const int m = ty * TM + i;
@@ -208,8 +210,8 @@ __global__ void __launch_bounds__(kThreads) k_dact(FfnGradArgs s, int tiles_n, i
     const size_t r = (size_t)(row0 + m);
     const float w = s.row_w ? s.row_w[r] : 1.f;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int n = n0 + tx * 4 + j;
+    for (int j = 0; j < TN; ++j) {
+      const int n = n0 + tx * TN + j;
       if (n >= F) continue;
       const float q = a2[i][j];
       float h, da, du = 0.f;
@@ -231,61 +233,70 @@ __global__ void __launch_bounds__(kThreads) k_dact(FfnGradArgs s, int tiles_n, i
       if (GLU) static_cast<float *>(s.du)[r * F + n] = w * du;
     }
   }
-  if (s.row_dot) {  // the tile's 16 column threads of a row
+  if (s.row_dot) {  // the tile's column threads of a row
 #pragma unroll
     for (int i = 0; i < TM; ++i) {
 #pragma unroll
-      for (int o = 8; o > 0; o >>= 1) dot[i] += __shfl_xor_sync(0xffffffffu, dot[i], o);
+      for (int o = T::TX / 2; o > 0; o >>= 1) dot[i] += __shfl_xor_sync(0xffffffffu, dot[i], o);
       const int m = ty * TM + i;
       if (tx == 0 && m < nrows) s.dot_part[(size_t)tile_n * s.rows + row0 + m] = dot[i];
     }
   }
-  if (s.db1) {  // the tile's 16 row threads of a column, through shared memory
+  if (s.db1) {  // the tile's row threads of a column, through shared memory
     float(*red)[BN] = reinterpret_cast<float(*)[BN]>(&sm.w1[0][0]);
     static_assert(sizeof(sm.w1) >= 16 * BN * sizeof(float), "reduction buffer");
     __syncthreads();
 #pragma unroll
-    for (int j = 0; j < 4; ++j) red[ty][tx * 4 + j] = col[j];
+    for (int j = 0; j < TN; ++j) red[ty][tx * TN + j] = col[j];
     __syncthreads();
     if (threadIdx.x < ncols) {
       float v = 0.f;
-      for (int i = 0; i < 16; ++i) v += red[i][threadIdx.x];
+      for (int i = 0; i < T::TY; ++i) v += red[i][threadIdx.x];
       s.col_part[(size_t)tile_m * F + n0 + threadIdx.x] = v;
     }
   }
 }
 
 // Step 2, one launch: tiles of dx = da W1 (+ du W3), tiles of the weights' gradients
-// (reduction over the expert's rows), and the reductions.
+// (reduction over the expert's rows), and the reductions. Few tiles of dx with their long
+// reduction over F are split along it into `splits` pieces (a single row of a wide expert
+// took 530 us in 33 blocks), which k_dx_sum adds in order.
 struct Products {
   int dx, dw;              // blocks of each (then come the reductions')
-  int dx_n;                // column tiles of dx
+  int dx_n, splits, piece; // column tiles of dx; pieces of F, `piece` long
   int jobs;                // weights: products of M x N
   const float *a[3], *b[3];
   float *c[3];
   int M[3], N[3], tiles[3];
 };
-template <class T, bool VEC>
+template <class TD, class TW, bool VEC>
 __global__ void __launch_bounds__(kThreads) k_products(FfnGradArgs s, Products p, Reduce q) {
-  __shared__ GemmSmem<T> sm;
+  __shared__ union Smem {
+    GemmSmem<TD> d;
+    GemmSmem<TW> w;
+  } sm;
   pdl_wait();
   pdl_trigger();
   int x = blockIdx.x;
-  float acc[T::TM][4];
   if (x < p.dx) {
-    const int tile_m = x / p.dx_n, n0 = x % p.dx_n * BN;
+    const int split = x % p.splits, n0 = x / p.splits % p.dx_n * BN;
+    const int tile_m = x / (p.splits * p.dx_n);
     const int g = group_of_tile(s.mprefix, s.G, tile_m);
     if (g < 0) return;
-    const int row0 = s.offsets[g] + (tile_m - s.mprefix[g]) * T::BM;
-    const int rows = min(T::BM, s.offsets[g + 1] - row0), cols = min(BN, s.d - n0);
-    const size_t wo = (size_t)g * s.F * s.d + n0;
+    const int row0 = s.offsets[g] + (tile_m - s.mprefix[g]) * TD::BM;
+    const int rows = min(TD::BM, s.offsets[g + 1] - row0), cols = min(BN, s.d - n0);
+    const int k0 = split * p.piece, K = min(p.piece, s.F - k0);
+    const size_t ao = (size_t)row0 * s.F + k0, wo = ((size_t)g * s.F + k0) * s.d + n0;
+    float acc[TD::TM][TD::TN];
     clear(acc);
-    mma_tile<T, false, VEC>(sm, acc, static_cast<const float *>(s.dg) + (size_t)row0 * s.F, s.F,
-                            rows, static_cast<const float *>(s.w1) + wo, s.d, cols, s.F);
+    mma_tile<TD, false, VEC>(sm.d, acc, static_cast<const float *>(s.dg) + ao, s.F, rows,
+                             static_cast<const float *>(s.w1) + wo, s.d, cols, K);
     if (s.act == MOE_ACT_SWIGLU)
-      mma_tile<T, false, VEC>(sm, acc, static_cast<const float *>(s.du) + (size_t)row0 * s.F, s.F,
-                              rows, static_cast<const float *>(s.w3) + wo, s.d, cols, s.F);
-    store_tile<T, true>(acc, static_cast<float *>(s.dx) + (size_t)row0 * s.d + n0, s.d, rows, cols);
+      mma_tile<TD, false, VEC>(sm.d, acc, static_cast<const float *>(s.du) + ao, s.F, rows,
+                               static_cast<const float *>(s.w3) + wo, s.d, cols, K);
+    float *out = p.splits > 1 ? s.dx_part + (size_t)split * s.rows * s.d
+                              : static_cast<float *>(s.dx);
+    store_tile<TD, true>(acc, out + (size_t)row0 * s.d + n0, s.d, rows, cols);
     return;
   }
   x -= p.dx;
@@ -297,16 +308,32 @@ __global__ void __launch_bounds__(kThreads) k_products(FfnGradArgs s, Products p
     }
     const int g = x / p.tiles[j], t = x % p.tiles[j];
     const int M = p.M[j], N = p.N[j], nt = ceil_div(N, BN);
-    const int m0 = t / nt * T::BM, n0 = t % nt * BN;
+    const int m0 = t / nt * TW::BM, n0 = t % nt * BN;
     const size_t row0 = (size_t)s.offsets[g];
+    float acc[TW::TM][TW::TN];
     clear(acc);
-    mma_tile<T, true, VEC>(sm, acc, p.a[j] + row0 * M + m0, M, M - m0, p.b[j] + row0 * N + n0, N,
-                           N - n0, s.offsets[g + 1] - s.offsets[g]);
-    store_tile<T, VEC>(acc, p.c[j] + ((size_t)g * M + m0) * N + n0, N, min(T::BM, M - m0),
-                       min(BN, N - n0));
+    mma_tile<TW, true, VEC>(sm.w, acc, p.a[j] + row0 * M + m0, M, M - m0, p.b[j] + row0 * N + n0, N,
+                            N - n0, s.offsets[g + 1] - s.offsets[g]);
+    store_tile<TW, VEC>(acc, p.c[j] + ((size_t)g * M + m0) * N + n0, N, min(TW::BM, M - m0),
+                        min(BN, N - n0));
     return;
   }
   reduce<float>(s, q, x - p.dw);
+}
+
+__global__ void __launch_bounds__(kThreads) k_dx_sum(FfnGradArgs s, int splits) {
+  pdl_wait();
+  pdl_trigger();
+  const size_t n = (size_t)s.offsets[s.G] * s.d, all = (size_t)s.rows * s.d;
+  const size_t i = ((size_t)blockIdx.x * kThreads + threadIdx.x) * 4;  // d is a multiple of 4
+  if (i >= n) return;
+  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int j = 0; j < splits; ++j) {
+    const float4 p = __ldg(reinterpret_cast<const float4 *>(s.dx_part + j * all + i));
+    v.x += p.x; v.y += p.y; v.z += p.z; v.w += p.w;
+  }
+  *reinterpret_cast<float4 *>(static_cast<float *>(s.dx) + i) = v;
 }
 
 // One warp: offsets -> checked copy (all zero when they are no partition of at most
@@ -383,14 +410,15 @@ __global__ void k_one_group(int n, int unit, int pad, int32_t *offsets, int32_t 
   poff[1] = ceil_div(n, pad) * pad;
 }
 
-template <class T, bool VEC>
+template <class TD, class TW, bool VEC>
 cudaError_t ffn_bwd_f32(const FfnGradArgs &a, cudaStream_t st) {
   const bool glu = a.act == MOE_ACT_SWIGLU;
   const dim3 b(kThreads);
   const int nt = ceil_div(a.F, BN), tiles = nt * a.m_tiles_ub;
   const int sums = a.db2 ? ceil_div(a.d, 64) * a.m_tiles_ub : 0;
-  cudaError_t e = glu ? launch_pdl(k_dact<T, true, VEC>, dim3(tiles + sums), b, 0, st, a, nt, tiles)
-                      : launch_pdl(k_dact<T, false, VEC>, dim3(tiles + sums), b, 0, st, a, nt, tiles);
+  cudaError_t e =
+      glu ? launch_pdl(k_dact<TD, true, VEC>, dim3(tiles + sums), b, 0, st, a, nt, tiles)
+          : launch_pdl(k_dact<TD, false, VEC>, dim3(tiles + sums), b, 0, st, a, nt, tiles);
   if (e != cudaSuccess) return e;
   Reduce q = reduce_blocks(a);
   q.first = a.mprefix;
@@ -398,7 +426,10 @@ cudaError_t ffn_bwd_f32(const FfnGradArgs &a, cudaStream_t st) {
   q.dots = nt;
   Products p{};
   p.dx_n = ceil_div(a.d, BN);
-  p.dx = a.dx ? p.dx_n * a.m_tiles_ub : 0;
+  p.splits = a.dx ? dx_splits(a.m_tiles_ub, a.d, a.F) : 1;
+  p.piece = ceil_div(ceil_div(a.F, p.splits), 32) * 32;
+  p.splits = ceil_div(a.F, p.piece);
+  p.dx = a.dx ? p.dx_n * a.m_tiles_ub * p.splits : 0;
   auto job = [&](const void *x, const void *y, void *c, int M, int N) {
     if (c == nullptr) return;
     const int j = p.jobs++;
@@ -407,7 +438,7 @@ cudaError_t ffn_bwd_f32(const FfnGradArgs &a, cudaStream_t st) {
     p.c[j] = static_cast<float *>(c);
     p.M[j] = M;
     p.N[j] = N;
-    p.tiles[j] = ceil_div(M, T::BM) * ceil_div(N, BN);
+    p.tiles[j] = ceil_div(M, TW::BM) * ceil_div(N, BN);
     p.dw += a.G * p.tiles[j];
   };
   job(a.dg, a.x, a.dw1, a.F, a.d);
@@ -415,7 +446,21 @@ cudaError_t ffn_bwd_f32(const FfnGradArgs &a, cudaStream_t st) {
   job(a.dy, a.h, a.dw2, a.d, a.F);
   const int blocks = p.dx + p.dw + q.db1 + q.db2 + q.rows;
   if (blocks == 0) return cudaSuccess;
-  return launch_pdl(k_products<T, VEC>, dim3(blocks), b, 0, st, a, p, q);
+  e = launch_pdl(k_products<TD, TW, VEC>, dim3(blocks), b, 0, st, a, p, q);
+  if (e != cudaSuccess || p.dx == 0 || p.splits == 1) return e;
+  return launch_pdl(k_dx_sum, dim3((unsigned)(((size_t)a.rows * a.d / 4 + kThreads - 1) / kThreads)),
+                    b, 0, st, a, p.splits);
+}
+
+// the weights' gradients take 128-row tiles unless those leave SMs without one
+template <class TD, bool VEC>
+cudaError_t ffn_bwd_f32(const FfnGradArgs &a, cudaStream_t st) {
+  const long long big = (long long)a.G * ceil_div(a.F, 128) * ceil_div(a.d, BN);
+  return big >= 148 ? ffn_bwd_f32<TD, Tile<128>, VEC>(a, st) : ffn_bwd_f32<TD, Tile<32>, VEC>(a, st);
+}
+template <class TD>
+cudaError_t ffn_bwd_f32(const FfnGradArgs &a, cudaStream_t st) {
+  return a.F % 4 == 0 ? ffn_bwd_f32<TD, true>(a, st) : ffn_bwd_f32<TD, false>(a, st);  // d always is
 }
 
 // bf16: the steps on the tensor cores
@@ -457,10 +502,8 @@ cudaError_t launch_one_group(int n, int unit, int pad, int32_t *offsets, int32_t
 
 cudaError_t launch_ffn_bwd(const FfnGradArgs &a, int dtype, cudaStream_t st) {
   if (dtype != MOE_DTYPE_F32) return ffn_bwd_tc(a, st);
-  const bool vec = a.F % 4 == 0;  // d always is
-  if (a.tile_rows == 32)
-    return vec ? ffn_bwd_f32<Tile<32>, true>(a, st) : ffn_bwd_f32<Tile<32>, false>(a, st);
-  return vec ? ffn_bwd_f32<Tile<128>, true>(a, st) : ffn_bwd_f32<Tile<128>, false>(a, st);
+  if (a.tile_rows == 8) return ffn_bwd_f32<Tile<8>>(a, st);
+  return a.tile_rows == 32 ? ffn_bwd_f32<Tile<32>>(a, st) : ffn_bwd_f32<Tile<128>>(a, st);
 }
 
 }  // namespace moe

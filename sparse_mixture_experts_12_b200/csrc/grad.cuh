@@ -104,7 +104,7 @@ struct FfnGradArgs {
   const int32_t *dx_off;     // [G+1] its first row in dx: offsets or poff
   const int32_t *mprefix;    // [G+1] prefix of the experts' tile_rows-row tiles
   const int32_t *pre256;     // [G+1] prefix of their 256-row tiles
-  int tile_rows;             // 32 or 128, see grad_tile_rows()
+  int tile_rows;             // 8, 32 or 128, see grad_tile_rows()
   int G, m_tiles_ub, pair_tiles_ub;  // bounds of those tiles and of the 256-row tiles
   int d, F, act;
   const void *w1, *w3, *w2;
@@ -114,6 +114,7 @@ struct FfnGradArgs {
   float *dot_part;           // [ceil(F / 32), rows] scratch (with row_dot)
   void *h, *dg, *du;         // [rows, F] dtype scratch: w h, w dg, w du
   void *dx;                  // [dx_rows, d] or nullptr
+  float *dx_part;            // [dx_splits(), rows, d] scratch (fp32 layers)
   int dx_f32, dx_rows;
   void *dw1, *dw3, *dw2;     // [G, F, d], [G, F, d], [G, d, F] dtype, or nullptr
   float *db1, *db2;          // [G, F], [G, d] fp32, or nullptr
@@ -133,9 +134,19 @@ inline long long padded_rows_ub(long long R, int G, int pad) {
   const long long r = R + (long long)(pad - 1) * (R < G ? R : G);
   return (r + pad - 1) / pad * pad;
 }
-// Rows of a tile of the CUDA-core products (and of a partial of db2): 32 where experts
-// average fewer than 64 rows, so that small experts do not pay for empty ones.
-inline int grad_tile_rows(long long rows, int G) { return rows < 64LL * G ? 32 : 128; }
+// Rows of a tile of the CUDA-core products (and of a partial of db2): fewer where experts
+// average fewer rows, so that small experts do not pay for empty ones.
+inline int grad_tile_rows(long long rows, int G) {
+  return rows <= 8LL * G ? 8 : (rows < 64LL * G ? 32 : 128);
+}
+// Pieces of F that dx's tiles on CUDA cores are split into: two blocks an SM, a reduction
+// of at least 256 each.
+inline int dx_splits(int m_tiles, int d, int F) {
+  const long long tiles = (long long)m_tiles * ceil_div(d, 64);
+  const int most = F / 256 > 1 ? F / 256 : 1;
+  const long long s = tiles > 0 ? (296 + tiles - 1) / tiles : 1;
+  return s < most ? (int)s : most;
+}
 inline int grad_tiles_ub(long long rows, int G, int unit) {
   return (int)(rows / unit + (rows < G ? rows : G));
 }

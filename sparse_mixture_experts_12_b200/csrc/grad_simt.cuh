@@ -2,8 +2,9 @@
 // BM x 64 tile of C = A B with B row-major [K, N], A row-major [M, K] or (AT) [K, M], from
 // K slices in shared memory while the next slice is fetched into registers.
 //
-// BM 128 (8 x 4 values a thread, 16-wide slices) is for experts with many rows; BM 32 (2 x
-// 4, 32-wide) for few: a 128-row tile of 16 rows took 22 us where the 32-row one takes 5.
+// BM 128 (8 x 4 values a thread, 16-wide slices) is for experts with many rows, BM 32 (2 x
+// 4, 32-wide) and BM 8 (1 x 2) for few: on 16 rows a 128-row tile took 22 us where the
+// 32-row one takes 8, and on a handful the 32-row one computes more than it loads.
 #pragma once
 
 #include "kernels.cuh"
@@ -15,9 +16,9 @@ constexpr int BN = 64, kThreads = 256;
 template <int BM_>
 struct Tile {
   static constexpr int BM = BM_, BK = BM == 128 ? 16 : 32;
-  static constexpr int TM = BM / 16, TN = 4;       // per thread; 16 x 16 threads
-  static constexpr int LDA = BM + (BM == 128 ? 4 : 2), LDB = BN + 4;
-  static constexpr int A4 = BM * BK / 4 / kThreads, B4 = BN * BK / 4 / kThreads;
+  static constexpr int TN = BM == 8 ? 2 : 4, TX = BN / TN;  // columns a thread, threads across
+  static constexpr int TY = kThreads / TX, TM = BM / TY;    // threads down, rows a thread
+  static constexpr int LDA = BM + (BM == 32 ? 2 : 4), LDB = BN + 4;
 };
 
 // the expert of row tile mt (mprefix [G+1]), or -1 past the last tile
@@ -51,12 +52,13 @@ __device__ __forceinline__ float4 ld4(const float *p, int n) {
 // shared memory as [BK][LD]. KMAJOR: the reduction's index is the contiguous one.
 template <int ROWS, int BK, int LD, bool KMAJOR, bool VEC>
 struct Slice {
-  static constexpr int N4 = ROWS * BK / 4 / kThreads;
+  static constexpr int kAll = ROWS * BK / 4, N4 = (kAll + kThreads - 1) / kThreads;
   float4 r[N4];
   __device__ __forceinline__ void fetch(const float *p, size_t ld, int rows, int k0, int K) {
 #pragma unroll
     for (int j = 0; j < N4; ++j) {
       const int i = threadIdx.x + kThreads * j;
+      if (kAll % kThreads && i >= kAll) break;
       if (KMAJOR) {
         const int m = i / (BK / 4), k = k0 + (i % (BK / 4)) * 4;
         r[j] = ld4<VEC>(p + (size_t)m * ld + k, m < rows ? K - k : 0);
@@ -70,6 +72,7 @@ struct Slice {
 #pragma unroll
     for (int j = 0; j < N4; ++j) {
       const int i = threadIdx.x + kThreads * j;
+      if (kAll % kThreads && i >= kAll) break;
       if (KMAJOR) {
         const int m = i / (BK / 4), k = (i % (BK / 4)) * 4;
         s[k][m] = r[j].x;
@@ -89,34 +92,37 @@ struct Slice {
   }
 };
 
-template <int TM>
-__device__ __forceinline__ void row_values(const float *p, float (&v)[TM]) {
-  if constexpr (TM == 8) {
+// N consecutive values of shared memory
+template <int N>
+__device__ __forceinline__ void values(const float *p, float (&v)[N]) {
+  if constexpr (N % 4 == 0) {
 #pragma unroll
-    for (int i = 0; i < TM; i += 4) {
+    for (int i = 0; i < N; i += 4) {
       const float4 q = *reinterpret_cast<const float4 *>(p + i);
       v[i] = q.x; v[i + 1] = q.y; v[i + 2] = q.z; v[i + 3] = q.w;
     }
-  } else {
+  } else if constexpr (N == 2) {
     const float2 q = *reinterpret_cast<const float2 *>(p);
     v[0] = q.x; v[1] = q.y;
+  } else {
+    v[0] = *p;
   }
 }
-template <int TM>
-__device__ __forceinline__ void outer(float (&acc)[TM][4], const float (&a)[TM], const float *b) {
-  const float4 q = *reinterpret_cast<const float4 *>(b);
+template <int TM, int TN>
+__device__ __forceinline__ void outer(float (&acc)[TM][TN], const float (&a)[TM], const float *b) {
+  float q[TN];
+  values(b, q);
 #pragma unroll
-  for (int i = 0; i < TM; ++i) {
-    acc[i][0] = fmaf(a[i], q.x, acc[i][0]);
-    acc[i][1] = fmaf(a[i], q.y, acc[i][1]);
-    acc[i][2] = fmaf(a[i], q.z, acc[i][2]);
-    acc[i][3] = fmaf(a[i], q.w, acc[i][3]);
-  }
+  for (int i = 0; i < TM; ++i)
+#pragma unroll
+    for (int j = 0; j < TN; ++j) acc[i][j] = fmaf(a[i], q[j], acc[i][j]);
 }
-template <int TM>
-__device__ __forceinline__ void clear(float (&acc)[TM][4]) {
+template <int TM, int TN>
+__device__ __forceinline__ void clear(float (&acc)[TM][TN]) {
 #pragma unroll
-  for (int i = 0; i < TM; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
+  for (int i = 0; i < TM; ++i)
+#pragma unroll
+    for (int j = 0; j < TN; ++j) acc[i][j] = 0.f;
 }
 
 template <class T>
@@ -128,10 +134,10 @@ struct GemmSmem {
 // acc += A B over K for the tile whose operands begin at a and b: `rows` rows of A, `cols`
 // columns of B inside
 template <class T, bool AT, bool VEC>
-__device__ __forceinline__ void mma_tile(GemmSmem<T> &s, float (&acc)[T::TM][4], const float *a,
-                                         size_t lda, int rows, const float *b, size_t ldb, int cols,
+__device__ __forceinline__ void mma_tile(GemmSmem<T> &s, float (&acc)[T::TM][T::TN],
+                                         const float *a, size_t lda, int rows, const float *b, size_t ldb, int cols,
                                          int K) {
-  const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
+  const int tx = threadIdx.x % T::TX, ty = threadIdx.x / T::TX;
   Slice<T::BM, T::BK, T::LDA, !AT, VEC> sa;
   Slice<BN, T::BK, T::LDB, false, VEC> sb;
   sa.fetch(a, lda, rows, 0, K);
@@ -148,29 +154,33 @@ __device__ __forceinline__ void mma_tile(GemmSmem<T> &s, float (&acc)[T::TM][4],
 #pragma unroll
     for (int k = 0; k < T::BK; ++k) {
       float av[T::TM];
-      row_values<T::TM>(&s.a[k][ty * T::TM], av);
-      outer<T::TM>(acc, av, &s.b[k][tx * 4]);
+      values(&s.a[k][ty * T::TM], av);
+      outer(acc, av, &s.b[k][tx * T::TN]);
     }
   }
 }
 
 // c: the tile's first element
 template <class T, bool VEC>
-__device__ __forceinline__ void store_tile(const float (&acc)[T::TM][4], float *c, size_t ldc,
+__device__ __forceinline__ void store_tile(const float (&acc)[T::TM][T::TN], float *c, size_t ldc,
                                            int rows, int cols) {
-  const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
+  constexpr int TN = T::TN;
+  const int tx = threadIdx.x % T::TX, ty = threadIdx.x / T::TX;
 #pragma unroll
   for (int i = 0; i < T::TM; ++i) {
     const int m = ty * T::TM + i;
     if (m >= rows) continue;
-    float *p = c + (size_t)m * ldc + tx * 4;
-    const int n = cols - tx * 4;
-    if (VEC) {
-      if (n > 0)
+    float *p = c + (size_t)m * ldc + tx * TN;
+    const int n = cols - tx * TN;
+    if constexpr (VEC) {
+      if (n <= 0) continue;
+      if constexpr (TN == 4)
         *reinterpret_cast<float4 *>(p) = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
+      else
+        *reinterpret_cast<float2 *>(p) = make_float2(acc[i][0], acc[i][1]);
     } else {
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
+      for (int j = 0; j < TN; ++j)
         if (j < n) p[j] = acc[i][j];
     }
   }

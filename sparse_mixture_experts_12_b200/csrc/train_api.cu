@@ -9,7 +9,7 @@ namespace {
 
 enum Buf {
   G_ERR, G_OFFSETS, G_MPREFIX, G_PRE256, G_POFF, G_SH, G_H, G_DG, G_DU,
-  G_COL, G_COL2, G_DLOGITS, G_ROUTE, G_X, G_DY, G_INV, G_DX, G_ROW_W, G_ROW_DOT, G_DOT_PART, G_DX_ROUTER,
+  G_COL, G_COL2, G_DLOGITS, G_ROUTE, G_X, G_DY, G_INV, G_DX, G_DX_PART, G_ROW_W, G_ROW_DOT, G_DOT_PART, G_DX_ROUTER,
   G_DX_SHARED, G_NBUF
 };
 
@@ -57,6 +57,13 @@ Layout layout_for(const moe_cfg_t &c) {
   sz[G_DY] = copies ? R * d * eb : 0;
   sz[G_INV] = tc ? T * (size_t)c.top_k * 4 : 0;
   sz[G_DX] = tc ? R * d * 4 : 0;
+  sz[G_DX_PART] = 0;
+  if (c.dtype == MOE_DTYPE_F32) {
+    const int us = grad_tile_rows(c.n_tokens, 1);
+    sz[G_DX_PART] = larger((size_t)dx_splits(tiles, c.d_model, c.d_ff) * R,
+                           Fs ? (size_t)dx_splits(ceil_div(c.n_tokens, us), c.d_model, (int)Fs) * T : 0) *
+                    d * 4;
+  }
   sz[G_ROW_W] = tc ? R * 4 : 0;
   sz[G_ROW_DOT] = tc ? R * 4 : 0;
   sz[G_DOT_PART] = tc ? R * (size_t)ceil_div(c.d_ff, 32) * 4 : 0;
@@ -141,6 +148,7 @@ FfnGradArgs expert_args(const moe_cfg_t &c, const moe_weights_t &w, const moe_gr
   a.du = at<void>(ws, L, G_DU);
   a.col_part = at<float>(ws, L, G_COL);
   a.part2 = at<float>(ws, L, G_COL2);
+  a.dx_part = at<float>(ws, L, G_DX_PART);
   a.dw1 = g.w1;
   a.dw3 = g.w3;
   a.dw2 = g.w2;
@@ -407,6 +415,7 @@ MOE_API moe_status_t moe_backward(const moe_cfg_t *cfg, const moe_weights_t *w, 
     s.dg = at<void>(ws, L, G_DG);
     s.du = at<void>(ws, L, G_DU);
     s.dx = dx_shared = dx ? at<float>(ws, L, G_DX_SHARED) : nullptr;
+    s.dx_part = at<float>(ws, L, G_DX_PART);
     s.dx_f32 = 1;
     s.dx_rows = c.n_tokens;
     s.dw1 = g.ws_gate;
