@@ -169,6 +169,13 @@ __global__ void __launch_bounds__(kThreads) k_dact(FfnGradArgs s, int tiles_n, i
   clear(a1);
   clear(a2);
   if (GLU) clear(a3);
+  // small tiles have the registers to add up their sums in parts of 512 (the error of a
+  // running sum grows with the root of its length)
+  constexpr bool kParts = BM < 128;
+  float t1[kParts ? TM : 1][TN], t3[kParts && GLU ? TM : 1][TN], t2[kParts ? TM : 1][TN];
+  clear(t1);
+  clear(t2);
+  if (GLU) clear(t3);
   Slice<BM, BK, T::LDA, true, true> sx, sy;  // d is a multiple of 4
   Slice<BN, BK, T::LDB, true, true> s1, s3;
   Slice<BN, BK, T::LDB, false, VEC> s2;
@@ -198,6 +205,13 @@ __global__ void __launch_bounds__(kThreads) k_dact(FfnGradArgs s, int tiles_n, i
       if constexpr (GLU) outer(a3, xv, &sm.w3[k][tx * TN]);
       outer(a2, yv, &sm.w2[k][tx * TN]);
     }
+    if constexpr (kParts) {
+      if (k0 + BK >= d || (k0 + BK) % 512 == 0) {
+        flush(t1, a1);
+        flush(t2, a2);
+        if constexpr (GLU) flush(t3, a3);
+      }
+    }
   }
   float col[TN], dot[TM];
 #pragma unroll
@@ -213,17 +227,17 @@ __global__ void __launch_bounds__(kThreads) k_dact(FfnGradArgs s, int tiles_n, i
     for (int j = 0; j < TN; ++j) {
       const int n = n0 + tx * TN + j;
       if (n >= F) continue;
-      const float q = a2[i][j];
+      const float q = kParts ? t2[i][j] : a2[i][j], v = kParts ? t1[i][j] : a1[i][j];
       float h, da, du = 0.f;
       if constexpr (GLU) {
-        const float v = a1[i][j], u = a3[i][j];
+        const float u = kParts ? t3[i][j] : a3[i][j];
         const float sg = 1.f / (1.f + expf(-v));
         h = v * sg * u;
         du = q * v * sg;
         da = q * u * sg * (1.f + v * (1.f - sg));
       } else {
         float sl;
-        act_and_slope(s.act, a1[i][j] + (s.b1 ? s.b1[(size_t)g * F + n] : 0.f), h, sl);
+        act_and_slope(s.act, v + (s.b1 ? s.b1[(size_t)g * F + n] : 0.f), h, sl);
         da = q * sl;
       }
       dot[i] = fmaf(q, h, dot[i]);
@@ -258,9 +272,10 @@ __global__ void __launch_bounds__(kThreads) k_dact(FfnGradArgs s, int tiles_n, i
 }
 
 // Step 2, one launch: tiles of dx = da W1 (+ du W3), tiles of the weights' gradients
-// (reduction over the expert's rows), and the reductions. Few tiles of dx with their long
-// reduction over F are split along it into `splits` pieces (a single row of a wide expert
-// took 530 us in 33 blocks), which k_dx_sum adds in order.
+// (reduction over the expert's rows), and the reductions. The long reduction of dx over F is
+// split into `splits` pieces, which k_dx_sum adds in order: so that few tiles fill the GPU
+// (two rows of a 2100 x 13008 expert took 530 us in 33 blocks, 125 us so), and that no
+// running sum grows too long (see dx_splits).
 struct Products {
   int dx, dw;              // blocks of each (then come the reductions')
   int dx_n, splits, piece; // column tiles of dx; pieces of F, `piece` long
@@ -426,7 +441,7 @@ cudaError_t ffn_bwd_f32(const FfnGradArgs &a, cudaStream_t st) {
   q.dots = nt;
   Products p{};
   p.dx_n = ceil_div(a.d, BN);
-  p.splits = a.dx ? dx_splits(a.m_tiles_ub, a.d, a.F) : 1;
+  p.splits = a.dx ? dx_splits(a.m_tiles_ub, a.d, a.F, glu) : 1;
   p.piece = ceil_div(ceil_div(a.F, p.splits), 32) * 32;
   p.splits = ceil_div(a.F, p.piece);
   p.dx = a.dx ? p.dx_n * a.m_tiles_ub * p.splits : 0;

@@ -139,13 +139,16 @@ inline long long padded_rows_ub(long long R, int G, int pad) {
 inline int grad_tile_rows(long long rows, int G) {
   return rows <= 8LL * G ? 8 : (rows < 64LL * G ? 32 : 128);
 }
-// Pieces of F that dx's tiles on CUDA cores are split into: two blocks an SM, a reduction
-// of at least 256 each.
-inline int dx_splits(int m_tiles, int d, int F) {
+// Pieces of F that dx's tiles on CUDA cores are split into: two blocks an SM, with a
+// reduction of at least 256 each; and at most 1024 products in one running sum (two for
+// each index with SwiGLU), whose fp32 error grows with the root of their number (2.3e-6 of
+// the result after 13008 of them, where sums of 1024 keep it near 5e-7).
+inline int dx_splits(int m_tiles, int d, int F, bool glu) {
   const long long tiles = (long long)m_tiles * ceil_div(d, 64);
   const int most = F / 256 > 1 ? F / 256 : 1;
-  const long long s = tiles > 0 ? (296 + tiles - 1) / tiles : 1;
-  return s < most ? (int)s : most;
+  const long long fill = tiles > 0 ? (296 + tiles - 1) / tiles : 1;
+  const int s = fill < most ? (int)fill : most, exact = ceil_div(F, glu ? 512 : 1024);
+  return s > exact ? s : exact;
 }
 inline int grad_tiles_ub(long long rows, int G, int unit) {
   return (int)(rows / unit + (rows < G ? rows : G));

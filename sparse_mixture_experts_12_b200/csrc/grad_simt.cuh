@@ -125,6 +125,18 @@ __device__ __forceinline__ void clear(float (&acc)[TM][TN]) {
     for (int j = 0; j < TN; ++j) acc[i][j] = 0.f;
 }
 
+// total += acc, acc = 0
+template <int TM, int TN>
+__device__ __forceinline__ void flush(float (&total)[TM][TN], float (&acc)[TM][TN]) {
+#pragma unroll
+  for (int i = 0; i < TM; ++i)
+#pragma unroll
+    for (int j = 0; j < TN; ++j) {
+      total[i][j] += acc[i][j];
+      acc[i][j] = 0.f;
+    }
+}
+
 template <class T>
 struct GemmSmem {
   alignas(16) float a[T::BK][T::LDA];

@@ -60,8 +60,8 @@ Layout layout_for(const moe_cfg_t &c) {
   sz[G_DX_PART] = 0;
   if (c.dtype == MOE_DTYPE_F32) {
     const int us = grad_tile_rows(c.n_tokens, 1);
-    sz[G_DX_PART] = larger((size_t)dx_splits(tiles, c.d_model, c.d_ff) * R,
-                           Fs ? (size_t)dx_splits(ceil_div(c.n_tokens, us), c.d_model, (int)Fs) * T : 0) *
+    sz[G_DX_PART] = larger((size_t)dx_splits(tiles, c.d_model, c.d_ff, glu) * R,
+                           Fs ? (size_t)dx_splits(ceil_div(c.n_tokens, us), c.d_model, (int)Fs, true) * T : 0) *
                     d * 4;
   }
   sz[G_ROW_W] = tc ? R * 4 : 0;
