@@ -273,6 +273,11 @@ struct ActCfg {
   static constexpr int kBytesQ = kOperand + kMnBlock;
   static constexpr int kBytesA = GLU ? 2 * kOperand : kOperand + kMnBlock;
   static constexpr int kStagesQ = GLU ? 3 : 4, kStagesA = 4;
+  // K slices of one accumulation. The tensor cores truncate what they add, a bias of some
+  // 2^-26 of the sum for each 16 products (-4.3e-6 at d = 4096). It does not matter beside
+  // the rounding of h and da, but db1 keeps it: with biases (MLP) the epilogue adds up
+  // parts of 512 products in fp32.
+  static constexpr int kPart = GLU ? 1 << 30 : 8;
   static constexpr size_t kRings = (size_t)kStagesQ * kBytesQ + (size_t)kStagesA * kBytesA;
   static constexpr size_t kBytes = kRings + (size_t)kEpiWarps * kStageOutBytes;
   static constexpr size_t kSmem = kBytes + sizeof(Ctl) + 1024;
@@ -343,24 +348,26 @@ k_act_grad(const __grid_constant__ ActMaps maps, ActArgs a) {
     RingQ ring(ring_q);
     bool ok = true, any = false;
     int it = 0;
-    for (int t = s.c0; ok && t < total; t += s.cstep, ++it) {
-      const int buf = it & 1;
-      const uint32_t acc = s.tmem + 256u + (uint32_t)(buf * kTileN);
-      // tile it - 2, which used the same buffer, has been drained
-      if (!(ok = wait_on(s, &ctl->tempty[buf], ((it >> 1) & 1) ^ 1u, a.err, 22))) break;
-      tc_fence_after();
-      for (int i = 0; i < nkb; ++i) {
-        if (!(ok = ring.filled(s, a.err, 23))) break;
-        const uint64_t xa = sw128_desc(ring.addr());
-        const uint64_t xb = sw128_desc_mn(ring.addr() + kOperand, kMnBlock);
+    for (int t = s.c0; ok && t < total; t += s.cstep) {
+      for (int i0 = 0; ok && i0 < nkb; i0 += C::kPart, ++it) {
+        const int buf = it & 1, i1 = min(nkb, i0 + C::kPart);
+        const uint32_t acc = s.tmem + 256u + (uint32_t)(buf * kTileN);
+        // part it - 2, which used the same buffer, has been drained
+        if (!(ok = wait_on(s, &ctl->tempty[buf], ((it >> 1) & 1) ^ 1u, a.err, 22))) break;
+        tc_fence_after();
+        for (int i = i0; i < i1; ++i) {
+          if (!(ok = ring.filled(s, a.err, 23))) break;
+          const uint64_t xa = sw128_desc(ring.addr());
+          const uint64_t xb = sw128_desc_mn(ring.addr() + kOperand, kMnBlock);
 #pragma unroll
-        for (int kk = 0; kk < kBlockK / 16; ++kk)
-          umma_bf16_pair(acc, xa + 2 * kk, xb + 128 * kk, idesc, (i | kk) != 0);
-        any = true;
-        ring.release(s);
-        ring.next();
+          for (int kk = 0; kk < kBlockK / 16; ++kk)
+            umma_bf16_pair(acc, xa + 2 * kk, xb + 128 * kk, idesc, ((i - i0) | kk) != 0);
+          any = true;
+          ring.release(s);
+          ring.next();
+        }
+        if (ok) umma_commit_pair_both(&ctl->tfull[buf]);
       }
-      if (ok) umma_commit_pair_both(&ctl->tfull[buf]);
     }
     if (!ok && any) retire(s, &ctl->drain[0]);
   } else if (warp == 2 && lane == 0 && s.rank == 0) {
@@ -369,24 +376,27 @@ k_act_grad(const __grid_constant__ ActMaps maps, ActArgs a) {
     RingA ring(ring_a);
     bool ok = true, any = false;
     int it = 0;
-    for (int t = s.c0; ok && t < total; t += s.cstep, ++it) {
-      const int buf = it & 1;
-      const uint32_t acc = s.tmem + (GLU ? 0u : (uint32_t)(buf * kTileN));
-      // SwiGLU has one a | u region: tile it - 1 has been drained
-      const int old = GLU ? it - 1 : it - 2;
-      if (old >= 0 && !(ok = wait_on(s, &ctl->tempty[old & 1], (old >> 1) & 1, a.err, 22))) break;
-      tc_fence_after();
-      for (int i = 0; i < nkb; ++i) {
-        if (!(ok = ring.filled(s, a.err, 23))) break;
-        const uint64_t xa = sw128_desc(ring.addr()), xb = sw128_desc(ring.addr() + kOperand);
+    for (int t = s.c0; ok && t < total; t += s.cstep) {
+      for (int i0 = 0; ok && i0 < nkb; i0 += C::kPart, ++it) {
+        const int buf = it & 1, i1 = min(nkb, i0 + C::kPart);
+        const uint32_t acc = s.tmem + (GLU ? 0u : (uint32_t)(buf * kTileN));
+        // SwiGLU has one a | u region: part it - 1 (the tile before) has been drained
+        const int old = GLU ? it - 1 : it - 2;
+        if (old >= 0 && !(ok = wait_on(s, &ctl->tempty[old & 1], (old >> 1) & 1, a.err, 22)))
+          break;
+        tc_fence_after();
+        for (int i = i0; i < i1; ++i) {
+          if (!(ok = ring.filled(s, a.err, 23))) break;
+          const uint64_t xa = sw128_desc(ring.addr()), xb = sw128_desc(ring.addr() + kOperand);
 #pragma unroll
-        for (int kk = 0; kk < kBlockK / 16; ++kk)
-          umma_bf16_pair(acc, xa + 2 * kk, xb + 2 * kk, idesc, (i | kk) != 0);
-        any = true;
-        ring.release(s);
-        ring.next();
+          for (int kk = 0; kk < kBlockK / 16; ++kk)
+            umma_bf16_pair(acc, xa + 2 * kk, xb + 2 * kk, idesc, ((i - i0) | kk) != 0);
+          any = true;
+          ring.release(s);
+          ring.next();
+        }
+        if (ok) umma_commit_pair_both(&ctl->tfull[buf]);
       }
-      if (ok) umma_commit_pair_both(&ctl->tfull[buf]);
     }
     if (!ok && any) retire(s, &ctl->drain[1]);
   } else if (warp >= 4) {
@@ -396,10 +406,10 @@ k_act_grad(const __grid_constant__ ActMaps maps, ActArgs a) {
     const uint32_t tempty0 = mapa_rank(smem_u32(&ctl->tempty[0]), 0);
     uint8_t *stage = s.smem + C::kRings + (warp - 4) * kStageOutBytes;
     int it = 0;
-    for (int t = s.c0; t < total; t += s.cstep, ++it) {
+    bool ok = true;
+    for (int t = s.c0; ok && t < total; t += s.cstep) {
       int g, n, m;
       decode_tile(t, ctl->pre, a.G, a.n_tiles, g, n, m);
-      const int buf = it & 1;
       const int lrow = m * kPairM + s.rank * kRowTile + ew * 32;  // the warp's first row
       const int prow = a.poff[g] + lrow;
       // padded groups of 32 rows belong to the expert as a whole or not at all; F is a
@@ -407,46 +417,84 @@ k_act_grad(const __grid_constant__ ActMaps maps, ActArgs a) {
       const bool rows_mine = prow < a.poff[g + 1];
       const bool valid = lrow + lane < a.offsets[g + 1] - a.offsets[g];
       const float w = (a.row_w && rows_mine) ? a.row_w[prow + lane] : 1.f;
-      bool ok = wait_on(s, &ctl->tfull[buf], (it >> 1) & 1, a.err, 24);
-      __syncwarp();
-      if (!__all_sync(0xffffffffu, ok)) break;
-      tc_fence_after();
+      auto wait_full = [&]() {
+        ok = wait_on(s, &ctl->tfull[it & 1], (it >> 1) & 1, a.err, 24);
+        __syncwarp();
+        ok = __all_sync(0xffffffffu, ok);
+        if (ok) tc_fence_after();
+        return ok;
+      };
+      auto drained = [&]() {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_remote(tempty0 + (uint32_t)((it & 1) * sizeof(uint64_t)));
+      };
+      const uint32_t lanes = s.tmem + ((uint32_t)(ew * 32) << 16);
+      float as[GLU ? 1 : 32], qs[GLU ? 1 : 32];  // MLP: the warp's one chunk, all parts
+      if constexpr (GLU) {
+        if (!wait_full()) break;
+      } else {
+        const int col = n * kTileN + part * 32;
+        const bool bias = a.b1 && col < a.F;
+#pragma unroll
+        for (int j = 0; j < 32; j += 4) {  // a begins with the bias, the same for every lane
+          const float4 b = bias ? __ldg(reinterpret_cast<const float4 *>(a.b1 + (size_t)g * a.F +
+                                                                         col + j))
+                                : make_float4(0.f, 0.f, 0.f, 0.f);
+          as[j] = b.x; as[j + 1] = b.y; as[j + 2] = b.z; as[j + 3] = b.w;
+          qs[j] = qs[j + 1] = qs[j + 2] = qs[j + 3] = 0.f;
+        }
+        for (int i0 = 0; i0 < nkb; i0 += C::kPart) {
+          if (!wait_full()) break;
+          const uint32_t at = lanes + (uint32_t)((it & 1) * kTileN + part * 32);
+          if (rows_mine) {
+#pragma unroll
+            for (int j2 = 0; j2 < 2; ++j2) {
+              uint32_t av[16], qv[16];
+              tmem_ld16(at + j2 * 16, av);
+              tmem_ld16(at + 256u + j2 * 16, qv);
+              tmem_ld_wait();
+#pragma unroll
+              for (int j = 0; j < 16; ++j) {
+                as[j2 * 16 + j] += __uint_as_float(av[j]);
+                qs[j2 * 16 + j] += __uint_as_float(qv[j]);
+              }
+            }
+          }
+          drained();
+          ++it;
+        }
+        if (!ok) break;
+      }
+      // (MLP: one chunk, said so that its sums need not outlive it)
 #pragma unroll 1
-      for (int c = part; c < kTileN / 32; c += kParts) {
+      for (int c = part; c < (GLU ? kTileN / 32 : part + 1); c += kParts) {
         const int col0 = n * kTileN + c * 32;
         const bool mine = rows_mine && col0 < a.F;
-        const uint32_t lane_base = s.tmem + ((uint32_t)(ew * 32) << 16) + (uint32_t)(c * 32);
-        const uint32_t tq = lane_base + 256u + (uint32_t)(buf * kTileN);
-        const uint32_t ta = lane_base + (GLU ? 0u : (uint32_t)(buf * kTileN));
+        const uint32_t ta = lanes + (uint32_t)(c * 32);               // SwiGLU
+        const uint32_t tq = ta + 256u + (uint32_t)((it & 1) * kTileN);
         float dot = 0.f;
         uint32_t hp[16], gp[16], up[GLU ? 16 : 1];  // packed pairs of columns
         if (mine) {
 #pragma unroll
           for (int j2 = 0; j2 < 2; ++j2) {
-            uint32_t av[16], uv[GLU ? 16 : 1], qv[16];
-            tmem_ld16(ta + j2 * 16, av);
-            if constexpr (GLU) tmem_ld16(ta + kTileN + j2 * 16, uv);
-            tmem_ld16(tq + j2 * 16, qv);
-            float bias[GLU ? 1 : 16];
-            if constexpr (!GLU) {
-#pragma unroll
-              for (int j = 0; j < 16; j += 4) {  // the same for every lane
-                const float4 b = a.b1 ? __ldg(reinterpret_cast<const float4 *>(
-                                            a.b1 + (size_t)g * a.F + col0 + j2 * 16 + j))
-                                      : make_float4(0.f, 0.f, 0.f, 0.f);
-                bias[j] = b.x; bias[j + 1] = b.y; bias[j + 2] = b.z; bias[j + 3] = b.w;
-              }
+            uint32_t av[GLU ? 16 : 1], uv[GLU ? 16 : 1], qv[GLU ? 16 : 1];
+            if constexpr (GLU) {
+              tmem_ld16(ta + j2 * 16, av);
+              tmem_ld16(ta + kTileN + j2 * 16, uv);
+              tmem_ld16(tq + j2 * 16, qv);
+              tmem_ld_wait();
             }
-            tmem_ld_wait();
             float da[16];
 #pragma unroll
             for (int j = 0; j < 16; j += 2) {
               float h[2], du[2];
 #pragma unroll
               for (int i = 0; i < 2; ++i) {
-                const float q = __uint_as_float(qv[j + i]);
-                float v = __uint_as_float(av[j + i]), x;
+                float q, v, x;
                 if constexpr (GLU) {
+                  q = __uint_as_float(qv[j + i]);
+                  v = __uint_as_float(av[j + i]);
                   const float u = __uint_as_float(uv[j + i]);
                   const float sg = __fdividef(1.f, 1.f + __expf(-v));
                   const float si = v * sg;
@@ -454,7 +502,8 @@ k_act_grad(const __grid_constant__ ActMaps maps, ActArgs a) {
                   du[i] = q * si;
                   x = q * u * fmaf(si, 1.f - sg, sg);
                 } else {
-                  v += bias[j + i];
+                  q = qs[j2 * 16 + j + i];
+                  v = as[j2 * 16 + j + i];
                   float sl;
                   if (a.act == MOE_ACT_RELU) {
                     h[i] = fmaxf(v, 0.f);
@@ -481,11 +530,8 @@ k_act_grad(const __grid_constant__ ActMaps maps, ActArgs a) {
             }
           }
         }
-        if (c + kParts >= kTileN / 32) {  // the warp's last chunk is in registers
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_remote(tempty0 + (uint32_t)(buf * sizeof(uint64_t)));
-        }
+        // SwiGLU: the warp's last chunk is in registers
+        if (GLU && c + kParts >= kTileN / 32) drained();
         if (mine) {
           put32(stage, &maps.h, hp, col0, prow);
           put32(stage, &maps.dg, gp, col0, prow);
@@ -493,6 +539,7 @@ k_act_grad(const __grid_constant__ ActMaps maps, ActArgs a) {
           if (a.dot_part && valid) a.dot_part[(size_t)(col0 / 32) * a.rows + prow + lane] = dot;
         }
       }
+      if (GLU) ++it;
     }
     if (lane == 0) bulk_wait_all();  // this warp's output stores are done
     __syncwarp();
