@@ -283,75 +283,80 @@ __global__ void __launch_bounds__(kProjThreads) k_route_proj(const T *x, const T
                                                              const float *dz, float *dx,
                                                              float *dw_part, int n_tok, int d,
                                                              int E, int per) {
-  __shared__ __align__(16) float zs[kProjTokens][EP];
+  __shared__ __align__(16) float2 zs[kProjTokens][EP];  // each dz twice: operands of packed FMAs
   const int tid = threadIdx.x;
   const int col = (blockIdx.x * kProjThreads + tid) * VC;
   const bool live = col < d;
-  pdl_wait();
-  pdl_trigger();
-  float wr[EP][VC], acc[EP][VC];
+  // W and x do not come from the kernel ahead (the logits' gradient), which began its
+  // successor after its own wait: they are read before this one's
+  constexpr int VP = VC / 2;  // pairs of columns
+  float2 wr[EP][VP], acc[EP][VP];
 #pragma unroll
   for (int e = 0; e < EP; ++e) {
 #pragma unroll
-    for (int c = 0; c < VC; ++c) wr[e][c] = acc[e][c] = 0.f;
+    for (int c = 0; c < VP; ++c) wr[e][c] = acc[e][c] = make_float2(0.f, 0.f);
     if (dx && live && e < E) {
       Cols<T, VC> r;
       r.load(w + (size_t)e * d + col);
 #pragma unroll
-      for (int c = 0; c < VC; ++c) wr[e][c] = r.get(c);
+      for (int c = 0; c < VP; ++c) wr[e][c] = make_float2(r.get(2 * c), r.get(2 * c + 1));
     }
   }
   const int t0 = blockIdx.y * per, t1 = min(n_tok, t0 + per);
-  for (int tb = t0; tb < t1; tb += kProjTokens) {
+  // 32 bytes of x per thread are requested while the 32 before are worked on
+  constexpr int NB = 32 / (VC * (int)sizeof(T)) < 8 ? 32 / (VC * (int)sizeof(T)) : 8;
+  Cols<T, VC> next[NB];
+  auto request = [&](int t) {
+#pragma unroll
+    for (int i = 0; i < NB; ++i)
+      if (dw_part && live && t + i < t1) next[i].load(x + (size_t)(t + i) * d + col);
+  };
+  request(t0);
+  pdl_wait();
+  pdl_trigger();
+  for (int tb = t0; tb < t1; tb += kProjTokens) {  // a multiple of NB
     const int n = min(kProjTokens, t1 - tb);
     __syncthreads();
     for (int i = tid; i < kProjTokens * EP; i += kProjThreads) {
       const int u = i / EP, e = i % EP;
-      zs[u][e] = (u < n && e < E) ? dz[(size_t)(tb + u) * E + e] : 0.f;
+      if (u >= n) break;
+      const float z = e < E ? dz[(size_t)(tb + u) * E + e] : 0.f;
+      zs[u][e] = make_float2(z, z);
     }
     __syncthreads();
     if (!live) continue;
-    // 32 bytes of x per thread are requested while the 32 before are worked on
-    constexpr int NB = 32 / (VC * (int)sizeof(T)) < 8 ? 32 / (VC * (int)sizeof(T)) : 8;
-    Cols<T, VC> next[NB];
-    auto request = [&](int u0) {
-#pragma unroll
-      for (int i = 0; i < NB; ++i)
-        if (dw_part && u0 + i < n) next[i].load(x + (size_t)(tb + u0 + i) * d + col);
-    };
-    request(0);
     for (int u0 = 0; u0 < n; u0 += NB) {
       Cols<T, VC> xv[NB];
 #pragma unroll
       for (int i = 0; i < NB; ++i) xv[i] = next[i];
-      request(u0 + NB);
+      request(tb + u0 + NB);
 #pragma unroll
       for (int i = 0; i < NB; ++i) {
         if (u0 + i >= n) break;
-        float o[VC], z[EP];
+        float2 o[VP], xp[VP];
 #pragma unroll
-        for (int e = 0; e < EP; e += 4) {
+        for (int c = 0; c < VP; ++c) {
+          o[c] = make_float2(0.f, 0.f);
+          xp[c] = make_float2(xv[i].get(2 * c), xv[i].get(2 * c + 1));
+        }
+#pragma unroll
+        for (int e = 0; e < EP; e += 2) {
           const float4 q = *reinterpret_cast<const float4 *>(&zs[u0 + i][e]);
-          z[e] = q.x; z[e + 1] = q.y; z[e + 2] = q.z; z[e + 3] = q.w;
+          const float2 z[2] = {make_float2(q.x, q.y), make_float2(q.z, q.w)};
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int c = 0; c < VP; ++c) {
+              if (dx) o[c] = __ffma2_rn(z[h], wr[e + h][c], o[c]);
+              if (dw_part) acc[e + h][c] = __ffma2_rn(z[h], xp[c], acc[e + h][c]);
+            }
         }
         if (dx) {
-#pragma unroll
-          for (int c = 0; c < VC; ++c) {
-            o[c] = 0.f;
-#pragma unroll
-            for (int e = 0; e < EP; ++e) o[c] = fmaf(z[e], wr[e][c], o[c]);
-          }
           float *out = dx + (size_t)(tb + u0 + i) * d + col;
           if constexpr (VC == 4)
-            *reinterpret_cast<float4 *>(out) = make_float4(o[0], o[1], o[2], o[3]);
+            *reinterpret_cast<float4 *>(out) = make_float4(o[0].x, o[0].y, o[1].x, o[1].y);
           else
-            *reinterpret_cast<float2 *>(out) = make_float2(o[0], o[1]);
-        }
-        if (dw_part) {
-#pragma unroll
-          for (int e = 0; e < EP; ++e)
-#pragma unroll
-            for (int c = 0; c < VC; ++c) acc[e][c] = fmaf(z[e], xv[i].get(c), acc[e][c]);
+            *reinterpret_cast<float2 *>(out) = o[0];
         }
       }
     }
@@ -362,7 +367,7 @@ __global__ void __launch_bounds__(kProjThreads) k_route_proj(const T *x, const T
       if (e < E) {
         float *out = dw_part + ((size_t)blockIdx.y * E + e) * d + col;
 #pragma unroll
-        for (int c = 0; c < VC; ++c) out[c] = acc[e][c];
+        for (int c = 0; c < VP; ++c) reinterpret_cast<float2 *>(out)[c] = acc[e][c];
       }
   }
 }
