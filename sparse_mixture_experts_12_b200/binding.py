@@ -634,7 +634,8 @@ def noise_draws(n_tokens: int, n_experts: int, seed: int, offset: int, eps: torc
 
 
 class AdamW:
-    """AdamW over a list of CUDA tensors on one device (moe_adamw_step), updated in place.
+    """AdamW over CUDA tensors on one device (moe_adamw_step), a list or a dict of them,
+    updated in place.
 
     ``state_bits``: 32, or 8 (e4m3 with one fp32 scale for each ADAMW_BLOCK elements).
     ``master``: keep fp32 copies of the bf16 parameters, which the step works on.
@@ -647,6 +648,7 @@ class AdamW:
     def __init__(self, params, lr: float = 1e-3, betas=(0.9, 0.999), eps: float = 1e-8,
                  weight_decay: float = 1e-2, state_bits: int = 32, master: bool = False,
                  state: Optional[dict] = None):
+        self.names = list(params) if isinstance(params, dict) else None
         self.params = list(params.values() if isinstance(params, dict) else params)
         self.lr, self.betas, self.eps, self.weight_decay = lr, betas, eps, weight_decay
         if not self.params:
@@ -678,6 +680,9 @@ class AdamW:
             self.master = list(state.get("master") or [None] * len(self.params))
         self._lib = load()
         n_params = len(self.params)
+        if len({p.data_ptr() for p in self.params if p.numel()}) != sum(1 for p in self.params
+                                                                        if p.numel()):
+            raise ValueError("the same parameter twice")
         dt = torch.float32 if self.bits == 32 else torch.float8_e4m3fn
         lists = [self.exp_avg, self.exp_avg_sq, self.master]
         if self.bits == 8:
@@ -719,12 +724,18 @@ class AdamW:
     def step(self, grads, grad_scale: Optional[torch.Tensor] = None,
              found_inf: Optional[torch.Tensor] = None, step: Optional[torch.Tensor] = None,
              lr: Optional[torch.Tensor] = None):
-        """One step from ``grads`` (a list in the parameters' order, or a dict's values).
+        """One step from ``grads``: a list in the parameters' order, or a dict with an entry for
+        each name of a dict of parameters (others are left alone).
         Device scalars, read when the kernel runs: ``grad_scale`` multiplies the gradients,
         ``found_inf`` nonzero skips the update (the step still counts), ``step`` (int64) and
         ``lr`` (fp32) take the place of the counter and of self.lr (a captured step needs
         them to move)."""
-        grads = list(grads.values() if isinstance(grads, dict) else grads)
+        if isinstance(grads, dict):
+            if self.names is None or any(n not in grads for n in self.names):
+                raise ValueError("a dict of gradients needs the names of a dict of parameters")
+            grads = [grads[n] for n in self.names]
+        else:
+            grads = list(grads)
         if len(grads) != len(self.params):
             raise ValueError(f"{len(grads)} gradients for {len(self.params)} parameters")
         if ([g.shape for g in grads] != self._shapes

@@ -129,7 +129,7 @@ def test_rows_outside_the_buffer_are_reported_and_skipped():
 ROUTES = [  # T, d, E, k
     (1, 64, 1, 1), (1, 128, 8, 2), (37, 64, 20, 3), (300, 256, 8, 2), (131, 128, 33, 8),
     (1000, 192, 128, 1), (257, 64, 256, 8), (4100, 64, 4, 4), (700, 1088, 64, 4), (2049, 320, 200, 2),
-    (50, 576, 16, 2), (611, 2112, 32, 3),
+    (50, 576, 16, 2), (611, 2112, 32, 3), (1, 64, 40, 2), (3, 128, 256, 8), (65, 64, 65, 1),
 ]
 
 
@@ -335,6 +335,46 @@ def test_expert_choice_rows_have_expert_gradients():
                                torch.empty(wl.T, wl.d_model, dtype=torch.bfloat16, device=DEV))
 
 
+def test_offsets_past_32_bits():
+    """Row buffers of more than 2^31 elements: the last rows are the right ones."""
+    T, d, k, b = 33000, 8192, 8, torch.bfloat16
+    wl = _workload(T, d, 8, k, BF16)
+    layer, g = B.MoELayer(wl, {}, DEV), _gen(1)
+    inv = torch.arange(T * k, device=DEV, dtype=torch.int32).flip(0).contiguous()
+    dy, gate = _rand(g, T, d, dt=b), torch.rand(T, k, device=DEV, generator=g)
+    yp = torch.empty(T * k, d, dtype=b, device=DEV).normal_(generator=g)
+    out, dgate = torch.zeros_like(yp), torch.empty(T, k, device=DEV)
+    layer.combine_backward(dy, yp, inv, gate, out, dgate)
+    for t in (0, 1, T // 2, T - 1):
+        rows = inv.reshape(T, k)[t].long()
+        ref = dy[t].double() * gate[t].double()[:, None]
+        R.check(out[rows], ref, (R.U(b) + 2.0 ** -23) * ref.abs(), "dy_perm")
+        dot = yp[rows].double() * dy[t].double()
+        R.check(dgate[t], dot.sum(1), (d + 2) * R.A * dot.abs().sum(1), "dgate")
+    dx = torch.empty(T, d, dtype=b, device=DEV)
+    layer.permute_backward(yp, inv, None, dx)
+    for t in (0, T - 1):
+        x = yp[inv.reshape(T, k)[t].long()].double()
+        R.check(dx[t], x.sum(0), R.U(b) * 1.01 * x.sum(0).abs() + k * R.A * x.abs().sum(0), "dx")
+    del yp, out, dx
+    # and the experts' hidden rows
+    rows, d, F = [1, 40000], 64, 57344
+    wl, layer, x, dy, off, n = _ffn_case(d, F, rows, synth.ACT_RELU, BF16, 3)
+    dx, gr = torch.empty_like(x), {m: layer.new_grads()[m] for m in ("w1", "w2")}
+    layer.expert_ffn_backward(x, off, dy, dx, gr)
+    p, e = {m: v[1:].double() for m, v in layer.p.items() if v is not None and m != "w_router"}, 1
+    last = slice(n - 3, n)                       # three rows of expert 1 by themselves
+    ref, lim = R.ffn_bwd(x[last], dy[last], [0, 3], {m: v for m, v in p.items()}, synth.ACT_RELU, b)
+    R.check(dx[last], ref["dx"], lim["dx"], "dx")
+    cols = slice(F - 64, F)                      # the last hidden columns, all rows
+    few = {"w1": p["w1"][:, cols], "w2": p["w2"][:, :, cols].contiguous(), "b1": p["b1"][:, cols],
+           "b2": p["b2"]}
+    ref, lim = R.ffn_bwd(x[1:n], dy[1:n], [0, n - 1], few, synth.ACT_RELU, b)
+    R.check(gr["w1"][1][cols], ref["w1"][0], lim["w1"][0], "w1")
+    R.check(gr["w2"][1][:, cols], ref["w2"][0], lim["w2"][0], "w2")
+    assert layer.last_backward_error() == (0, 0)
+
+
 # --------------------------------------------------------------- the whole layer
 LAYERS = ["tiny", "mixtral_small", "deepseek_small", "switch_small", "mixtral_cap", "decode_small",
           "deepseek_decode", "fp32_swiglu", "fp32_gelu_cap", "router_e20", "router_e256", "one_token"]
@@ -537,6 +577,21 @@ def test_adamw_scalars_on_the_device():
         assert torch.allclose(p, r, rtol=1e-6, atol=1e-7)
 
 
+def test_adamw_takes_gradients_by_name():
+    ps, gs, opt = _adam_case([100, 100, 7], torch.float32, torch.float32, 32, False, 6)
+    qs = {n: p.clone() for n, p in zip("abc", ps)}
+    named = B.AdamW(qs, lr=0.01, betas=(0.8, 0.95), eps=1e-6, weight_decay=0.1)
+    opt.step(gs)
+    named.step({"other": gs[0], "c": gs[2], "b": gs[1], "a": gs[0]})
+    assert all(torch.equal(p, q) for p, q in zip(ps, qs.values()))
+    with pytest.raises(ValueError):
+        named.step({"a": gs[0], "b": gs[1]})
+    with pytest.raises(ValueError):
+        opt.step(dict(zip("abc", gs)))
+    with pytest.raises(ValueError):
+        B.AdamW([ps[0], ps[0]])
+
+
 def test_adamw_refuses_what_does_not_fit():
     ps, gs, opt = _adam_case([100, 31], torch.float32, torch.float32, 32, False, 4)
     with pytest.raises(ValueError):
@@ -591,7 +646,7 @@ def _train(wl, steps, seed, how):
         count.add_(1)
         layer.forward(x, y, aux=aux, taps=taps)
         layer.backward(x, dy, taps, dx=dx, grads=grads, d_losses=dl)
-        opt.step([grads[n] for n in params], step=count, lr=lr)
+        opt.step(grads, step=count, lr=lr)
 
     seen = []
     side = torch.cuda.Stream()
