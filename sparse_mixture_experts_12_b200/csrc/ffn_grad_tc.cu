@@ -21,7 +21,7 @@
 #include <mutex>
 
 #include "grad.cuh"
-#include "tc_ptx.cuh"
+#include "grad_ptx.cuh"
 
 namespace moe {
 
@@ -749,7 +749,7 @@ k_pair_gemm(const __grid_constant__ GemmMaps maps, GemmArgs a) {
       tc_fence_after();
       const uint32_t ta = s.tmem + ((uint32_t)(ew * 32) << 16) + (uint32_t)(buf * 256 + part * 64);
       if (mine && staged) {
-        if (lane == 0) bulk_wait_read<0>();  // the previous tile's store has read the buffer
+        if (lane == 0) bulk_wait_read_all();  // the previous tile's store has read the buffer
         __syncwarp();
       }
       if (mine) {
@@ -768,7 +768,7 @@ k_pair_gemm(const __grid_constant__ GemmMaps maps, GemmArgs a) {
           }
           if (f32 && staged) {  // 32 rows of 128 bytes, 16-byte pieces swizzled
             if (c > 0) {
-              if (lane == 0) bulk_wait_read<0>();
+              if (lane == 0) bulk_wait_read_all();
               __syncwarp();
             }
             float4 *dst = reinterpret_cast<float4 *>(stage + lane * 128);
@@ -965,7 +965,7 @@ cudaError_t launch_route_tc(const RouteTcArgs &r, cudaStream_t st) {
   if (r.dx) {
     for (int j = 0; j < kSplit; ++j)
       ok = ok &&
-           make_map(&m.a[j], r.terms + (size_t)j * r.Ep, T, (uint64_t)r.Ep, kRowTile, ld) &&
+           make_map_ld(&m.a[j], r.terms + (size_t)j * r.Ep, T, (uint64_t)r.Ep, kRowTile, ld) &&
            make_mn_map(&m.b[j], r.w, (uint64_t)r.E, d);
     ok = ok && make_f32_map(&m.o, r.dx, T, d);
     a.poff = r.all;
