@@ -488,7 +488,10 @@ class MoELayer:
             _check(st, name)
 
     def _want(self, t, shape, name, dtype=None, optional=False):
-        check_tensor(t, shape, dtype or self.w.torch_dtype, name, self.ws.device, optional)
+        dtype = dtype or self.w.torch_dtype
+        if (t is None or t.shape != shape or t.dtype is not dtype or not t.is_contiguous()
+                or t.get_device() != self.ws.get_device()):
+            check_tensor(t, shape, dtype, name, self.ws.device, optional)
 
     def grad_shapes(self) -> dict:
         """name -> (shape, dtype) of every parameter's gradient: the parameters this layer
@@ -718,7 +721,9 @@ class AdamW:
         self._grad_types = np.ndarray((n_params,), np.int32, self._batch,
                                       MoeAdamWTensor.grad_dtype.offset,
                                       (ctypes.sizeof(MoeAdamWTensor),))
+        self._grad_dtypes = None  # the types that _grad_types holds
         self._shapes = [p.shape for p in self.params]
+        self._devices = [p.get_device() for p in self.params]
         self._index = self.params[0].get_device()
 
     def step(self, grads, grad_scale: Optional[torch.Tensor] = None,
@@ -738,16 +743,21 @@ class AdamW:
             grads = list(grads)
         if len(grads) != len(self.params):
             raise ValueError(f"{len(grads)} gradients for {len(self.params)} parameters")
+        # list by list: a hundred tensors are checked in the time of a launch or two
         if ([g.shape for g in grads] != self._shapes
-                or not all([g.is_contiguous() and g.get_device() == self._index for g in grads])):
+                or [g.get_device() for g in grads] != self._devices
+                or not all([g.is_contiguous() for g in grads])):
             for i, (g, p) in enumerate(zip(grads, self.params)):  # which one
                 check_tensor(g, p.shape, g.dtype, f"gradient {i}", self.device)
-        types = [_ADAMW_DTYPES.get(g.dtype, -1) for g in grads]
-        if -1 in types:
-            raise ValueError(f"gradient {types.index(-1)} is {grads[types.index(-1)].dtype}: fp32 "
-                             "or bf16 are supported")
+        dtypes = [g.dtype for g in grads]
+        if dtypes != self._grad_dtypes:
+            bad = [i for i, dt in enumerate(dtypes) if dt not in _ADAMW_DTYPES]
+            if bad:
+                raise ValueError(f"gradient {bad[0]} is {dtypes[bad[0]]}: fp32 or bf16 are "
+                                 "supported")
+            self._grad_types[:] = [_ADAMW_DTYPES[dt] for dt in dtypes]
+            self._grad_dtypes = dtypes
         self._grad_ptrs[:] = [g.data_ptr() for g in grads]
-        self._grad_types[:] = types
         o = MoeAdamW(self.betas[0], self.betas[1], self.lr, self.eps, self.weight_decay, self.t + 1)
         for name, t, dt in (("grad_scale", grad_scale, torch.float32),
                             ("found_inf", found_inf, torch.float32),

@@ -277,8 +277,10 @@ __global__ void __launch_bounds__(kThreads, 5) k_adamw(const __grid_constant__ B
   }
 }
 
-constexpr int kFew = 32, kMany = 288;  // tensors per launch (kernel parameters of 4 KB, 32 KB)
-static_assert(sizeof(Batch<kFew>) <= 4096 && sizeof(Batch<kMany>) <= 32764, "kernel parameters");
+// Tensors per launch: kernel parameters of 3, 10 and 22 KB, which the launch copies (96
+// tensors: a call of 13 us with the largest, 6 us with the middle one).
+constexpr int kFew = 32, kSome = 128, kMany = 288;
+static_assert(sizeof(Batch<kMany>) <= 32764, "kernel parameters");
 
 template <int N>
 moe_status_t launch(const moe_adamw_tensor_t *ts, int n, const moe_adamw_t &o, cudaStream_t st) {
@@ -357,8 +359,9 @@ MOE_API moe_status_t moe_adamw_step(const moe_adamw_tensor_t *tensors, int32_t n
       ctas += c;
       ++m;
     }
-    MOE_TRY(m <= kFew ? launch<kFew>(tensors + i, m, o, stream)
-                      : launch<kMany>(tensors + i, m, o, stream));
+    MOE_TRY(m <= kFew    ? launch<kFew>(tensors + i, m, o, stream)
+            : m <= kSome ? launch<kSome>(tensors + i, m, o, stream)
+                         : launch<kMany>(tensors + i, m, o, stream));
     i += m;
   }
   return MOE_OK;
