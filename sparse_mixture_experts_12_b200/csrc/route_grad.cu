@@ -249,12 +249,10 @@ __global__ void __launch_bounds__(kDzThreads, 8) k_dlogits(RouteBwdArgs a, float
   }
 }
 
-// Few experts (EP >= E, at most kFewExperts): both products on CUDA cores in one pass over
+// Few experts (EP >= E, see few_experts()): both products on CUDA cores in one pass over
 // x. A thread owns VC columns and keeps their EP rows of W and of dW in registers; the
-// block walks over its piece of the tokens with dz broadcast from shared memory. 4 E flops
-// per element of x: up to E = 16 the reads of x and the writes of dx bound it.
-constexpr int kFewExperts = 32;
-constexpr int kProjThreads = 128, kProjTokens = 128;
+// block walks over its piece of the tokens with dz broadcast from shared memory.
+constexpr int kProjThreads = 128, kProjTokens = 128, kProjCols = 4;
 
 // VC values of type T as they lie in memory, and unpacked
 template <typename T, int VC>
@@ -265,11 +263,10 @@ struct Cols {
     if constexpr (n == 4) {
       const uint4 v = __ldg(reinterpret_cast<const uint4 *>(p));
       u[0] = v.x; u[1] = v.y; u[2] = v.z; u[3] = v.w;
-    } else if constexpr (n == 2) {
+    } else {
+      static_assert(n == 2, "8 or 16 bytes");
       const uint2 v = __ldg(reinterpret_cast<const uint2 *>(p));
       u[0] = v.x; u[1] = v.y;
-    } else {
-      u[0] = __ldg(reinterpret_cast<const uint32_t *>(p));
     }
   }
   __device__ __forceinline__ float get(int c) const {
@@ -278,11 +275,12 @@ struct Cols {
   }
 };
 
-template <typename T, int EP, int VC>
+template <typename T, int EP>
 __global__ void __launch_bounds__(kProjThreads) k_route_proj(const T *x, const T *w,
                                                              const float *dz, float *dx,
                                                              float *dw_part, int n_tok, int d,
                                                              int E, int per) {
+  constexpr int VC = kProjCols;
   __shared__ __align__(16) float2 zs[kProjTokens][EP];  // each dz twice: operands of packed FMAs
   const int tid = threadIdx.x;
   const int col = (blockIdx.x * kProjThreads + tid) * VC;
@@ -353,10 +351,7 @@ __global__ void __launch_bounds__(kProjThreads) k_route_proj(const T *x, const T
         }
         if (dx) {
           float *out = dx + (size_t)(tb + u0 + i) * d + col;
-          if constexpr (VC == 4)
-            *reinterpret_cast<float4 *>(out) = make_float4(o[0].x, o[0].y, o[1].x, o[1].y);
-          else
-            *reinterpret_cast<float2 *>(out) = o[0];
+          *reinterpret_cast<float4 *>(out) = make_float4(o[0].x, o[0].y, o[1].x, o[1].y);
         }
       }
     }
@@ -454,9 +449,8 @@ int dw_pieces_tc(int T, int d) {
 
 // ... of k_route_proj: as many blocks as the SMs hold (registers), at least sixteen tokens
 // each
-int proj_cols(int E) { return E <= 16 ? 4 : 2; }
 int proj_pieces(int T, int d, int E) {
-  const int s = 148 * (E <= 8 ? 4 : 2) / ceil_div(d, kProjThreads * proj_cols(E)), most = ceil_div(T, 16);
+  const int s = 148 * (E <= 8 ? 4 : 2) / ceil_div(d, kProjThreads * kProjCols), most = ceil_div(T, 16);
   return s < 1 ? 1 : (s < most ? s : most);
 }
 
@@ -495,15 +489,17 @@ cudaError_t route_bwd_few(const RouteBwdArgs &a, cudaStream_t st) {
   const int pieces = proj_pieces(a.T, a.d, a.E);
   float *dw_part = db_part + (size_t)kMaxBlocks * a.E;
   if (a.dx || a.dw) {
-    const dim3 g(ceil_div(a.d, kProjThreads * proj_cols(a.E)), pieces), b(kProjThreads);
+    const dim3 g(ceil_div(a.d, kProjThreads * kProjCols), pieces), b(kProjThreads);
     const T *x = static_cast<const T *>(a.x), *w = static_cast<const T *>(a.w);
     auto run = [&](auto kernel) {
       return launch_pdl(kernel, g, b, 0, st, x, w, (const float *)a.dlogits, a.dx,
                         a.dw ? dw_part : static_cast<float *>(nullptr), a.T, a.d, a.E,
                         ceil_div(a.T, pieces));
     };
-    e = a.E <= 8 ? run(k_route_proj<T, 8, 4>)
-                 : (a.E <= 16 ? run(k_route_proj<T, 16, 4>) : run(k_route_proj<T, 32, 2>));
+    if constexpr (sizeof(T) == 2)
+      e = run(k_route_proj<T, 8>);
+    else
+      e = a.E <= 8 ? run(k_route_proj<T, 8>) : run(k_route_proj<T, 16>);
     if (e != cudaSuccess) return e;
   }
   return sums<T>(a, dw_part, pieces, a.E, db_part, dz_lanes(a.E), st);
@@ -607,21 +603,28 @@ cudaError_t route_bwd_tc(const RouteBwdArgs &a, cudaStream_t st) {
 
 }  // namespace
 
+// Whether the one pass of k_route_proj takes the products. Against the tensor cores (bf16,
+// T = 4096, d = 4096): 36 us to 39 with 8 experts, 63 to 39 with 12, 167 to 40 with 32.
+// Against the tiles on CUDA cores (fp32): 43 us to 142 with 8 and 62 to 142 with 16, but 163
+// to 156 with 32, where a thread's registers hold half the columns.
+static bool few_experts(int E, int dtype) { return E <= (dtype == MOE_DTYPE_F32 ? 16 : 8); }
+
 bool route_bwd_reads_dlogits(int E, int dtype) {
-  return E <= kFewExperts || dtype == MOE_DTYPE_F32;
+  return few_experts(E, dtype) || dtype == MOE_DTYPE_F32;
 }
 
 size_t route_bwd_scratch_bytes(int T, int d, int E, int dtype) {
   if (T < 1) T = 1;
   if (!route_bwd_reads_dlogits(E, dtype)) return tc_scratch(T, d, E).total;
-  const int pieces = E <= kFewExperts ? proj_pieces(T, d, E) : dw_pieces(T, d, E);
+  const int pieces = few_experts(E, dtype) ? proj_pieces(T, d, E) : dw_pieces(T, d, E);
   return sizeof(float) * ((size_t)kMaxBlocks * E + (size_t)pieces * E * d);
 }
 
 cudaError_t launch_route_bwd(const RouteBwdArgs &a, int dtype, cudaStream_t st) {
   if (a.T == 0) return cudaSuccess;
   const bool f32 = dtype == MOE_DTYPE_F32;
-  if (a.E <= kFewExperts) return f32 ? route_bwd_few<float>(a, st) : route_bwd_few<__nv_bfloat16>(a, st);
+  if (few_experts(a.E, dtype))
+    return f32 ? route_bwd_few<float>(a, st) : route_bwd_few<__nv_bfloat16>(a, st);
   return f32 ? route_bwd_simt(a, st) : route_bwd_tc(a, st);
 }
 
