@@ -15,7 +15,7 @@
 //
 // A CTA pair's roles, barriers and bounded waits are those of the forward's GEMM
 // (ffn_tc.cu): warp 0 of each CTA loads its operand halves, warp 1 of the leader issues
-// the MMAs, warps 4.. drain tensor memory; a wait that runs out records
+// the MMAs (k_act_grad: warps 0 and 3, 1 and 2), warps 4.. drain tensor memory; a wait that runs out records
 // MOE_DEVERR_WAIT_TIMEOUT and ends both CTAs.
 #include <algorithm>
 #include <mutex>
