@@ -53,6 +53,7 @@ struct Setup {
   uint8_t *smem;
   Ctl *ctl;
   uint32_t tmem, peer_abort;
+  uint32_t full0;  // the leader's full[0] (pairs)
   int rank, c0, cstep;
 };
 
@@ -60,6 +61,7 @@ struct Setup {
 // threads complete a tile's accumulators, `drainers` warps of both CTAs drain them (one
 // arrival each).
 // `unit`: rows of a tile whose prefix over the experts goes to pre[] (0: their first rows).
+template <bool PAIR>
 __device__ __forceinline__ Setup set_up(uint8_t *raw, size_t bytes, int issuers, int drainers,
                                         const int32_t *poff, int G, int unit) {
   Setup s;
@@ -68,7 +70,7 @@ __device__ __forceinline__ Setup set_up(uint8_t *raw, size_t bytes, int issuers,
   s.ctl = reinterpret_cast<Ctl *>(s.smem + bytes);
   Ctl *ctl = s.ctl;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  s.rank = (int)cluster_ctarank();
+  s.rank = PAIR ? (int)cluster_ctarank() : 0;
   if (tid == 0) {
     for (int i = 0; i < kMaxStages; ++i) {
       mbar_init(&ctl->full[i], 1);
@@ -83,8 +85,13 @@ __device__ __forceinline__ Setup set_up(uint8_t *raw, size_t bytes, int issuers,
     fence_mbar_init();
   }
   if (warp == 2) {
-    tmem_alloc_pair(&ctl->tmem_base, kTmemCols);
-    tmem_relinquish_pair();
+    if constexpr (PAIR) {
+      tmem_alloc_pair(&ctl->tmem_base, kTmemCols);
+      tmem_relinquish_pair();
+    } else {
+      tmem_alloc(&ctl->tmem_base, kTmemCols);
+      tmem_relinquish();
+    }
   }
   pdl_wait();
   if (unit == 0) {
@@ -109,13 +116,20 @@ __device__ __forceinline__ Setup set_up(uint8_t *raw, size_t bytes, int issuers,
   }
   tc_fence_before();
   __syncthreads();
-  cluster_sync_all();  // both CTAs' barriers and tensor memory exist
+  if constexpr (PAIR) cluster_sync_all();  // both CTAs' barriers and tensor memory exist
   pdl_trigger();
   tc_fence_after();
   s.tmem = ctl->tmem_base;
-  s.peer_abort = mapa_rank(smem_u32(&ctl->abort_flag), (uint32_t)(s.rank ^ 1));
-  s.c0 = (int)cluster_index();
-  s.cstep = (int)cluster_count();
+  if constexpr (PAIR) {
+    s.peer_abort = mapa_rank(smem_u32(&ctl->abort_flag), (uint32_t)(s.rank ^ 1));
+    s.full0 = mapa_rank(smem_u32(&ctl->full[0]), 0);
+    s.c0 = (int)cluster_index();
+    s.cstep = (int)cluster_count();
+  } else {
+    s.peer_abort = s.full0 = 0;
+    s.c0 = (int)blockIdx.x;
+    s.cstep = (int)gridDim.x;
+  }
   return s;
 }
 
@@ -127,9 +141,31 @@ __device__ __forceinline__ bool wait_on(const Setup &s, uint64_t *bar, uint32_t 
                    limit_ns);
 }
 
+// arrive on `bar` (in both CTAs of a pair) once the MMAs issued so far are done
+template <bool PAIR>
+__device__ __forceinline__ void commit(uint64_t *bar) {
+  if constexpr (PAIR) umma_commit_pair_both(bar);
+  else umma_commit(bar);
+}
+template <bool PAIR>
+__device__ __forceinline__ void mma(uint32_t acc, uint64_t a, uint64_t b, uint32_t idesc,
+                                    bool accumulate) {
+  if constexpr (PAIR) umma_bf16_pair(acc, a, b, idesc, accumulate);
+  else umma_bf16(acc, a, b, idesc, accumulate);
+}
+// a draining warp's arrival on the leader's tempty[i] (tempty0: the first's address)
+template <bool PAIR>
+__device__ __forceinline__ void release_tmem(const Setup &s, uint32_t tempty0, int i) {
+  tc_fence_before();
+  __syncwarp();
+  if ((threadIdx.x & 31) != 0) return;
+  if constexpr (PAIR) mbar_arrive_remote(tempty0 + (uint32_t)(i * sizeof(uint64_t)));
+  else mbar_arrive(&s.ctl->tempty[i]);
+}
+
 // A ring of N operand stages of BYTES each, from stage FIRST of the barriers on; producer
 // and MMA issuer hold one each and walk through it in step.
-template <int N, int FIRST, int BYTES>
+template <bool PAIR, int N, int FIRST, int BYTES>
 struct Ring {
   uint8_t *base;
   int stage = 0;
@@ -138,14 +174,19 @@ struct Ring {
   // producer: the next stage, free to be filled with `bytes` by each CTA, or nullptr
   __device__ __forceinline__ uint8_t *acquire(const Setup &s, int bytes, int32_t *err, int site) {
     if (!wait_on(s, &s.ctl->empty[FIRST + stage], phase ^ 1u, err, site)) return nullptr;
-    if (s.rank == 0) mbar_expect_tx(&s.ctl->full[FIRST + stage], 2 * bytes);
+    if (s.rank == 0) mbar_expect_tx(&s.ctl->full[FIRST + stage], PAIR ? 2 * bytes : bytes);
     issued |= 1u << stage;
     last_phase = (last_phase & ~(1u << stage)) | (phase << stage);
     return base + (size_t)stage * BYTES;
   }
-  // ... its barrier (full0: the leader's first)
-  __device__ __forceinline__ uint32_t bar(uint32_t full0) const {
-    return full0 + (uint32_t)((FIRST + stage) * sizeof(uint64_t));
+  // ... and a copy into it
+  __device__ __forceinline__ void load(const Setup &s, const CUtensorMap *map, uint8_t *dst, int c0,
+                                       int c1) const {
+    if constexpr (PAIR) tma_load_2d_pair(map, bar(s), dst, c0, c1);
+    else tma_load_2d(map, &s.ctl->full[FIRST + stage], dst, c0, c1);
+  }
+  __device__ __forceinline__ uint32_t bar(const Setup &s) const {  // the leader's (pairs)
+    return s.full0 + (uint32_t)((FIRST + stage) * sizeof(uint64_t));
   }
   // issuer: the next stage, filled
   __device__ __forceinline__ bool filled(const Setup &s, int32_t *err, int site) const {
@@ -156,7 +197,7 @@ struct Ring {
   __device__ __forceinline__ uint32_t addr() const { return smem_u32(base) + stage * BYTES; }
   // ... handed back once the MMAs issued so far are done
   __device__ __forceinline__ void release(const Setup &s) const {
-    umma_commit_pair_both(&s.ctl->empty[FIRST + stage]);
+    commit<PAIR>(&s.ctl->empty[FIRST + stage]);
   }
   __device__ __forceinline__ void next() {
     if (++stage == N) { stage = 0; phase ^= 1u; }
@@ -171,28 +212,32 @@ struct Ring {
 };
 
 // issuer, at its end: the MMAs in flight retire before tensor memory is released
+template <bool PAIR>
 __device__ __forceinline__ void retire(const Setup &s, uint64_t *bar) {
-  umma_commit_pair_own(bar);
+  if constexpr (PAIR) umma_commit_pair_own(bar);
+  else umma_commit(bar);
   wait_on(s, bar, 0, nullptr, 0, false, kDrainNs);
 }
 
+template <bool PAIR>
 __device__ __forceinline__ void tear_down(const Setup &s) {
   if (*(volatile int *)&s.ctl->abort_flag) settle_ns(100000);  // copies in flight land
   tc_fence_before();
   __syncthreads();
-  cluster_sync_all();  // the peer's remote arrivals are done before either CTA exits
+  if constexpr (PAIR) cluster_sync_all();  // the peer's remote arrivals are done before exit
   if ((threadIdx.x >> 5) == 2) {
     tc_fence_after();
-    tmem_dealloc_pair(s.tmem, kTmemCols);
+    if constexpr (PAIR) tmem_dealloc_pair(s.tmem, kTmemCols);
+    else tmem_dealloc(s.tmem, kTmemCols);
   }
 }
 
-// First row of this CTA's half of row tile m of expert g, or `rows` (past the operand's
+// First row of this CTA's half of the tile that begins at row m0 of expert g, or `rows` (past the operand's
 // bounds: zeros, no traffic) when the expert ends before it. The MMAs of such a half take
 // their time all the same, but on zeros, which cost less of the power that limits long
 // grids.
-__device__ __forceinline__ int first_row(const int32_t *poff, int g, int m, int rank, int rows) {
-  const int r = poff[g] + m * kPairM + rank * kRowTile;
+__device__ __forceinline__ int first_row(const int32_t *poff, int g, int m0, int rank, int rows) {
+  const int r = poff[g] + m0 + rank * kRowTile;
   return r < poff[g + 1] ? r : rows;
 }
 
@@ -265,14 +310,20 @@ __device__ __forceinline__ void gelu_and_slope(float v, float &h, float &s) {
 // a loading and an issuing thread of their own: one thread for both spent more time on
 // issuing (about 400 clocks a slice and thread) than the MMAs took, and q of the next tile
 // runs while the epilogue drains the one a | u region of SwiGLU.
+// Experts of few rows (MLP, at most 128 on average) take single-CTA tiles of 128 rows
+// (PAIR false): a pair's MMAs take their time for 256 rows, and shared memory's bandwidth
+// bounds them: some 940 clocks a slice for a pair against 1060 for one CTA.
 constexpr int kTileN = 128;
-template <bool GLU>
+template <bool GLU, bool PAIR>
 struct ActCfg {
+  static_assert(PAIR || !GLU, "SwiGLU: pairs only");
+  static constexpr int kTileM = PAIR ? kPairM : kRowTile;
   static constexpr int kEpiWarps = GLU ? 8 : 16;  // MLP tiles are shorter, their epilogue longer
   static constexpr int kThreads = 128 + 32 * kEpiWarps;
-  static constexpr int kBytesQ = kOperand + kMnBlock;
-  static constexpr int kBytesA = GLU ? 2 * kOperand : kOperand + kMnBlock;
-  static constexpr int kStagesQ = GLU ? 3 : 4, kStagesA = 4;
+  static constexpr int kWeights = PAIR ? kMnBlock : kOperand;  // a CTA's share of 128 columns
+  static constexpr int kBytesQ = kOperand + kWeights;
+  static constexpr int kBytesA = GLU ? 2 * kOperand : kOperand + kWeights;
+  static constexpr int kStagesQ = GLU || !PAIR ? 3 : 4, kStagesA = PAIR ? 4 : 3;
   // K slices of one accumulation. The tensor cores truncate what they add, a bias of some
   // 2^-26 of the sum for each 16 products (-4.3e-6 at d = 4096). It does not matter beside
   // the rounding of h and da, but db1 keeps it: with biases (MLP) the epilogue adds up
@@ -283,14 +334,15 @@ struct ActCfg {
   static constexpr size_t kSmem = kBytes + sizeof(Ctl) + 1024;
 };
 
-template <bool GLU>
-__global__ void __launch_bounds__(ActCfg<GLU>::kThreads, 1)
+template <bool GLU, bool PAIR>
+__global__ void __launch_bounds__(ActCfg<GLU, PAIR>::kThreads, 1)
 k_act_grad(const __grid_constant__ ActMaps maps, ActArgs a) {
-  using C = ActCfg<GLU>;
-  using RingQ = Ring<C::kStagesQ, 0, C::kBytesQ>;
-  using RingA = Ring<C::kStagesA, C::kStagesQ, C::kBytesA>;
+  using C = ActCfg<GLU, PAIR>;
+  using RingQ = Ring<PAIR, C::kStagesQ, 0, C::kBytesQ>;
+  using RingA = Ring<PAIR, C::kStagesA, C::kStagesQ, C::kBytesA>;
   extern __shared__ uint8_t smem_raw[];
-  const Setup s = set_up(smem_raw, C::kBytes, 2, 2 * C::kEpiWarps, a.poff, a.G, kPairM);
+  const Setup s = set_up<PAIR>(smem_raw, C::kBytes, 2, (PAIR ? 2 : 1) * C::kEpiWarps, a.poff, a.G,
+                               C::kTileM);
   Ctl *ctl = s.ctl;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int total = ctl->pre[a.G] * a.n_tiles;
@@ -301,20 +353,20 @@ k_act_grad(const __grid_constant__ ActMaps maps, ActArgs a) {
     // ----------------------------------------------- TMA producer of dy and W2
     prefetch_map(&maps.dy);
     prefetch_map(&maps.w2);
-    const uint32_t full0 = mapa_rank(smem_u32(&ctl->full[0]), 0);
     RingQ ring(ring_q);
     bool ok = true;
     for (int t = s.c0; ok && t < total; t += s.cstep) {
       int g, n, m;
       decode_tile(t, ctl->pre, a.G, a.n_tiles, g, n, m);
-      const int arow = first_row(a.poff, g, m, s.rank, a.x_rows);
+      const int arow = first_row(a.poff, g, m * C::kTileM, s.rank, a.x_rows);
       const int col = n * kTileN + s.rank * kBlockK, brow = g * a.d;
       for (int i = 0; i < nkb; ++i) {
         uint8_t *st = ring.acquire(s, C::kBytesQ, a.err, 21);
         if (!(ok = st != nullptr)) break;
-        const uint32_t bar = ring.bar(full0);
-        tma_load_2d_pair(&maps.dy, bar, st, i * kBlockK, arow);
-        tma_load_2d_pair(&maps.w2, bar, st + kOperand, col, brow + i * kBlockK);
+        ring.load(s, &maps.dy, st, i * kBlockK, arow);
+        ring.load(s, &maps.w2, st + kOperand, col, brow + i * kBlockK);
+        if (!PAIR)  // both blocks of 64 columns
+          ring.load(s, &maps.w2, st + kOperand + kMnBlock, col + kBlockK, brow + i * kBlockK);
         ring.next();
       }
     }
@@ -324,27 +376,25 @@ k_act_grad(const __grid_constant__ ActMaps maps, ActArgs a) {
     const CUtensorMap *w = GLU && s.rank ? &maps.w3 : &maps.w1;
     prefetch_map(&maps.x);
     prefetch_map(w);
-    const uint32_t full0 = mapa_rank(smem_u32(&ctl->full[0]), 0);
     RingA ring(ring_a);
     bool ok = true;
     for (int t = s.c0; ok && t < total; t += s.cstep) {
       int g, n, m;
       decode_tile(t, ctl->pre, a.G, a.n_tiles, g, n, m);
-      const int arow = first_row(a.poff, g, m, s.rank, a.x_rows);
+      const int arow = first_row(a.poff, g, m * C::kTileM, s.rank, a.x_rows);
       const int brow = g * a.F + n * kTileN + (GLU ? 0 : s.rank * kBlockK);
       for (int i = 0; i < nkb; ++i) {
         uint8_t *st = ring.acquire(s, C::kBytesA, a.err, 21);
         if (!(ok = st != nullptr)) break;
-        const uint32_t bar = ring.bar(full0);
-        tma_load_2d_pair(&maps.x, bar, st, i * kBlockK, arow);
-        tma_load_2d_pair(w, bar, st + kOperand, i * kBlockK, brow);
+        ring.load(s, &maps.x, st, i * kBlockK, arow);
+        ring.load(s, w, st + kOperand, i * kBlockK, brow);
         ring.next();
       }
     }
     ring.drain(s, ok);
   } else if (warp == 1 && lane == 0 && s.rank == 0) {
     // ------------------------------------------------------------ MMAs of q
-    constexpr uint32_t idesc = make_idesc(kPairM, kTileN) | kIdescMnB;
+    constexpr uint32_t idesc = make_idesc(C::kTileM, kTileN) | kIdescMnB;
     RingQ ring(ring_q);
     bool ok = true, any = false;
     int it = 0;
@@ -361,18 +411,18 @@ k_act_grad(const __grid_constant__ ActMaps maps, ActArgs a) {
           const uint64_t xb = sw128_desc_mn(ring.addr() + kOperand, kMnBlock);
 #pragma unroll
           for (int kk = 0; kk < kBlockK / 16; ++kk)
-            umma_bf16_pair(acc, xa + 2 * kk, xb + 128 * kk, idesc, ((i - i0) | kk) != 0);
+            mma<PAIR>(acc, xa + 2 * kk, xb + 128 * kk, idesc, ((i - i0) | kk) != 0);
           any = true;
           ring.release(s);
           ring.next();
         }
-        if (ok) umma_commit_pair_both(&ctl->tfull[buf]);
+        if (ok) commit<PAIR>(&ctl->tfull[buf]);
       }
     }
-    if (!ok && any) retire(s, &ctl->drain[0]);
+    if (!ok && any) retire<PAIR>(s, &ctl->drain[0]);
   } else if (warp == 2 && lane == 0 && s.rank == 0) {
     // ------------------------------------------------------- MMAs of a (| u)
-    constexpr uint32_t idesc = make_idesc(kPairM, GLU ? 2 * kTileN : kTileN);
+    constexpr uint32_t idesc = make_idesc(C::kTileM, GLU ? 2 * kTileN : kTileN);
     RingA ring(ring_a);
     bool ok = true, any = false;
     int it = 0;
@@ -390,27 +440,27 @@ k_act_grad(const __grid_constant__ ActMaps maps, ActArgs a) {
           const uint64_t xa = sw128_desc(ring.addr()), xb = sw128_desc(ring.addr() + kOperand);
 #pragma unroll
           for (int kk = 0; kk < kBlockK / 16; ++kk)
-            umma_bf16_pair(acc, xa + 2 * kk, xb + 2 * kk, idesc, ((i - i0) | kk) != 0);
+            mma<PAIR>(acc, xa + 2 * kk, xb + 2 * kk, idesc, ((i - i0) | kk) != 0);
           any = true;
           ring.release(s);
           ring.next();
         }
-        if (ok) umma_commit_pair_both(&ctl->tfull[buf]);
+        if (ok) commit<PAIR>(&ctl->tfull[buf]);
       }
     }
-    if (!ok && any) retire(s, &ctl->drain[1]);
+    if (!ok && any) retire<PAIR>(s, &ctl->drain[1]);
   } else if (warp >= 4) {
     // ----------------------------------------------------------------- epilogue
     const int ew = warp & 3, part = (warp - 4) >> 2;  // lanes 32 ew.., column chunks part..
     constexpr int kParts = C::kEpiWarps / 4;
-    const uint32_t tempty0 = mapa_rank(smem_u32(&ctl->tempty[0]), 0);
+    const uint32_t tempty0 = PAIR ? mapa_rank(smem_u32(&ctl->tempty[0]), 0) : 0u;
     uint8_t *stage = s.smem + C::kRings + (warp - 4) * kStageOutBytes;
     int it = 0;
     bool ok = true;
     for (int t = s.c0; ok && t < total; t += s.cstep) {
       int g, n, m;
       decode_tile(t, ctl->pre, a.G, a.n_tiles, g, n, m);
-      const int lrow = m * kPairM + s.rank * kRowTile + ew * 32;  // the warp's first row
+      const int lrow = m * C::kTileM + s.rank * kRowTile + ew * 32;  // the warp's first row
       const int prow = a.poff[g] + lrow;
       // padded groups of 32 rows belong to the expert as a whole or not at all; F is a
       // multiple of 64
@@ -424,11 +474,7 @@ k_act_grad(const __grid_constant__ ActMaps maps, ActArgs a) {
         if (ok) tc_fence_after();
         return ok;
       };
-      auto drained = [&]() {
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_remote(tempty0 + (uint32_t)((it & 1) * sizeof(uint64_t)));
-      };
+      auto drained = [&]() { release_tmem<PAIR>(s, tempty0, it & 1); };
       const uint32_t lanes = s.tmem + ((uint32_t)(ew * 32) << 16);
       float as[GLU ? 1 : 32], qs[GLU ? 1 : 32];  // MLP: the warp's one chunk, all parts
       if constexpr (GLU) {
@@ -544,7 +590,7 @@ k_act_grad(const __grid_constant__ ActMaps maps, ActArgs a) {
     if (lane == 0) bulk_wait_all();  // this warp's output stores are done
     __syncwarp();
   }
-  tear_down(s);
+  tear_down<PAIR>(s);
 }
 
 // ============================================================ dx and the weights
@@ -577,13 +623,13 @@ constexpr int kStageOut = 4096;  // output staging of an epilogue warp
 constexpr size_t kGemmRing = (size_t)kGemmStages * kGemmStageBytes;
 constexpr size_t kGemmBytes = kGemmRing + (size_t)kGemmEpiWarps * kStageOut;
 constexpr size_t kGemmSmem = kGemmBytes + sizeof(Ctl) + 1024;
-using GemmRing = Ring<kGemmStages, 0, kGemmStageBytes>;
+using GemmRing = Ring<true, kGemmStages, 0, kGemmStageBytes>;
 
 __global__ void __launch_bounds__(kGemmThreads, 1)
 k_pair_gemm(const __grid_constant__ GemmMaps maps, GemmArgs a) {
   extern __shared__ uint8_t smem_raw[];
   // the groups' first rows of the sums stay in shared memory: their tiles can be short
-  const Setup s = set_up(smem_raw, kGemmBytes, 1, 2 * kGemmEpiWarps, a.first, a.groups, 0);
+  const Setup s = set_up<true>(smem_raw, kGemmBytes, 1, 2 * kGemmEpiWarps, a.first, a.groups, 0);
   Ctl *ctl = s.ctl;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // sums: a group's tiles are those of job 0, then 1, then 2 (end: their prefix)
@@ -638,7 +684,7 @@ k_pair_gemm(const __grid_constant__ GemmMaps maps, GemmArgs a) {
       r.m0 = m * kPairM;
       r.n0 = n * 256;
       r.nkb = a.nseg * nk1;
-      r.row0 = first_row(a.poff, r.g, m, s.rank, a.a_rows);
+      r.row0 = first_row(a.poff, r.g, r.m0, s.rank, a.a_rows);
     }
   };
   auto first_tile = [&]() {
@@ -661,7 +707,6 @@ k_pair_gemm(const __grid_constant__ GemmMaps maps, GemmArgs a) {
       prefetch_map(&maps.sa[j]);
       prefetch_map(&maps.sb[j]);
     }
-    const uint32_t full0 = mapa_rank(smem_u32(&ctl->full[0]), 0);
     GemmRing ring(s.smem);
     bool ok = true;
     for (Tile q = first_tile(); ok && q.t < total; next_tile(q)) {
@@ -670,7 +715,7 @@ k_pair_gemm(const __grid_constant__ GemmMaps maps, GemmArgs a) {
       for (int kb = 0; kb < q.nkb; ++kb) {
         uint8_t *st = ring.acquire(s, kGemmStageBytes, a.err, 31);
         if (!(ok = st != nullptr)) break;
-        const uint32_t bar = ring.bar(full0);
+        const uint32_t bar = ring.bar(s);
         if (q.sums) {
           const int r = row0 + kb * kBlockK;
           tma_load_3d_pair(&maps.sa[q.job], bar, st, 0, r, q.m0 / kBlockK + 2 * s.rank);
@@ -714,7 +759,7 @@ k_pair_gemm(const __grid_constant__ GemmMaps maps, GemmArgs a) {
       }
       if (ok) umma_commit_pair_both(&ctl->tfull[buf]);
     }
-    if (!ok && any) retire(s, &ctl->drain[0]);
+    if (!ok && any) retire<true>(s, &ctl->drain[0]);
   } else if (warp >= 4) {
     // ----------------------------------------------------------------- epilogue
     const int ew = warp & 3, part = (warp - 4) >> 2;  // lanes 32 ew.., columns 64 part..
@@ -805,9 +850,7 @@ k_pair_gemm(const __grid_constant__ GemmMaps maps, GemmArgs a) {
           }
         }
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_remote(tempty0 + (uint32_t)(buf * sizeof(uint64_t)));
+      release_tmem<true>(s, tempty0, buf);
       if (mine && staged && !f32) {
         fence_proxy_async_smem();
         __syncwarp();
@@ -820,25 +863,25 @@ k_pair_gemm(const __grid_constant__ GemmMaps maps, GemmArgs a) {
     if (lane == 0) bulk_wait_all();
     __syncwarp();
   }
-  tear_down(s);
+  tear_down<true>(s);
 }
 
 // ------------------------------------------------------------------ host side
 std::mutex g_mu;
 
-// A persistent grid of CTA pairs, at most `tiles` of them; `slot` names the kernel in the
-// per-device table of grid sizes.
-template <typename... KArgs, typename... Args>
-cudaError_t launch_pairs(void (*kernel)(KArgs...), int slot, int threads, size_t smem,
+// A persistent grid of CTA pairs (or CTAs), at most `tiles` of them; `slot` names the kernel
+// in the per-device table of grid sizes.
+template <bool PAIR, typename... KArgs, typename... Args>
+cudaError_t launch_grid(void (*kernel)(KArgs...), int slot, int threads, size_t smem,
                          long long tiles, cudaStream_t st, const Args &...args) {
-  static int max_pairs[64][3] = {};
+  static int max_groups[64][4] = {};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.x = PAIR ? 2 : 1;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -848,21 +891,24 @@ cudaError_t launch_pairs(void (*kernel)(KArgs...), int slot, int threads, size_t
   cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  int &most = max_pairs[dev & 63][slot];
+  int &most = max_groups[dev & 63][slot];
   {
     std::lock_guard<std::mutex> lock(g_mu);
     if (most == 0) {
       e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                (int)smem);
       if (e != cudaSuccess) return e;
-      cfg.gridDim = dim3(2 * (sm_count() / 2));
-      int n = 0;
-      if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n <= 0)
-        n = sm_count() / 2;
+      int n = PAIR ? sm_count() / 2 : sm_count();
+      if (PAIR) {
+        cfg.gridDim = dim3(2 * n);
+        int fit = 0;
+        if (cudaOccupancyMaxActiveClusters(&fit, kernel, &cfg) == cudaSuccess && fit > 0) n = fit;
+      }
       most = n;
     }
   }
-  cfg.gridDim = dim3((unsigned)(2 * std::max<long long>(1, std::min<long long>(tiles, most))));
+  cfg.gridDim = dim3((unsigned)((PAIR ? 2 : 1) *
+                                std::max<long long>(1, std::min<long long>(tiles, most))));
   cfg.numAttrs = take_pdl() ? 2 : 1;
   e = cudaLaunchKernelEx(&cfg, kernel, args...);
   return e == cudaSuccess ? cudaGetLastError() : e;
@@ -872,11 +918,12 @@ cudaError_t launch_pairs(void (*kernel)(KArgs...), int slot, int threads, size_t
 
 cudaError_t launch_act_grad_tc(const FfnGradArgs &f, cudaStream_t st) {
   const bool glu = f.act == MOE_ACT_SWIGLU;
+  const bool single = !glu && f.row_bound <= (long long)kRowTile * f.G;
   ActMaps m;
   const uint64_t R = (uint64_t)f.rows, X = (uint64_t)f.x_rows, d = (uint64_t)f.d,
                  F = (uint64_t)f.F, G = (uint64_t)f.G;
   bool ok = make_map(&m.x, f.x, X, d, kRowTile) && make_map(&m.dy, f.dy, X, d, kRowTile) &&
-            make_map(&m.w1, f.w1, G * F, d, glu ? kRowTile : kBlockK) &&
+            make_map(&m.w1, f.w1, G * F, d, glu || single ? kRowTile : kBlockK) &&
             make_map(&m.w2, f.w2, G * d, F, kBlockK) && make_store_map(&m.h, f.h, R, F) &&
             make_store_map(&m.dg, f.dg, R, F);
   m.w3 = m.w1;
@@ -900,10 +947,14 @@ cudaError_t launch_act_grad_tc(const FfnGradArgs &f, cudaStream_t st) {
   a.x_rows = f.x_rows;
   a.err = f.err;
   const long long tiles = (long long)f.pair_tiles_ub * a.n_tiles;
-  return glu ? launch_pairs(k_act_grad<true>, 0, ActCfg<true>::kThreads, ActCfg<true>::kSmem,
-                            tiles, st, m, a)
-             : launch_pairs(k_act_grad<false>, 1, ActCfg<false>::kThreads, ActCfg<false>::kSmem,
-                            tiles, st, m, a);
+  if (glu)
+    return launch_grid<true>(k_act_grad<true, true>, 0, ActCfg<true, true>::kThreads,
+                             ActCfg<true, true>::kSmem, tiles, st, m, a);
+  if (single)
+    return launch_grid<false>(k_act_grad<false, false>, 3, ActCfg<false, false>::kThreads,
+                              ActCfg<false, false>::kSmem, 2 * tiles, st, m, a);
+  return launch_grid<true>(k_act_grad<false, true>, 1, ActCfg<false, true>::kThreads,
+                           ActCfg<false, true>::kSmem, tiles, st, m, a);
 }
 
 cudaError_t launch_products_tc(const FfnGradArgs &f, cudaStream_t st) {
@@ -953,7 +1004,7 @@ cudaError_t launch_products_tc(const FfnGradArgs &f, cudaStream_t st) {
   a.first = f.poff;
   a.groups = f.G;
   a.err = f.err;
-  return launch_pairs(k_pair_gemm, 2, kGemmThreads, kGemmSmem, tiles, st, m, a);
+  return launch_grid<true>(k_pair_gemm, 2, kGemmThreads, kGemmSmem, tiles, st, m, a);
 }
 
 cudaError_t launch_route_tc(const RouteTcArgs &r, cudaStream_t st) {
@@ -997,7 +1048,7 @@ cudaError_t launch_route_tc(const RouteTcArgs &r, cudaStream_t st) {
   if (!ok) return cudaErrorInvalidValue;
   a.first = r.piece;  // (read up to `groups`, which is 0 without dw)
   a.err = r.err;
-  return launch_pairs(k_pair_gemm, 2, kGemmThreads, kGemmSmem, tiles, st, m, a);
+  return launch_grid<true>(k_pair_gemm, 2, kGemmThreads, kGemmSmem, tiles, st, m, a);
 }
 
 }  // namespace moe

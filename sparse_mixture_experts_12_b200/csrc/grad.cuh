@@ -98,6 +98,7 @@ struct FfnGradArgs {
   int x_rows;                // rows allocated in x and dy (rows past the experts' are zero
                              // up to the padding, or not allocated)
   int rows;                  // rows allocated in the scratch, row_w and row_dot
+  long long row_bound;       // rows the experts may have in all
   const int32_t *offsets;    // [G+1] checked (all zero when the caller's were invalid):
                              // expert g has offsets[g+1] - offsets[g] rows
   const int32_t *poff;       // [G+1] its first row in all arrays but dx

@@ -127,6 +127,7 @@ FfnGradArgs expert_args(const moe_cfg_t &c, const moe_weights_t &w, const moe_gr
                         const Layout &L) {
   FfnGradArgs a{};
   a.rows = a.x_rows = (int)scratch_rows(c);
+  a.row_bound = expert_rows(c);
   a.offsets = at<int32_t>(ws, L, G_OFFSETS);
   a.mprefix = at<int32_t>(ws, L, G_MPREFIX);
   a.pre256 = at<int32_t>(ws, L, G_PRE256);
@@ -398,6 +399,7 @@ MOE_API moe_status_t moe_backward(const moe_cfg_t *cfg, const moe_weights_t *w, 
     s.dy = dy;
     s.x_rows = c.n_tokens;  // the padding rows lie past the operands' bounds: read as zero
     s.rows = (int)padded_rows_ub(c.n_tokens, 1, row_pad(c.dtype));
+    s.row_bound = c.n_tokens;
     s.offsets = tab;
     s.mprefix = tab + 2;
     s.pre256 = tab + 4;
