@@ -478,6 +478,38 @@ cudaError_t ffn_bwd_f32(const FfnGradArgs &a, cudaStream_t st) {
   return a.F % 4 == 0 ? ffn_bwd_f32<TD, true>(a, st) : ffn_bwd_f32<TD, false>(a, st);  // d always is
 }
 
+// dx of the padded rows from its parts, in order: a warp per row
+template <typename TO>
+__global__ void __launch_bounds__(kThreads) k_dx_join(FfnGradArgs s, int splits) {
+  pdl_wait();
+  pdl_trigger();
+  const int p = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  if (p >= s.poff[s.G]) return;
+  int lo = 0, hi = s.G - 1;  // last g with poff[g] <= p
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (s.poff[mid] <= p) lo = mid; else hi = mid - 1;
+  }
+  const int local = p - s.poff[lo];
+  if (local >= s.offsets[lo + 1] - s.offsets[lo]) return;
+  const float *from = s.dx_part + (size_t)p * s.d;
+  TO *to = static_cast<TO *>(s.dx) + (size_t)(s.dx_off[lo] + local) * s.d;
+  const size_t all = (size_t)s.rows * s.d;
+  for (int i = 4 * lane; i < s.d; i += 128) {
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int j = 0; j < splits; ++j) {
+      const float4 q = __ldg(reinterpret_cast<const float4 *>(from + j * all + i));
+      v.x += q.x; v.y += q.y; v.z += q.z; v.w += q.w;
+    }
+    if constexpr (sizeof(TO) == 4)
+      *reinterpret_cast<float4 *>(to + i) = v;
+    else
+      *reinterpret_cast<uint2 *>(to + i) =
+          make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+  }
+}
+
 // bf16: the steps on the tensor cores
 cudaError_t ffn_bwd_tc(const FfnGradArgs &a, cudaStream_t st) {
   cudaError_t e = cudaSuccess;
@@ -497,7 +529,13 @@ cudaError_t ffn_bwd_tc(const FfnGradArgs &a, cudaStream_t st) {
                    q);
     if (e != cudaSuccess) return e;
   }
-  return launch_products_tc(a, st);
+  const int splits =
+      a.dx ? dx_splits_tc(a.pair_tiles_ub, a.d, a.F, a.act == MOE_ACT_SWIGLU) : 1;
+  e = launch_products_tc(a, splits, st);
+  if (e != cudaSuccess || splits == 1) return e;
+  const dim3 g(ceil_div(a.rows, 8)), b(kThreads);
+  return a.dx_f32 ? launch_pdl(k_dx_join<float>, g, b, 0, st, a, splits)
+                  : launch_pdl(k_dx_join<__nv_bfloat16>, g, b, 0, st, a, splits);
 }
 
 }  // namespace

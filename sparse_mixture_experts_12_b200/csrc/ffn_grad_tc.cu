@@ -602,6 +602,8 @@ struct GemmArgs {
   // in the output; N columns, reduction length K
   const int32_t *poff, *offsets, *pre, *out_off;
   int G, N, K, nseg, a_rows;
+  int splits, piece;      // the nseg K / 64 slices in `splits` parts of `piece`, each with an
+  int part_rows;          // output of its own, part_rows rows apart
   void *out;
   int out_f32;
   int clipped;            // no other rows lie in a group's last 32 (padding, or the output
@@ -645,13 +647,14 @@ k_pair_gemm(const __grid_constant__ GemmMaps maps, GemmArgs a) {
     }
   }
   const int per = end[2], n_tiles = ceil_div(a.N, 256);
-  const int row_tiles = n_tiles ? a.pre[a.G] * n_tiles : 0;
+  const int one_split = n_tiles ? a.pre[a.G] * n_tiles : 0, row_tiles = one_split * a.splits;
   const int total = row_tiles + a.groups * per;
   // a tile: group, job (sums), first row and column, K slices; and the walk over every
   // cstep-th of them
   struct Tile {
     int t, g, job, m0, n0, nkb;
     int row0;   // sums: the reduction's first row; rows: this CTA's first row of A
+    int split;  // rows
     bool sums;
   };
   const int nk1 = ceil_div(a.K, kBlockK);
@@ -679,16 +682,21 @@ k_pair_gemm(const __grid_constant__ GemmMaps maps, GemmArgs a) {
       r.row0 = ctl->pre[r.g];
       r.nkb = (ctl->pre[r.g + 1] - r.row0) / kBlockK;
     } else {
-      int n, m;
-      decode_tile(r.t, a.pre, a.G, n_tiles, r.g, n, m);
+      int n, m, t = r.t;
+      r.split = 0;
+      while (t >= one_split) {
+        t -= one_split;
+        ++r.split;
+      }
+      decode_tile(t, a.pre, a.G, n_tiles, r.g, n, m);
       r.m0 = m * kPairM;
       r.n0 = n * 256;
-      r.nkb = a.nseg * nk1;
+      r.nkb = min(a.piece, a.nseg * nk1 - r.split * a.piece);
       r.row0 = first_row(a.poff, r.g, r.m0, s.rank, a.a_rows);
     }
   };
   auto first_tile = [&]() {
-    Tile r{s.c0, 0, 0, 0, 0, 0, 0, false};
+    Tile r{s.c0, 0, 0, 0, 0, 0, 0, 0, false};
     place(r);
     return r;
   };
@@ -711,7 +719,12 @@ k_pair_gemm(const __grid_constant__ GemmMaps maps, GemmArgs a) {
     bool ok = true;
     for (Tile q = first_tile(); ok && q.t < total; next_tile(q)) {
       const int row0 = q.row0, bblk = q.n0 / kBlockK + 2 * s.rank;
-      int seg = 0, k = 0;  // pair of operands, slice of it
+      // pair of operands, slice of it
+      int seg = 0, k = q.sums ? 0 : q.split * a.piece;
+      while (!q.sums && k >= nk1) {
+        k -= nk1;
+        ++seg;
+      }
       for (int kb = 0; kb < q.nkb; ++kb) {
         uint8_t *st = ring.acquire(s, kGemmStageBytes, a.err, 31);
         if (!(ok = st != nullptr)) break;
@@ -778,7 +791,7 @@ k_pair_gemm(const __grid_constant__ GemmMaps maps, GemmArgs a) {
       } else {
         rows = a.offsets[q.g + 1] - a.offsets[q.g];
         N = a.N;
-        orow = (size_t)a.out_off[q.g] + lrow;
+        orow = (size_t)q.split * a.part_rows + a.out_off[q.g] + lrow;
       }
       const bool mine = lrow < rows && col0 < N;  // N is a multiple of 64
       const bool valid = lrow + lane < rows;
@@ -957,7 +970,7 @@ cudaError_t launch_act_grad_tc(const FfnGradArgs &f, cudaStream_t st) {
                            ActCfg<false, true>::kSmem, tiles, st, m, a);
 }
 
-cudaError_t launch_products_tc(const FfnGradArgs &f, cudaStream_t st) {
+cudaError_t launch_products_tc(const FfnGradArgs &f, int splits, cudaStream_t st) {
   const bool glu = f.act == MOE_ACT_SWIGLU;
   const uint64_t R = (uint64_t)f.rows, X = (uint64_t)f.x_rows, d = (uint64_t)f.d,
                  F = (uint64_t)f.F, G = (uint64_t)f.G;
@@ -982,8 +995,17 @@ cudaError_t launch_products_tc(const FfnGradArgs &f, cudaStream_t st) {
     a.a_rows = f.rows;
     a.out = f.dx;
     a.out_f32 = f.dx_f32;
-    a.clipped = f.dx_off == f.poff;  // the rows behind an expert's are its own padding
-    tiles += (long long)f.pair_tiles_ub * ceil_div(f.d, 256);
+    a.splits = splits;
+    a.piece = ceil_div(a.nseg * ceil_div(f.F, kBlockK), splits);
+    if (splits > 1) {
+      ok = ok && make_f32_map(&m.o, f.dx_part, (uint64_t)splits * R, d);
+      a.out = f.dx_part;
+      a.out_f32 = 1;
+      a.out_off = f.poff;
+      a.part_rows = f.rows;
+    }
+    a.clipped = a.out_off == f.poff;  // the rows behind an expert's are its own padding
+    tiles += (long long)f.pair_tiles_ub * ceil_div(f.d, 256) * splits;
   }
   auto job = [&](const void *p, uint64_t prows, const void *q, uint64_t qrows, void *out, int M,
                  int N) {
@@ -1026,6 +1048,8 @@ cudaError_t launch_route_tc(const RouteTcArgs &r, cudaStream_t st) {
     a.N = r.d;
     a.K = r.Ep;
     a.nseg = kSplit;
+    a.splits = 1;
+    a.piece = kSplit * ceil_div(r.Ep, kBlockK);
     a.a_rows = r.T;
     a.out = r.dx;
     a.out_f32 = 1;

@@ -115,7 +115,7 @@ struct FfnGradArgs {
   float *dot_part;           // [ceil(F / 32), rows] scratch (with row_dot)
   void *h, *dg, *du;         // [rows, F] dtype scratch: w h, w dg, w du
   void *dx;                  // [dx_rows, d] or nullptr
-  float *dx_part;            // [dx_splits(), rows, d] scratch (fp32 layers)
+  float *dx_part;            // [dx_splits() or dx_splits_tc(), rows, d] scratch
   int dx_f32, dx_rows;
   void *dw1, *dw3, *dw2;     // [G, F, d], [G, F, d], [G, d, F] dtype, or nullptr
   float *db1, *db2;          // [G, F], [G, d] fp32, or nullptr
@@ -125,7 +125,8 @@ struct FfnGradArgs {
 cudaError_t launch_ffn_bwd(const FfnGradArgs &a, int dtype, cudaStream_t st);
 // its steps on the tensor cores (bf16)
 cudaError_t launch_act_grad_tc(const FfnGradArgs &a, cudaStream_t st);
-cudaError_t launch_products_tc(const FfnGradArgs &a, cudaStream_t st);
+// splits > 1: dx in parts (fp32, the padded rows) to dx_part [splits, rows, d]
+cudaError_t launch_products_tc(const FfnGradArgs &a, int splits, cudaStream_t st);
 
 // Rows to which each expert's are padded: the K slice of the tensor-core products of the
 // weights' gradients (bf16), none on CUDA cores.
@@ -150,6 +151,16 @@ inline int dx_splits(int m_tiles, int d, int F, bool glu) {
   const long long fill = tiles > 0 ? (296 + tiles - 1) / tiles : 1;
   const int s = fill < most ? (int)fill : most, exact = ceil_div(F, glu ? 512 : 1024);
   return s > exact ? s : exact;
+}
+// ... and its CTA-pair tiles (bf16): where they leave half of the pairs without one, into as
+// many as fill them, of sixteen 64-wide slices at least. (Two rows of two experts of 64 x
+// 7104: 222 slices one after another took 78 of 88 us.)
+inline int dx_splits_tc(int pair_tiles, int d, int F, bool glu) {
+  const long long tiles = (long long)pair_tiles * ceil_div(d, 256);
+  const int slices = (glu ? 2 : 1) * ceil_div(F, 64);
+  if (tiles == 0 || 2 * tiles > 74 || slices < 32) return 1;
+  const int fill = (int)(74 / tiles), s = fill < slices / 16 ? fill : slices / 16;
+  return ceil_div(slices, ceil_div(slices, s));  // none of them empty
 }
 inline int grad_tiles_ub(long long rows, int G, int unit) {
   return (int)(rows / unit + (rows < G ? rows : G));

@@ -57,13 +57,18 @@ Layout layout_for(const moe_cfg_t &c) {
   sz[G_DY] = copies ? R * d * eb : 0;
   sz[G_INV] = tc ? T * (size_t)c.top_k * 4 : 0;
   sz[G_DX] = tc ? R * d * 4 : 0;
-  sz[G_DX_PART] = 0;
+  const int us = grad_tile_rows(c.n_tokens, 1);
+  const int pt = grad_tiles_ub(expert_rows(c), c.n_experts, 2 * kRowTile);
+  const int pt_sh = ceil_div(c.n_tokens, 2 * kRowTile);
+  size_t parts, parts_sh;  // of dx: the routed experts', the shared experts'
   if (c.dtype == MOE_DTYPE_F32) {
-    const int us = grad_tile_rows(c.n_tokens, 1);
-    sz[G_DX_PART] = larger((size_t)dx_splits(tiles, c.d_model, c.d_ff, glu) * R,
-                           Fs ? (size_t)dx_splits(ceil_div(c.n_tokens, us), c.d_model, (int)Fs, true) * T : 0) *
-                    d * 4;
+    parts = (size_t)dx_splits(tiles, c.d_model, c.d_ff, glu);
+    parts_sh = (size_t)dx_splits(ceil_div(c.n_tokens, us), c.d_model, (int)Fs, true);
+  } else {
+    parts = (size_t)dx_splits_tc(pt, c.d_model, c.d_ff, glu);
+    parts_sh = (size_t)dx_splits_tc(pt_sh, c.d_model, (int)Fs, true);
   }
+  sz[G_DX_PART] = larger(parts > 1 ? parts * R : 0, Fs && parts_sh > 1 ? parts_sh * Ts : 0) * d * 4;
   sz[G_ROW_W] = tc ? R * 4 : 0;
   sz[G_ROW_DOT] = tc ? R * 4 : 0;
   sz[G_DOT_PART] = tc ? R * (size_t)ceil_div(c.d_ff, 32) * 4 : 0;

@@ -210,6 +210,7 @@ FFN = [  # d, F, rows per expert
     (512, 192, [257]), (192, 640, [1, 2, 3, 4, 5, 6, 7, 8]), (64, 64, [0, 0]), (1024, 128, [31, 33]),
     (320, 576, [700, 255, 256, 511]), (64, 192, [i % 5 for i in range(100)]), (576, 64, [0, 0, 90, 0]),
     (64, 1088, [2, 0, 1]), (128, 832, [9, 30, 1]), (64, 2048, [70, 100]),
+    (64, 7104, [1, 1]), (2112, 64, [1, 0, 2]),
 ]
 ACTS = [synth.ACT_RELU, synth.ACT_GELU, synth.ACT_SWIGLU]
 
