@@ -36,7 +36,8 @@ __device__ __forceinline__ void split_terms(float v, __nv_bfloat16 (&t)[kSplit])
 
 // LPT lanes per token, eight consecutive experts each: a warp works on 32 / LPT tokens at
 // once, reductions over the experts take log2(LPT) exchanges, and rows move in 16-byte
-// pieces. Every lane goes through the token's slots by itself. With TC dz also goes out as
+// pieces (a warp per token took 17 us on 16384 tokens of 128 experts, this 13, bound by its
+// instructions). Every lane goes through the token's slots by itself. With TC dz also goes out as
 // bf16 terms, and the first block writes the tables of the tensor-core products.
 constexpr int kDzThreads = 128, kEpl = 8;
 
@@ -251,7 +252,9 @@ __global__ void __launch_bounds__(kDzThreads, 8) k_dlogits(RouteBwdArgs a, float
 
 // Few experts (EP >= E, see few_experts()): both products on CUDA cores in one pass over
 // x. A thread owns VC columns and keeps their EP rows of W and of dW in registers; the
-// block walks over its piece of the tokens with dz broadcast from shared memory.
+// block walks over its piece of the tokens with dz broadcast from shared memory: 100 MB in
+// 25 us on 4096 tokens of 4096, bound by latency (four blocks an SM of 55 tokens each; two,
+// three, eight and twelve were slower).
 constexpr int kProjThreads = 128, kProjTokens = 128, kProjCols = 4;
 
 // VC values of type T as they lie in memory, and unpacked
@@ -369,8 +372,8 @@ __global__ void __launch_bounds__(kProjThreads) k_route_proj(const T *x, const T
 
 // dw [E, d] = the sum of the `parts` partials (each `rows` x d, its first E rows), and (the
 // last blocks) db[e] = the sum of the blocks' partials. Eight (32) groups of threads take
-// every eighth (32nd) partial, so that few loads follow one another; the groups are added
-// in order.
+// every eighth (32nd) partial, so that few loads follow one another (one thread for all of
+// them: 14 us for 74 partials, this 4); the groups are added in order.
 template <typename T>
 __global__ void __launch_bounds__(256) k_route_sums(const float *part, int parts, int rows, int d,
                                                     T *dw, int dw_blocks, const float *db_part,
