@@ -441,7 +441,7 @@ cudaError_t ffn_bwd_f32(const FfnGradArgs &a, cudaStream_t st) {
   q.dots = nt;
   Products p{};
   p.dx_n = ceil_div(a.d, BN);
-  p.splits = a.dx ? dx_splits(a.m_tiles_ub, a.d, a.F, glu) : 1;
+  p.splits = a.dx ? dx_splits(a.rows, a.m_tiles_ub, a.d, a.F, glu) : 1;
   p.piece = ceil_div(ceil_div(a.F, p.splits), 32) * 32;
   p.splits = ceil_div(a.F, p.piece);
   p.dx = a.dx ? p.dx_n * a.m_tiles_ub * p.splits : 0;

@@ -144,13 +144,17 @@ inline int grad_tile_rows(long long rows, int G) {
 // Pieces of F that dx's tiles on CUDA cores are split into: two blocks an SM, with a
 // reduction of at least 256 each; and at most 1024 products in one running sum (two for
 // each index with SwiGLU), whose fp32 error grows with the root of their number (2.3e-6 of
-// the result after 13008 of them, where sums of 1024 keep it near 5e-7).
-inline int dx_splits(int m_tiles, int d, int F, bool glu) {
+// the result after 13008 of them, where sums of 1024 keep it near 5e-7) while the parts take
+// no more than 256 MB.
+inline int dx_splits(long long rows, int m_tiles, int d, int F, bool glu) {
   const long long tiles = (long long)m_tiles * ceil_div(d, 64);
   const int most = F / 256 > 1 ? F / 256 : 1;
   const long long fill = tiles > 0 ? (296 + tiles - 1) / tiles : 1;
-  const int s = fill < most ? (int)fill : most, exact = ceil_div(F, glu ? 512 : 1024);
-  return s > exact ? s : exact;
+  const int s = fill < most ? (int)fill : most;
+  const long long fit = (256ll << 20) / (4 * (rows > 0 ? rows : 1) * d);
+  const long long exact = ceil_div(F, glu ? 512 : 1024);
+  const long long more = exact < fit ? exact : fit;
+  return s > more ? s : (int)more;
 }
 // ... and its CTA-pair tiles (bf16): where they leave half of the pairs without one, into as
 // many as fill them, of sixteen 64-wide slices at least. (Two rows of two experts of 64 x

@@ -62,8 +62,8 @@ Layout layout_for(const moe_cfg_t &c) {
   const int pt_sh = ceil_div(c.n_tokens, 2 * kRowTile);
   size_t parts, parts_sh;  // of dx: the routed experts', the shared experts'
   if (c.dtype == MOE_DTYPE_F32) {
-    parts = (size_t)dx_splits(tiles, c.d_model, c.d_ff, glu);
-    parts_sh = (size_t)dx_splits(ceil_div(c.n_tokens, us), c.d_model, (int)Fs, true);
+    parts = (size_t)dx_splits((long long)R, tiles, c.d_model, c.d_ff, glu);
+    parts_sh = (size_t)dx_splits(c.n_tokens, ceil_div(c.n_tokens, us), c.d_model, (int)Fs, true);
   } else {
     parts = (size_t)dx_splits_tc(pt, c.d_model, c.d_ff, glu);
     parts_sh = (size_t)dx_splits_tc(pt_sh, c.d_model, (int)Fs, true);

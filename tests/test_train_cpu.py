@@ -170,6 +170,10 @@ def test_backward_workspace_follows_the_layer(lib):
     n = ctypes.c_size_t(0)
     assert lib.moe_backward_workspace_size(None, ctypes.byref(n)) == 1
     assert lib.moe_backward_workspace_size(ctypes.byref(B.make_cfg(small)), None) == 1
+    # rows of h, da, du, x, dy and dx, and no more than 256 MB for the parts of dx
+    wide = B.make_cfg(synth.SMALL["fp32_swiglu"], n_tokens=30000, d_model=1024, d_ff=8192)
+    R = 30000 * wide.top_k
+    assert _bytes(wide) < 4 * R * (3 * 8192 + 4 * 1024 + 8192 // 32 + 8) + (300 << 20)
     # the forward's own workspace did not grow for it
     R, F, d, T = small.T * 2, small.d_ff, small.d_model, small.T
     assert B.workspace_size(B.make_cfg(small)) < 2 * R * (F + 2 * d) + 40 * T * 64 + 65536
