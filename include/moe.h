@@ -1,5 +1,6 @@
 /*
- * moe.h — C ABI of the B200 (sm_100a) sparse Mixture-of-Experts FFN forward.
+ * moe.h — C ABI of the B200 (sm_100a) sparse Mixture-of-Experts FFN layer: the forward
+ * pass, and (further down) the training step.
  *
  * The layer computes, for every token x_t (pages cited by title and listing):
  *
@@ -31,7 +32,9 @@
  *   their first weight slices. The tables are complete by then: they come from an
  *   earlier kernel of the same call that the kernel ahead waited for, or (the
  *   tile table of moe_expert_ffn) from the kernel ahead itself, which does not let
- *   its successor begin before it has completed.
+ *   its successor begin before it has completed. In the same way the router's
+ *   gradient reads x and w_router before its wait: what wrote them had completed
+ *   before the kernel ahead, of the same call, passed its own.
  * - Layout: row-major. Weights use the nn.Linear [out_features, in_features]
  *   layout, stacked over experts. Activations, weights, x_perm, y_perm and y are
  *   stored in cfg->dtype (fp32 or bf16); biases, logits, gates are fp32; index
@@ -46,7 +49,7 @@
  *   moe_last_device_error(). A kernel that detects one skips the offending
  *   access instead of faulting.
  * - Workspace: one buffer of moe_workspace_size() bytes serves every entry point
- *   of a configuration. Zero it once with moe_workspace_init() before first use.
+ *   of a configuration (the gradients have one of their own). Zero it once with moe_workspace_init() before first use.
  *   Calls that share a workspace must not overlap on the GPU.
  */
 #ifndef MOE_H_
