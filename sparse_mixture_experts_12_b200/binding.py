@@ -303,6 +303,7 @@ class MoELayer:
         self.ws = new_workspace(self.cfg, self.device)
         self.lib = load()
         self._bws = None
+        self._index, self._dtype = self.ws.get_device(), workload.torch_dtype
 
     # -------------------------------------------------------------- whole layer
     def forward(self, x: torch.Tensor, y: Optional[torch.Tensor] = None,
@@ -481,16 +482,16 @@ class MoELayer:
     def _call(self, name: str, *args):
         """lib.name(cfg, *args, workspace, its size, stream) on this layer's device, on
         that device's current stream."""
-        bws = self.bws
-        st = _on_device(bws.get_device(), getattr(self.lib, name), ctypes.byref(self.cfg), *args,
+        bws = self._bws if self._bws is not None else self.bws
+        st = _on_device(self._index, getattr(self.lib, name), ctypes.byref(self.cfg), *args,
                         bws.data_ptr(), bws.numel())
         if st:
             _check(st, name)
 
     def _want(self, t, shape, name, dtype=None, optional=False):
-        dtype = dtype or self.w.torch_dtype
+        dtype = dtype or self._dtype
         if (t is None or t.shape != shape or t.dtype is not dtype or not t.is_contiguous()
-                or t.get_device() != self.ws.get_device()):
+                or t.get_device() != self._index):
             check_tensor(t, shape, dtype, name, self.ws.device, optional)
 
     def grad_shapes(self) -> dict:
