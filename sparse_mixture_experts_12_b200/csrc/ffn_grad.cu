@@ -137,9 +137,12 @@ __global__ void __launch_bounds__(kThreads) k_reduce(FfnGradArgs s, Reduce q) {
 
 // --------------------------------------------------------------- fp32, CUDA cores
 // Step 1: one BM-row x 64-column tile of h, da (and du) from the three products, all with
-// reduction length d; blocks behind the tiles add up db2's columns.
+// reduction length d; blocks behind the tiles add up db2's columns. Two blocks an SM hold
+// the MLP's 128-row tiles (16 experts of 416 x 6540 on 1,961 rows: the pass 1.89 -> 1.67 ms);
+// SwiGLU's three sums do not fit so (3.08 ms where one block takes 2.71).
 template <class T, bool GLU, bool VEC>
-__global__ void __launch_bounds__(kThreads) k_dact(FfnGradArgs s, int tiles_n, int tiles) {
+__global__ void __launch_bounds__(kThreads, !GLU && T::BM == 128 ? 2 : 0)
+    k_dact(FfnGradArgs s, int tiles_n, int tiles) {
   constexpr int BM = T::BM, BK = T::BK, TM = T::TM, TN = T::TN;
   struct Smem {
     alignas(16) float x[BK][T::LDA], y[BK][T::LDA];
@@ -285,7 +288,8 @@ struct Products {
   int M[3], N[3], tiles[3];
 };
 template <class TD, class TW, bool VEC>
-__global__ void __launch_bounds__(kThreads) k_products(FfnGradArgs s, Products p, Reduce q) {
+__global__ void __launch_bounds__(kThreads, TW::BN == 128 ? 2 : 0)
+    k_products(FfnGradArgs s, Products p, Reduce q) {
   __shared__ union Smem {
     GemmSmem<TD> d;
     GemmSmem<TW> w;
@@ -294,12 +298,12 @@ __global__ void __launch_bounds__(kThreads) k_products(FfnGradArgs s, Products p
   pdl_trigger();
   int x = blockIdx.x;
   if (x < p.dx) {
-    const int split = x % p.splits, n0 = x / p.splits % p.dx_n * BN;
+    const int split = x % p.splits, n0 = x / p.splits % p.dx_n * TD::BN;
     const int tile_m = x / (p.splits * p.dx_n);
     const int g = group_of_tile(s.mprefix, s.G, tile_m);
     if (g < 0) return;
     const int row0 = s.offsets[g] + (tile_m - s.mprefix[g]) * TD::BM;
-    const int rows = min(TD::BM, s.offsets[g + 1] - row0), cols = min(BN, s.d - n0);
+    const int rows = min(TD::BM, s.offsets[g + 1] - row0), cols = min(TD::BN, s.d - n0);
     const int k0 = split * p.piece, K = min(p.piece, s.F - k0);
     const size_t ao = (size_t)row0 * s.F + k0, wo = ((size_t)g * s.F + k0) * s.d + n0;
     float acc[TD::TM][TD::TN];
@@ -322,15 +326,15 @@ __global__ void __launch_bounds__(kThreads) k_products(FfnGradArgs s, Products p
       ++j;
     }
     const int g = x / p.tiles[j], t = x % p.tiles[j];
-    const int M = p.M[j], N = p.N[j], nt = ceil_div(N, BN);
-    const int m0 = t / nt * TW::BM, n0 = t % nt * BN;
+    const int M = p.M[j], N = p.N[j], nt = ceil_div(N, TW::BN);
+    const int m0 = t / nt * TW::BM, n0 = t % nt * TW::BN;
     const size_t row0 = (size_t)s.offsets[g];
     float acc[TW::TM][TW::TN];
     clear(acc);
     mma_tile<TW, true, VEC>(sm.w, acc, p.a[j] + row0 * M + m0, M, M - m0, p.b[j] + row0 * N + n0, N,
                             N - n0, s.offsets[g + 1] - s.offsets[g]);
     store_tile<TW, VEC>(acc, p.c[j] + ((size_t)g * M + m0) * N + n0, N, min(TW::BM, M - m0),
-                        min(BN, N - n0));
+                        min(TW::BN, N - n0));
     return;
   }
   reduce<float>(s, q, x - p.dw);
@@ -432,15 +436,15 @@ cudaError_t ffn_bwd_f32(const FfnGradArgs &a, cudaStream_t st) {
   const int nt = ceil_div(a.F, BN), tiles = nt * a.m_tiles_ub;
   const int sums = a.db2 ? ceil_div(a.d, 64) * a.m_tiles_ub : 0;
   cudaError_t e =
-      glu ? launch_pdl(k_dact<TD, true, VEC>, dim3(tiles + sums), b, 0, st, a, nt, tiles)
-          : launch_pdl(k_dact<TD, false, VEC>, dim3(tiles + sums), b, 0, st, a, nt, tiles);
+      glu ? launch_pdl(k_dact<Tile<TD::BM>, true, VEC>, dim3(tiles + sums), b, 0, st, a, nt, tiles)
+          : launch_pdl(k_dact<Tile<TD::BM>, false, VEC>, dim3(tiles + sums), b, 0, st, a, nt, tiles);
   if (e != cudaSuccess) return e;
   Reduce q = reduce_blocks(a);
   q.first = a.mprefix;
   q.unit = 1;
   q.dots = nt;
   Products p{};
-  p.dx_n = ceil_div(a.d, BN);
+  p.dx_n = ceil_div(a.d, TD::BN);
   p.splits = a.dx ? dx_splits(a.rows, a.m_tiles_ub, a.d, a.F, glu) : 1;
   p.piece = ceil_div(ceil_div(a.F, p.splits), 32) * 32;
   p.splits = ceil_div(a.F, p.piece);
@@ -453,7 +457,7 @@ cudaError_t ffn_bwd_f32(const FfnGradArgs &a, cudaStream_t st) {
     p.c[j] = static_cast<float *>(c);
     p.M[j] = M;
     p.N[j] = N;
-    p.tiles[j] = ceil_div(M, TW::BM) * ceil_div(N, BN);
+    p.tiles[j] = ceil_div(M, TW::BM) * ceil_div(N, TW::BN);
     p.dw += a.G * p.tiles[j];
   };
   job(a.dg, a.x, a.dw1, a.F, a.d);
@@ -467,11 +471,18 @@ cudaError_t ffn_bwd_f32(const FfnGradArgs &a, cudaStream_t st) {
                     b, 0, st, a, p.splits);
 }
 
-// the weights' gradients take 128-row tiles unless those leave SMs without one
+// The weights' gradients take 128-row tiles unless those leave SMs without one. With 128
+// rows, they and dx take 128 columns where those give every SM its two blocks: 2.88 -> 2.69
+// ms with 448 tiles of dW1, but 313 -> 331 us with 180.
 template <class TD, bool VEC>
 cudaError_t ffn_bwd_f32(const FfnGradArgs &a, cudaStream_t st) {
-  const long long big = (long long)a.G * ceil_div(a.F, 128) * ceil_div(a.d, BN);
-  return big >= 148 ? ffn_bwd_f32<TD, Tile<128>, VEC>(a, st) : ffn_bwd_f32<TD, Tile<32>, VEC>(a, st);
+  const long long m = (long long)a.G * ceil_div(a.F, 128);
+  if constexpr (TD::BM == 128) {
+    if (m * ceil_div(a.d, 128) >= 2 * 148)
+      return ffn_bwd_f32<Tile<128, 128>, Tile<128, 128>, VEC>(a, st);
+  }
+  return m * ceil_div(a.d, BN) >= 148 ? ffn_bwd_f32<TD, Tile<128>, VEC>(a, st)
+                                      : ffn_bwd_f32<TD, Tile<32>, VEC>(a, st);
 }
 template <class TD>
 cudaError_t ffn_bwd_f32(const FfnGradArgs &a, cudaStream_t st) {

@@ -1,10 +1,12 @@
-// fp32 tiles on CUDA cores (FFMA) shared by the gradients: 256 threads compute a
-// BM x 64 tile of C = A B with B row-major [K, N], A row-major [M, K] or (AT) [K, M], from
-// K slices in shared memory while the next slice is fetched into registers.
+// fp32 tiles on CUDA cores (FFMA) shared by the gradients: 256 threads compute a BM x BN
+// tile of C = A B with B row-major [K, N], A row-major [M, K] or (AT) [K, M], from K slices
+// in shared memory while the next slice is fetched into registers.
 //
-// BM 128 (8 x 4 values a thread, 16-wide slices) is for experts with many rows, BM 32 (2 x
-// 4, 32-wide) and BM 8 (1 x 2) for few: on 16 rows a 128-row tile took 22 us where the
-// 32-row one takes 8, and on a handful the 32-row one computes more than it loads.
+// BM 128 (8 x 4 values a thread, 16-wide slices; 8 x 8 where BN is 128, two thirds of the
+// reads of shared memory per product) is for experts with many rows, BM 32 (2 x 4, 32-wide)
+// and BM 8 (1 x 2) for few: on 16 rows a 128-row tile took 22 us where the 32-row one takes
+// 8, and on a handful the 32-row one computes more than it loads. Products are issued in
+// pairs, which leaves issue slots for the reads: 7 to 13 % of the expert gradients' time.
 #pragma once
 
 #include "kernels.cuh"
@@ -12,13 +14,15 @@
 namespace moe {
 namespace simt {
 
-constexpr int BN = 64, kThreads = 256;
-template <int BM_>
+constexpr int BN = 64, kThreads = 256;  // BN: columns of a tile but the widest
+template <int BM_, int BN_ = 64>
 struct Tile {
-  static constexpr int BM = BM_, BK = BM == 128 ? 16 : 32;
-  static constexpr int TN = BM == 8 ? 2 : 4, TX = BN / TN;  // columns a thread, threads across
-  static constexpr int TY = kThreads / TX, TM = BM / TY;    // threads down, rows a thread
+  static constexpr int BM = BM_, BN = BN_, BK = BM == 128 ? 16 : 32;
+  static constexpr int TN = BN == 128 ? 8 : (BM == 8 ? 2 : 4);  // columns a thread
+  static constexpr int TX = BN / TN, TY = kThreads / TX, TM = BM / TY;
   static constexpr int LDA = BM + (BM == 32 ? 2 : 4), LDB = BN + 4;
+  // thread tx has columns TC tx .. TC tx + TC - 1, and with TN = 8 those 64 further on
+  static constexpr int TC = TN == 8 ? 4 : TN;
 };
 
 // the expert of row tile mt (mprefix [G+1]), or -1 past the last tile
@@ -108,14 +112,40 @@ __device__ __forceinline__ void values(const float *p, float (&v)[N]) {
     v[0] = *p;
   }
 }
+// c += a b for two values at once: one instruction, each rounded as an fmaf
+__device__ __forceinline__ void fma2(float &c0, float &c1, float a0, float a1, float b0, float b1) {
+  asm("{\n\t.reg .b64 a, b, c;\n\t"
+      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%0, %1};\n\t"
+      "fma.rn.f32x2 c, a, b, c;\n\tmov.b64 {%0, %1}, c;\n\t}"
+      : "+f"(c0), "+f"(c1)
+      : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
+}
 template <int TM, int TN>
 __device__ __forceinline__ void outer(float (&acc)[TM][TN], const float (&a)[TM], const float *b) {
   float q[TN];
-  values(b, q);
+  if constexpr (TN == 8) {
+    float lo[4], hi[4];
+    values(b, lo);
+    values(b + 64, hi);
 #pragma unroll
-  for (int i = 0; i < TM; ++i)
+    for (int j = 0; j < 4; ++j) {
+      q[j] = lo[j];
+      q[4 + j] = hi[j];
+    }
+  } else {
+    values(b, q);
+  }
+  if constexpr (TM >= 4) {
 #pragma unroll
-    for (int j = 0; j < TN; ++j) acc[i][j] = fmaf(a[i], q[j], acc[i][j]);
+    for (int i = 0; i < TM; i += 2)
+#pragma unroll
+      for (int j = 0; j < TN; ++j) fma2(acc[i][j], acc[i + 1][j], a[i], a[i + 1], q[j], q[j]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+      for (int j = 0; j < TN; j += 2) fma2(acc[i][j], acc[i][j + 1], a[i], a[i], q[j], q[j + 1]);
+  }
 }
 template <int TM, int TN>
 __device__ __forceinline__ void clear(float (&acc)[TM][TN]) {
@@ -151,7 +181,7 @@ __device__ __forceinline__ void mma_tile(GemmSmem<T> &s, float (&acc)[T::TM][T::
                                          int K) {
   const int tx = threadIdx.x % T::TX, ty = threadIdx.x / T::TX;
   Slice<T::BM, T::BK, T::LDA, !AT, VEC> sa;
-  Slice<BN, T::BK, T::LDB, false, VEC> sb;
+  Slice<T::BN, T::BK, T::LDB, false, VEC> sb;
   sa.fetch(a, lda, rows, 0, K);
   sb.fetch(b, ldb, cols, 0, K);
   for (int k0 = 0; k0 < K; k0 += T::BK) {
@@ -167,7 +197,7 @@ __device__ __forceinline__ void mma_tile(GemmSmem<T> &s, float (&acc)[T::TM][T::
     for (int k = 0; k < T::BK; ++k) {
       float av[T::TM];
       values(&s.a[k][ty * T::TM], av);
-      outer(acc, av, &s.b[k][tx * T::TN]);
+      outer(acc, av, &s.b[k][tx * T::TC]);
     }
   }
 }
@@ -176,24 +206,28 @@ __device__ __forceinline__ void mma_tile(GemmSmem<T> &s, float (&acc)[T::TM][T::
 template <class T, bool VEC>
 __device__ __forceinline__ void store_tile(const float (&acc)[T::TM][T::TN], float *c, size_t ldc,
                                            int rows, int cols) {
-  constexpr int TN = T::TN;
+  constexpr int TC = T::TC;
   const int tx = threadIdx.x % T::TX, ty = threadIdx.x / T::TX;
 #pragma unroll
   for (int i = 0; i < T::TM; ++i) {
     const int m = ty * T::TM + i;
     if (m >= rows) continue;
-    float *p = c + (size_t)m * ldc + tx * TN;
-    const int n = cols - tx * TN;
-    if constexpr (VEC) {
-      if (n <= 0) continue;
-      if constexpr (TN == 4)
-        *reinterpret_cast<float4 *>(p) = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
-      else
-        *reinterpret_cast<float2 *>(p) = make_float2(acc[i][0], acc[i][1]);
-    } else {
 #pragma unroll
-      for (int j = 0; j < TN; ++j)
-        if (j < n) p[j] = acc[i][j];
+    for (int g = 0; g < T::TN / TC; ++g) {
+      const int n0 = 64 * g + tx * TC, n = cols - n0;
+      float *p = c + (size_t)m * ldc + n0;
+      const float *v = &acc[i][g * TC];
+      if constexpr (VEC) {
+        if (n <= 0) continue;
+        if constexpr (TC == 4)
+          *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
+        else
+          *reinterpret_cast<float2 *>(p) = make_float2(v[0], v[1]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < TC; ++j)
+          if (j < n) p[j] = v[j];
+      }
     }
   }
 }
