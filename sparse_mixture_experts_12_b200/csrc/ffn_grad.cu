@@ -472,7 +472,7 @@ cudaError_t ffn_bwd_f32(const FfnGradArgs &a, cudaStream_t st) {
 }
 
 // The weights' gradients take 128-row tiles unless those leave SMs without one. With 128
-// rows, they and dx take 128 columns where those give every SM its two blocks: 2.88 -> 2.69
+// rows, they and dx take 128 columns where those give every SM its two blocks: 2.86 -> 2.69
 // ms with 448 tiles of dW1, but 313 -> 331 us with 180.
 template <class TD, bool VEC>
 cudaError_t ffn_bwd_f32(const FfnGradArgs &a, cudaStream_t st) {
