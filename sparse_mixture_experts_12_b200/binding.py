@@ -647,6 +647,11 @@ class AdamW:
     ``exp_avg_sq``, with 8 bits ``exp_avg_scale`` and ``exp_avg_sq_scale``, and optionally
     ``master`` (None where a parameter has none), used as they are; `state_dict` gives one.
     With 8 bits exp_avg_sq holds the root of the second moment.
+
+    The step works on the storage that the parameters and the state had at first. A step
+    after a parameter got another one (``p.data = ...``, ``p.set_()``) raises ValueError: make
+    a new optimizer from `state_dict`. The state's tensors are for reading and for updates
+    in place.
     """
 
     def __init__(self, params, lr: float = 1e-3, betas=(0.9, 0.999), eps: float = 1e-8,
@@ -666,22 +671,23 @@ class AdamW:
             self.bits, self.t = state_bits, 0
             dt = torch.float32 if state_bits == 32 else torch.float8_e4m3fn
             new = lambda p: torch.zeros(p.shape, dtype=dt, device=p.device)  # noqa: E731
-            self.exp_avg = [new(p) for p in self.params]
-            self.exp_avg_sq = [new(p) for p in self.params]
+            self.exp_avg = tuple(new(p) for p in self.params)
+            self.exp_avg_sq = tuple(new(p) for p in self.params)
             self.exp_avg_scale = self.exp_avg_sq_scale = None
             if state_bits == 8:
                 scale = lambda p: torch.zeros(-(-p.numel() // ADAMW_BLOCK), device=p.device)  # noqa: E731
-                self.exp_avg_scale = [scale(p) for p in self.params]
-                self.exp_avg_sq_scale = [scale(p) for p in self.params]
-            self.master = [p.float() if master and p.dtype == torch.bfloat16 else None
-                           for p in self.params]
+                self.exp_avg_scale = tuple(scale(p) for p in self.params)
+                self.exp_avg_sq_scale = tuple(scale(p) for p in self.params)
+            self.master = tuple(p.float() if master and p.dtype == torch.bfloat16 else None
+                                for p in self.params)
         else:
             self.t = int(state["step"])
-            self.exp_avg, self.exp_avg_sq = list(state["exp_avg"]), list(state["exp_avg_sq"])
-            self.exp_avg_scale = state.get("exp_avg_scale")
-            self.exp_avg_sq_scale = state.get("exp_avg_sq_scale")
+            self.exp_avg, self.exp_avg_sq = tuple(state["exp_avg"]), tuple(state["exp_avg_sq"])
+            scales = [state.get(n) for n in ("exp_avg_scale", "exp_avg_sq_scale")]
+            self.exp_avg_scale, self.exp_avg_sq_scale = (None if x is None else tuple(x)
+                                                         for x in scales)
             self.bits = 32 if self.exp_avg_scale is None else 8
-            self.master = list(state.get("master") or [None] * len(self.params))
+            self.master = tuple(state.get("master") or [None] * len(self.params))
         self._lib = load()
         n_params = len(self.params)
         if len({p.data_ptr() for p in self.params if p.numel()}) != sum(1 for p in self.params
@@ -723,6 +729,10 @@ class AdamW:
                                       MoeAdamWTensor.grad_dtype.offset,
                                       (ctypes.sizeof(MoeAdamWTensor),))
         self._grad_dtypes = None  # the types that _grad_types holds
+        # what the addresses above point to: the parameters' are compared at every step, the
+        # state's memory is kept by aliases of our own, whatever is done to its tensors
+        self._addresses = [p.data_ptr() for p in self.params]
+        self._held = [x.detach() for xs in lists for x in xs if x is not None]
         self._shapes = [p.shape for p in self.params]
         self._devices = [p.get_device() for p in self.params]
         self._index = self.params[0].get_device()
@@ -745,9 +755,14 @@ class AdamW:
         if len(grads) != len(self.params):
             raise ValueError(f"{len(grads)} gradients for {len(self.params)} parameters")
         # list by list: a hundred tensors are checked in the time of a launch or two
+        data_ptr = torch.Tensor.data_ptr
+        if list(map(data_ptr, self.params)) != self._addresses:
+            moved = [i for i, p in enumerate(self.params) if p.data_ptr() != self._addresses[i]]
+            raise ValueError(f"parameter {moved[0]} has another storage than when the optimizer "
+                             "was made")
         if ([g.shape for g in grads] != self._shapes
-                or [g.get_device() for g in grads] != self._devices
-                or not all([g.is_contiguous() for g in grads])):
+                or list(map(torch.Tensor.get_device, grads)) != self._devices
+                or not all(map(torch.Tensor.is_contiguous, grads))):
             for i, (g, p) in enumerate(zip(grads, self.params)):  # which one
                 check_tensor(g, p.shape, g.dtype, f"gradient {i}", self.device)
         dtypes = [g.dtype for g in grads]
@@ -758,7 +773,7 @@ class AdamW:
                                  "supported")
             self._grad_types[:] = [_ADAMW_DTYPES[dt] for dt in dtypes]
             self._grad_dtypes = dtypes
-        self._grad_ptrs[:] = [g.data_ptr() for g in grads]
+        self._grad_ptrs[:] = list(map(data_ptr, grads))
         o = MoeAdamW(self.betas[0], self.betas[1], self.lr, self.eps, self.weight_decay, self.t + 1)
         for name, t, dt in (("grad_scale", grad_scale, torch.float32),
                             ("found_inf", found_inf, torch.float32),
@@ -775,9 +790,9 @@ class AdamW:
         self.t += 1
 
     def state_dict(self) -> dict:
-        return {"step": self.t, "exp_avg": self.exp_avg, "exp_avg_sq": self.exp_avg_sq,
-                "exp_avg_scale": self.exp_avg_scale, "exp_avg_sq_scale": self.exp_avg_sq_scale,
-                "master": self.master}
+        lists = {n: getattr(self, n) for n in ("exp_avg", "exp_avg_sq", "exp_avg_scale",
+                                               "exp_avg_sq_scale", "master")}
+        return {"step": self.t, **{n: None if x is None else list(x) for n, x in lists.items()}}
 
 
 def shared_as_experts(layer: MoELayer):
