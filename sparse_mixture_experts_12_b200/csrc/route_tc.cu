@@ -402,10 +402,6 @@ k_router_tc(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUt
   const int nkb = ceil_div(a.d, kBlockK);
   const int kb0 = rank * nkb / S, kb1 = (rank + 1) * nkb / S;  // this CTA's K share
 
-  for (int e = tid; e < kMaxExperts; e += kRtThreads) {
-    ctl->br[e] = (a.b_router && e < E) ? a.b_router[e] : 0.f;
-    ctl->lb[e] = (a.logit_bias && e < E) ? a.logit_bias[e] : 0.f;
-  }
   for (int i = tid; i < kRtMaxSubs * kMaxExperts; i += kRtThreads) (&ctl->cnt[0][0])[i] = 0;
   if (tid == 0) {
     for (int s = 0; s < C::kStages; ++s) {
@@ -426,8 +422,8 @@ k_router_tc(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUt
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = ctl->tmem_base;
-  // the set-up above overlaps the previous kernel; x, the weights and every output
-  // are touched only after it has completed
+  // the set-up above overlaps the previous kernel; x, the weights, the biases and every
+  // output are touched only after it has completed
   pdl_wait();
   pdl_trigger();
 
@@ -485,6 +481,12 @@ k_router_tc(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUt
   } else if (warp >= 2) {
     // ------------------------------------------ epilogue, 1: TMEM -> partial tile
     const int et = tid - 64;
+    // the biases, under the MMAs: after the wait, since an optimizer step that writes them
+    // may stand directly ahead (the sync below shows them to the whole CTA)
+    for (int e = et; e < kMaxExperts; e += kRtEpiThreads) {
+      ctl->br[e] = (a.b_router && e < E) ? a.b_router[e] : 0.f;
+      ctl->lb[e] = (a.logit_bias && e < E) ? a.logit_bias[e] : 0.f;
+    }
     // one thread waits; the named barrier is reached by all epilogue threads
     if (et == 0) ctl->epi_ok = rt_wait(&ctl->tfull, 0, ctl, a.err, 13) ? 1 : 0;
     rt_epi_sync();

@@ -6,8 +6,9 @@ import torch
 
 from sparse_mixture_experts_12_b200 import binding as B
 from sparse_mixture_experts_12_b200 import build as BUILD
+from sparse_mixture_experts_12_b200 import synth
 from tests import train_ref as R
-from tests.test_gpu_train import DEV, _adam_case
+from tests.test_gpu_train import DEV, _adam_case, _forward
 
 pytestmark = pytest.mark.gpu
 
@@ -61,3 +62,49 @@ def test_adamw_state_cannot_be_pulled_from_under_it(bits):
     opt.step(gs)
     ref.step(gs)
     assert (other == 7).all() and all(torch.equal(p, q) for p, q in zip(ps, qs))
+
+
+# ------------------------------------------------------------- the step as a whole
+def _steps(wl, how, n=4):
+    """n training steps on one input; the router's biases are trained too. "apart": the GPU is
+    waited for after every call; "together": nothing lies between one call and the next;
+    "graph": so, captured and replayed once. Returns what the last step left."""
+    wl = wl.replace(router_bias=True, logit_bias_std=0.5, bias_std=0.1)
+    layer, x, taps, dy = _forward(wl, 17)
+    names = [m for m in layer.grad_shapes() if layer.p.get(m) is not None] + ["logit_bias"]
+    opt = B.AdamW([layer.p[m] for m in names], lr=0.05, betas=(0.8, 0.9))
+    gr, dx, y = layer.new_grads(), torch.empty_like(x), torch.empty_like(x)
+    grads = [gr["b_router" if m == "logit_bias" else m] for m in names]
+    layer.bws
+    torch.cuda.synchronize()
+
+    def run():
+        for _ in range(n):
+            for call in (lambda: layer.forward(x, y, taps=taps),
+                         lambda: layer.backward(x, dy, taps, dx=dx, grads=gr),
+                         lambda: opt.step(grads)):
+                call()
+                if how == "apart":
+                    torch.cuda.synchronize()
+
+    if how == "graph":
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            run()
+        graph.replay()
+    else:
+        run()
+    torch.cuda.synchronize()
+    assert layer.last_backward_error() == (0, 0) and layer.last_device_error() == (0, 0)
+    return [y, dx, taps["logits"], *grads, *(layer.p[m] for m in names)]
+
+
+@pytest.mark.parametrize("how", ["together", "graph"])
+@pytest.mark.parametrize("name", ["router_e20", "router_e256", "switch_small", "decode_e32", "tiny",
+                                  "fp32_gelu_cap", "deepseek_small"])
+def test_steps_with_nothing_between_them(name, how):
+    """An optimizer step directly ahead of the next forward pass: its kernels see the weights
+    and the biases that the step wrote."""
+    wl = synth.SMALL[name]
+    for a, b in zip(_steps(wl, "apart"), _steps(wl, how)):
+        assert torch.equal(a, b)

@@ -3,6 +3,7 @@ differentiation and against differences of the oracle's forward pass, the refusa
 the C entry points, struct layouts, and the binding's checks."""
 import ctypes
 import os
+import re
 import subprocess
 
 import numpy as np
@@ -314,3 +315,27 @@ def test_binding_checks_tensors():
         B.AdamW([])
     with pytest.raises(ValueError):
         B.AdamW([x])
+
+
+def _kernels_launched_ahead():
+    """(name, body before the first wait) of every kernel that calls pdl_wait()."""
+    csrc = os.path.join(ROOT, "sparse_mixture_experts_12_b200", "csrc")
+    for name in sorted(os.listdir(csrc)):
+        with open(os.path.join(csrc, name)) as f:
+            text = re.sub(r"//[^\n]*", "", f.read())
+        for m in re.finditer(r"__global__.*?\bvoid\b.*?(k_\w+)\(", text, re.S):
+            end = text.find("\n}\n", m.end())
+            body = text[m.end():end]
+            if "pdl_wait()" in body:
+                yield f"{name}:{m.group(1)}", body[:body.index("pdl_wait()")]
+
+
+def test_no_kernel_reads_a_bias_before_its_wait():
+    """An optimizer step writes the biases and may stand directly ahead of a forward pass:
+    their loads come after the wait for the kernel ahead. (The expert GEMMs read their
+    weights before it, from behind a kernel of the same call that has waited.)"""
+    seen = dict(_kernels_launched_ahead())
+    assert len(seen) > 20 and "route_tc.cu:k_router_tc" in seen
+    early = [k for k, body in seen.items()
+             if re.search(r"\b(b_router|logit_bias|b1|b2|bias)\s*\[", body)]
+    assert early == []
