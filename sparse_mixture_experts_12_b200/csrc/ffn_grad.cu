@@ -63,11 +63,13 @@ __device__ __forceinline__ void col_sums(const FfnGradArgs &s, int unit, int x, 
     s.part2[(size_t)y * d + n] = (red[0][c] + red[1][c]) + (red[2][c] + red[3][c]);
   }
 }
+// (one dimension, as for fp32: the row tiles can be more than the 65535 of a grid's y)
 template <typename T>
 __global__ void __launch_bounds__(kThreads) k_col_sums(FfnGradArgs s, int unit) {
   pdl_wait();
   pdl_trigger();
-  col_sums<T>(s, unit, blockIdx.x, blockIdx.y);
+  const int dn = ceil_div(s.d, 64);
+  col_sums<T>(s, unit, blockIdx.x % dn, blockIdx.x / dn);
 }
 
 // What follows from the activations' gradients beside the matrix products, as blocks of
@@ -525,7 +527,7 @@ __global__ void __launch_bounds__(kThreads) k_dx_join(FfnGradArgs s, int splits)
 cudaError_t ffn_bwd_tc(const FfnGradArgs &a, cudaStream_t st) {
   cudaError_t e = cudaSuccess;
   if (a.db2) {
-    e = launch_pdl(k_col_sums<__nv_bfloat16>, dim3(ceil_div(a.d, 64), a.m_tiles_ub), dim3(kThreads),
+    e = launch_pdl(k_col_sums<__nv_bfloat16>, dim3(ceil_div(a.d, 64) * a.m_tiles_ub), dim3(kThreads),
                    0, st, a, a.tile_rows);
     if (e != cudaSuccess) return e;
   }

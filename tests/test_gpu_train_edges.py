@@ -8,7 +8,7 @@ from sparse_mixture_experts_12_b200 import binding as B
 from sparse_mixture_experts_12_b200 import build as BUILD
 from sparse_mixture_experts_12_b200 import synth
 from tests import train_ref as R
-from tests.test_gpu_train import DEV, _adam_case, _forward
+from tests.test_gpu_train import DEV, _adam_case, _forward, _gen, _rand, _workload
 
 pytestmark = pytest.mark.gpu
 
@@ -108,3 +108,31 @@ def test_steps_with_nothing_between_them(name, how):
     wl = synth.SMALL[name]
     for a, b in zip(_steps(wl, "apart"), _steps(wl, how)):
         assert torch.equal(a, b)
+
+
+# ----------------------------------------------------------------------- experts
+def test_output_biases_of_more_row_tiles_than_a_grid_dimension_holds():
+    """bf16 MLP experts on 8.4 M rows: 65625 tiles of 128. dy holds small whole numbers, so
+    that every partial sum of db2 is exact (below 2^24)."""
+    rows, d, F, b = [3, 8_399_990, 7], 64, 64, torch.bfloat16
+    n, E = sum(rows), len(rows)
+    wl = _workload(n, d, E, 1, synth.DT_BF16, F=F, act=synth.ACT_RELU)
+    g = _gen(3)
+    p = {"w1": _rand(g, E, F, d, dt=b, std=1 / 8), "w2": _rand(g, E, d, F, dt=b, std=1 / 8),
+         "b1": _rand(g, E, F, std=0.3), "b2": _rand(g, E, d, std=0.3)}
+    layer = B.MoELayer(wl, p, DEV)
+    x = torch.empty(n, d, dtype=b, device=DEV).normal_(generator=g)
+    dy = torch.randint(-1, 2, (n, d), device=DEV, generator=g, dtype=torch.int8).to(b)
+    off = torch.tensor([0, rows[0], rows[0] + rows[1], n], dtype=torch.int32, device=DEV)
+    gr, dx = {m: layer.new_grads()[m] for m in ("b1", "b2")}, torch.empty_like(x)
+    layer.expert_ffn_backward(x, off, dy, dx, gr)
+    for e in range(E):
+        want = dy[off[e]:off[e + 1]].sum(0, dtype=torch.int64)
+        assert torch.equal(gr["b2"][e].double(), want.double())
+    for e in (0, 2):  # the first and the last rows, by themselves
+        r = slice(int(off[e]), int(off[e + 1]))
+        ref, lim = R.ffn_bwd(x[r], dy[r], [0, rows[e]], {m: v[e:e + 1] for m, v in p.items()},
+                             wl.act, b)
+        R.check(dx[r], ref["dx"], lim["dx"], "dx")
+        R.check(gr["b1"][e], ref["b1"][0], lim["b1"][0], "b1")
+    assert layer.last_backward_error() == (0, 0)
