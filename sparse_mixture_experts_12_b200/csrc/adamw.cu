@@ -25,6 +25,7 @@ constexpr int kThreads = 256;
 constexpr int kVec = 8;                            // elements per lane and step
 constexpr int kQBlock = MOE_ADAMW_BLOCK;           // elements of one 8-bit scale: a warp's step
 constexpr int kChunk = kThreads * kVec;            // elements per CTA
+constexpr long long kMaxCtas = 0x7fffffff;         // of a grid
 static_assert(kQBlock == 32 * kVec, "a warp's step is one scale block");
 constexpr float kE4M3Max = 448.f;
 constexpr float kE4M3Tiny = 0.001953125f;          // 2^-9, the smallest positive code
@@ -323,7 +324,7 @@ moe_status_t check_tensor(const moe_adamw_tensor_t &t) {
       (t.state_bits != 8 && t.state_bits != 32))
     return MOE_ERR_INVALID_ARG;
   if (t.master && t.param_dtype == MOE_DTYPE_F32) return MOE_ERR_INVALID_ARG;
-  if (t.n > (1ll << 42)) return MOE_ERR_UNSUPPORTED;  // the grid holds 2^31 - 1 chunks
+  if (t.n > kMaxCtas * kChunk) return MOE_ERR_UNSUPPORTED;
   if (t.n == 0) return MOE_OK;
   const bool q = t.state_bits == 8;
   if (!q && (t.exp_avg_scale || t.exp_avg_sq_scale)) return MOE_ERR_INVALID_ARG;
@@ -355,7 +356,7 @@ MOE_API moe_status_t moe_adamw_step(const moe_adamw_tensor_t *tensors, int32_t n
     int m = 0;
     while (i + m < n_tensors && m < kMany) {
       const long long c = (tensors[i + m].n + kChunk - 1) / kChunk;
-      if (ctas + c > 0x7fffffffll) break;
+      if (ctas + c > kMaxCtas) break;  // (never at m = 0: check_tensor)
       ctas += c;
       ++m;
     }

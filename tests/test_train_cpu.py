@@ -5,6 +5,7 @@ import ctypes
 import os
 import re
 import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -288,6 +289,20 @@ def _adam(lib, t=None, o=None, n=1):
 ])
 def test_adamw_refuses_before_launching(lib, t, o, expect):
     assert _adam(lib, t, o) == expect
+
+
+@pytest.mark.parametrize("n", [1 << 42, (1 << 42) - 2047, (1 << 62) + 5])
+def test_adamw_refuses_a_tensor_of_more_blocks_than_a_grid_holds(n):
+    """2048 elements a block, 2^31 - 1 blocks: one element more is refused (in a process of its
+    own, which an endless loop on the host would not hold up for good)."""
+    prog = ("import ctypes; from sparse_mixture_experts_12_b200 import binding as B; "
+            f"t = (B.MoeAdamWTensor * 1)(B.MoeAdamWTensor(n={n}, param=4096, grad=4096, "
+            "exp_avg=4096, exp_avg_sq=4096, param_dtype=1, grad_dtype=1, state_bits=32)); "
+            "o = B.MoeAdamW(beta1=0.9, beta2=0.9, step=1); "
+            "print(B.load().moe_adamw_step(t, 1, ctypes.byref(o), None))")
+    r = subprocess.run([sys.executable, "-c", prog], cwd=ROOT, capture_output=True, text=True,
+                       timeout=120)
+    assert r.stdout.strip() == "2", r.stderr
 
 
 def test_adamw_with_nothing_to_do(lib):
