@@ -437,7 +437,8 @@ moe_status_t moe_aux_finalize(const moe_cfg_t *cfg, long long n_tokens_total,
  * same bits. */
 
 /* The parameters' gradients: the shapes of moe_weights_t's members; a NULL member is
- * not computed. b_router is the gradient of logit_bias as well. */
+ * not computed. b_router is the gradient of logit_bias as well: a layer whose only
+ * router bias is logit_bias trains it with this gradient. */
 typedef struct {
   void *w_router;   /* [E, d] dtype */
   float *b_router;  /* [E] */

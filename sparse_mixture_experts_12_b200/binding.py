@@ -508,6 +508,14 @@ class MoELayer:
             has.add("b_router")
         return {n: s for n, s in shapes.items() if n in has}
 
+    def parameters(self) -> dict:
+        """name of the gradient -> this layer's parameter of it, for AdamW. The router's bias
+        (b_router) is logit_bias in a layer that has no other; next to a b_router, logit_bias is
+        left out: the logits take their sum, and trained both it would move twice as far."""
+        bias = self.p.get("b_router")
+        own = dict(self.p, b_router=self.p.get("logit_bias") if bias is None else bias)
+        return {n: own[n] for n in self.grad_shapes() if own.get(n) is not None}
+
     def new_grads(self) -> dict:
         """Buffers for the gradients of this layer's parameters."""
         return {n: torch.empty(s, dtype=dt, device=self.ws.device)

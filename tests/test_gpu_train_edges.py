@@ -110,6 +110,34 @@ def test_steps_with_nothing_between_them(name, how):
         assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("name,biases", [("switch_small", ("logit_bias",)), ("tiny", ("b_router",)),
+                                         ("router_e20", ("b_router", "logit_bias")),
+                                         ("mixtral_small", ())])
+def test_every_parameter_is_trained(name, biases):
+    """The optimizer over layer.parameters() moves all of them, the router's bias among them,
+    under whichever name the layer has it."""
+    layer, x, taps, dy = _forward(synth.SMALL[name], 3)
+    params = layer.parameters()
+    had = {n for n in layer.grad_shapes() if layer.p.get(n) is not None}
+    assert set(params) == had | ({"b_router"} if biases else set())
+    assert all(params[n] is layer.p[n] for n in had)
+    assert tuple(n for n in ("b_router", "logit_bias") if layer.p.get(n) is not None) == biases
+    old = {n: t.clone() for n, t in layer.p.items() if t is not None}
+    _, gr = layer.backward(x, dy, taps)
+    B.AdamW(params, lr=0.01, eps=1e-8, weight_decay=0.0).step(gr)
+    for n, t in params.items():
+        g = gr[n].double()
+        if n == "b_router":
+            # the first step: lr g / (|g| + eps)
+            want = old[biases[0]].double() - 0.01 * g / (g.abs() + 1e-8)
+            R.check(layer.p[biases[0]], want, 2.0 ** -20 * (want.abs() + 0.01), n)
+            assert t is layer.p[biases[0]] and float(g.abs().max()) > 0
+        else:
+            assert not torch.equal(t, old[n]), n
+    if biases == ("b_router", "logit_bias"):
+        assert torch.equal(layer.p["logit_bias"], old["logit_bias"])
+
+
 # ----------------------------------------------------------------------- experts
 def test_output_biases_of_more_row_tiles_than_a_grid_dimension_holds():
     """bf16 MLP experts on 8.4 M rows: 65625 tiles of 128. dy holds small whole numbers, so
