@@ -768,10 +768,17 @@ class AdamW:
             moved = [i for i, p in enumerate(self.params) if p.data_ptr() != self._addresses[i]]
             raise ValueError(f"parameter {moved[0]} has another storage than when the optimizer "
                              "was made")
-        if ([g.shape for g in grads] != self._shapes
-                or list(map(torch.Tensor.get_device, grads)) != self._devices
-                or not all(map(torch.Tensor.is_contiguous, grads))):
+        try:
+            fit = ([g.shape for g in grads] == self._shapes
+                   and list(map(torch.Tensor.get_device, grads)) == self._devices
+                   and all(map(torch.Tensor.is_contiguous, grads)))
+        except (AttributeError, TypeError):  # no tensor: None where nothing was computed
+            fit = False
+        if not fit:
             for i, (g, p) in enumerate(zip(grads, self.params)):  # which one
+                if not isinstance(g, torch.Tensor):
+                    raise ValueError(f"gradient {i} is missing" if g is None else
+                                     f"gradient {i} is no tensor")
                 check_tensor(g, p.shape, g.dtype, f"gradient {i}", self.device)
         dtypes = [g.dtype for g in grads]
         if dtypes != self._grad_dtypes:

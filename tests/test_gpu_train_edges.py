@@ -44,6 +44,17 @@ def test_adamw_refuses_a_parameter_whose_storage_was_replaced():
         R.check(ps[1], rp, 2.0 ** -20 * rp.abs() + 1e-12, "p")
 
 
+def test_adamw_names_a_gradient_that_is_missing():
+    ps, gs, opt = _adam_case([100, 31], torch.float32, torch.float32, 32, False, 4)
+    was = [p.clone() for p in ps]
+    named = B.AdamW({"a": ps[0], "b": ps[1]})
+    for call in (lambda: opt.step([gs[0], None]), lambda: named.step({"a": gs[0], "b": None}),
+                 lambda: opt.step([gs[0], gs[1].cpu().numpy()])):
+        with pytest.raises(ValueError, match="gradient 1"):
+            call()
+    assert opt.t == named.t == 0 and all(torch.equal(p, w) for p, w in zip(ps, was))
+
+
 @pytest.mark.parametrize("bits", [32, 8])
 def test_adamw_state_cannot_be_pulled_from_under_it(bits):
     """The state's tensors cannot be exchanged, and what happens to them leaves the memory that
