@@ -472,11 +472,17 @@ class MoELayer:
     # ------------------------------------------------------------ the training step
     @property
     def bws(self) -> torch.Tensor:
-        """The workspace of the gradients, made at the first use (so make that use before
-        a capture). Calls that share it must not overlap."""
+        """The workspace of the gradients, made at the first use, and ready on every stream from
+        then on. Calls that share it must not overlap. In a capture it cannot be made (the
+        captured initialisation would not have run): make that use before."""
         if self._bws is None:
             with torch.cuda.device(self.ws.device):
-                self._bws = new_workspace(self.cfg, self.ws.device, backward=True)
+                if torch.cuda.is_current_stream_capturing():
+                    raise RuntimeError("the gradients' workspace must be made before a capture: "
+                                       "read layer.bws first")
+                ws = new_workspace(self.cfg, self.ws.device, backward=True)
+                torch.cuda.current_stream().synchronize()
+                self._bws = ws
         return self._bws
 
     def _call(self, name: str, *args):

@@ -121,6 +121,38 @@ def test_steps_with_nothing_between_them(name, how):
         assert torch.equal(a, b)
 
 
+def test_the_gradients_workspace_is_made_outside_a_capture():
+    layer, x, taps, dy = _forward(synth.SMALL["mixtral_small"], 5)
+    dx, gr = torch.empty_like(x), layer.new_grads()
+    graph, one = torch.cuda.CUDAGraph(), torch.zeros(1, device=DEV)
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        one.add_(1)
+        with pytest.raises(RuntimeError, match="before a capture"):
+            layer.backward(x, dy, taps, dx=dx, grads=gr)
+    graph.replay()
+    assert float(one) == 1
+    layer.bws
+    with torch.cuda.graph(graph2 := torch.cuda.CUDAGraph()):
+        layer.backward(x, dy, taps, dx=dx, grads=gr)
+    graph2.replay()
+    dx2, g2 = layer.backward(x, dy, taps)
+    assert torch.equal(dx, dx2) and all(torch.equal(gr[n], g2[n]) for n in gr)
+    assert layer.last_backward_error() == (0, 0)
+
+
+def test_the_gradients_workspace_is_ready_on_every_stream():
+    """Made on a stream that is behind, it is initialised all the same when another uses it."""
+    layer, x, taps, dy = _forward(synth.SMALL["mixtral_small"], 5)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)     # some 10 ms of clocks
+        layer.bws
+        assert side.query()
+    assert layer.last_backward_error() == (0, 0)
+
+
 @pytest.mark.parametrize("name,biases", [("switch_small", ("logit_bias",)), ("tiny", ("b_router",)),
                                          ("router_e20", ("b_router", "logit_bias")),
                                          ("mixtral_small", ())])
