@@ -636,8 +636,8 @@ class MoELayer:
 
     def _device_error(self, ws):
         code, info = ctypes.c_int32(0), ctypes.c_int32(0)
-        st = self.lib.moe_last_device_error(_ptr(ws), ctypes.byref(code), ctypes.byref(info),
-                                            _stream())
+        st = _on_device(self._index, self.lib.moe_last_device_error, _ptr(ws),
+                        ctypes.byref(code), ctypes.byref(info))
         if st not in (MOE_OK, 6):
             raise MoeError(st, "moe_last_device_error")
         return code.value, info.value

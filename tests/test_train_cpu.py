@@ -332,6 +332,25 @@ def test_binding_checks_tensors():
         B.AdamW([x])
 
 
+def test_errors_are_read_on_the_layers_own_device(monkeypatch):
+    """The gradients run on the layer's device whichever is current; their errors are read
+    there too, on that device's stream."""
+    layer, seen = object.__new__(B.MoELayer), []
+
+    class Lib:
+        @staticmethod
+        def moe_last_device_error(ws, code, info, stream):
+            seen.append(stream)
+            code._obj.value, info._obj.value = 2, 5
+            return 6
+
+    layer.lib, layer._index = Lib, 3
+    layer.ws = layer._bws = torch.zeros(64, dtype=torch.uint8)
+    monkeypatch.setattr(B, "_on_device", lambda index, call, *a: call(*a, ("stream of", index)))
+    assert layer.last_backward_error() == layer.last_device_error() == (2, 5)
+    assert seen == [("stream of", 3)] * 2
+
+
 def _kernels_launched_ahead():
     """(name, body before the first wait) of every kernel that calls pdl_wait()."""
     csrc = os.path.join(ROOT, "sparse_mixture_experts_12_b200", "csrc")
