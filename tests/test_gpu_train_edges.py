@@ -7,6 +7,7 @@ import torch
 from sparse_mixture_experts_12_b200 import binding as B
 from sparse_mixture_experts_12_b200 import build as BUILD
 from sparse_mixture_experts_12_b200 import synth
+from tests import test_gpu_train as G
 from tests import train_ref as R
 from tests.test_gpu_train import DEV, _adam_case, _forward, _gen, _rand, _workload
 
@@ -206,4 +207,49 @@ def test_output_biases_of_more_row_tiles_than_a_grid_dimension_holds():
                              wl.act, b)
         R.check(dx[r], ref["dx"], lim["dx"], "dx")
         R.check(gr["b1"][e], ref["b1"][0], lim["b1"][0], "b1")
+    assert layer.last_backward_error() == (0, 0)
+
+
+def _fp32_tiles(d, F, rows):
+    """(rows of a row tile, rows and columns of a tile of the weights' gradients) that the fp32
+    experts' dispatch takes."""
+    n, E = sum(rows), len(rows)
+    tile = 8 if n <= 8 * E else (32 if n < 64 * E else 128)
+    m = E * -(-F // 128)
+    if tile == 128 and m * -(-d // 128) >= 296:
+        return tile, (128, 128)
+    return tile, ((128, 64) if m * -(-d // 64) >= 148 else (32, 64))
+
+
+WIDE = [  # d, F, rows per expert, tiles: widths that end in either 64-column half of a tile
+    (580, 1924, [70, 200, 130, 65], (128, (128, 128))), (580, 1923, [70, 200, 130, 65], (128, (128, 128))),
+    (1220, 1137, [129, 1, 0, 300], (128, (128, 128))), (1028, 2500, [128, 190], (128, (128, 128))),
+    (300, 1100, [70, 200, 130, 65], (128, (128, 64))), (300, 1101, [70, 200, 130, 65], (128, (128, 64))),
+    (260, 520, [30] * 9 + [0, 64, 1, 33, 40, 32, 31], (32, (128, 64))),
+    (260, 521, [30] * 9 + [0, 64, 1, 33, 40, 32, 31], (32, (128, 64))),
+    (64, 193, [i % 5 for i in range(100)], (8, (128, 64))),
+]
+
+
+@pytest.mark.parametrize("act", G.ACTS, ids=["relu", "gelu", "swiglu"])
+@pytest.mark.parametrize("d,F,rows,tiles", WIDE)
+def test_fp32_experts_of_every_tile(d, F, rows, tiles, act):
+    assert _fp32_tiles(d, F, rows) == tiles
+    G.test_expert_ffn_backward(d, F, rows, act, synth.DT_F32)
+
+
+@pytest.mark.parametrize("act", [synth.ACT_GELU, synth.ACT_SWIGLU], ids=["gelu", "swiglu"])
+def test_fp32_layer_of_wide_experts(act):
+    """The whole layer through the widest fp32 tiles, the shared experts' too."""
+    T, d, E, k, F, Fs = 220, 1028, 4, 2, 1156, 2150
+    assert _fp32_tiles(d, F, [T * k // E] * E)[1] == _fp32_tiles(d, 2 * Fs, [T])[1] == (128, 128)
+    wl = _workload(T, d, E, k, synth.DT_F32, F=F, act=act, n_shared=2, d_ff_shared=Fs,
+                   expert_bias=act == synth.ACT_GELU, bias_std=0.2, router_bias=True)
+    layer, x, taps, dy = _forward(wl, 9)
+    dl = torch.tensor([3.0, 0.2], device=DEV)
+    dx, gr = layer.backward(x, dy, taps, d_losses=dl)
+    ref, lim = R.layer_bwd(x, dy, taps, layer.p, wl, dl)
+    for n, t in {"dx": dx, **gr}.items():
+        R.check(t, ref[n], lim[n], n)
+        R.check_norm(t, ref[n], torch.float32, n)
     assert layer.last_backward_error() == (0, 0)
