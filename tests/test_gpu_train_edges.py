@@ -253,3 +253,55 @@ def test_fp32_layer_of_wide_experts(act):
         R.check(t, ref[n], lim[n], n)
         R.check_norm(t, ref[n], torch.float32, n)
     assert layer.last_backward_error() == (0, 0)
+
+
+@pytest.mark.parametrize("name", ["tiny", "mixtral_small", "deepseek_small", "switch_small", "fp32_gelu_cap"])
+def test_layer_whose_capacity_drops_everything(name):
+    """No expert has a row: their gradients are zero, x's is the losses' and the shared
+    experts' (each token's gates have none)."""
+    wl = synth.SMALL[name].replace(capacity_factor=1e-6)
+    layer, x, taps, dy = _forward(wl, 4)
+    assert (taps["inv"] == -1).all() and int(taps["offsets"][-1]) == 0
+    for losses in (None, torch.tensor([3.0, 0.2], device=DEV)):
+        layer.bws[64:].fill_(255)
+        dx, gr = layer.backward(x, dy, taps, d_losses=losses)
+        ref, lim = R.layer_bwd(x, dy, taps, layer.p, wl, losses)
+        for n, t in {"dx": dx, **gr}.items():
+            R.check(t, ref[n], lim[n], n)
+        assert all((gr[n] == 0).all() for n in ("w1", "w3", "w2", "b1", "b2") if n in gr)
+    assert layer.last_backward_error() == (0, 0)
+
+
+@pytest.mark.parametrize("E,dt", [(8, synth.DT_BF16), (12, synth.DT_BF16), (100, synth.DT_BF16),
+                                  (8, synth.DT_F32), (40, synth.DT_F32)])
+def test_route_backward_keeps_infinities_to_their_column_and_token(E, dt):
+    """An infinite weight or activation spoils its column of dx or dW (to infinity or NaN), a
+    token without finite logits its row of dx; nothing else changes."""
+    T, d, k = 300, 320, 2
+    wl, layer, x, z, idx, counts, dg, _ = G._route_case(T, d, E, k, dt, 0, 5)
+    full = lambda z: (torch.empty_like(z), torch.empty(T, d, device=DEV), layer.new_grads())  # noqa: E731
+    dz, dx, gr = full(z)
+    layer.route_backward(x, z, idx, None, dg, None, dz, dx, gr)
+    x2 = x.clone()
+    x2[7, 33] = float("inf")
+    layer.p["w_router"][E - 1, 100] = float("-inf")
+    dz2, dx2, g2 = full(z)
+    layer.route_backward(x2, z, idx, None, dg, None, dz2, dx2, g2)
+    cols = torch.arange(d, device=DEV)
+    assert torch.equal(dz2, dz) and torch.equal(g2["b_router"], gr["b_router"])
+    assert torch.equal(dx2[:, cols != 100], dx[:, cols != 100])
+    assert torch.equal(g2["w_router"][:, cols != 33], gr["w_router"][:, cols != 33])
+    hit = idx[7].long()                       # the experts that token chose
+    assert not torch.isfinite(g2["w_router"][hit, 33].float()).any()
+    assert not torch.isfinite(dx2[(idx == E - 1).any(1), 100]).any()
+    layer.p["w_router"][E - 1, 100] = 0.25
+    z2 = z.clone()
+    z2[9, idx[9, 0].long()] = float("nan")
+    dz, dx, gr = full(z)
+    layer.route_backward(x, z, idx, None, dg, None, dz, dx, gr)
+    dz2, dx2, g2 = full(z)
+    layer.route_backward(x, z2, idx, None, dg, None, dz2, dx2, g2)
+    rows = torch.arange(T, device=DEV) != 9
+    assert torch.equal(dz2[rows], dz[rows]) and torch.equal(dx2[rows], dx[rows])
+    assert torch.isnan(dx2[9]).all()
+    assert layer.last_backward_error() == (0, 0)
