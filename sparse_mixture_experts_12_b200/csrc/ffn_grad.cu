@@ -322,21 +322,31 @@ __global__ void __launch_bounds__(kThreads, TW::BN == 128 ? 2 : 0)
   }
   x -= p.dx;
   if (x < p.dw) {
-    int j = 0;
-    while (x >= s.G * p.tiles[j]) {
-      x -= s.G * p.tiles[j];
-      ++j;
-    }
-    const int g = x / p.tiles[j], t = x % p.tiles[j];
-    const int M = p.M[j], N = p.N[j], nt = ceil_div(N, TW::BN);
-    const int m0 = t / nt * TW::BM, n0 = t % nt * TW::BN;
-    const size_t row0 = (size_t)s.offsets[g];
-    float acc[TW::TM][TW::TN];
-    clear(acc);
-    mma_tile<TW, true, VEC>(sm.w, acc, p.a[j] + row0 * M + m0, M, M - m0, p.b[j] + row0 * N + n0, N,
-                            N - n0, s.offsets[g + 1] - s.offsets[g]);
-    store_tile<TW, VEC>(acc, p.c[j] + ((size_t)g * M + m0) * N + n0, N, min(TW::BM, M - m0),
-                        min(TW::BN, N - n0));
+    // in parts of kSumRows rows (see sum_rows); the tile is worked out anew for each, so that
+    // nothing but its number stays in a register beside the sums (the layer of 191 rows of
+    // 3152 x 8764 takes 1394 us so, 1435 through sum_rows, 1382 with one sum)
+    int k0 = 0, left;
+    do {
+      int y = x;
+      asm volatile("" : "+r"(y));
+      int j = 0;
+      while (y >= s.G * p.tiles[j]) {
+        y -= s.G * p.tiles[j];
+        ++j;
+      }
+      const int g = y / p.tiles[j], t = y % p.tiles[j];
+      const int M = p.M[j], N = p.N[j], nt = ceil_div(N, TW::BN);
+      const int m0 = t / nt * TW::BM, n0 = t % nt * TW::BN;
+      const size_t row0 = (size_t)s.offsets[g] + k0;
+      left = s.offsets[g + 1] - (int)row0;
+      float acc[TW::TM][TW::TN];
+      clear(acc);
+      mma_tile<TW, true, VEC>(sm.w, acc, p.a[j] + row0 * M + m0, M, M - m0, p.b[j] + row0 * N + n0,
+                              N, N - n0, min(left, kSumRows));
+      store_tile<TW, VEC>(acc, p.c[j] + ((size_t)g * M + m0) * N + n0, N, min(TW::BM, M - m0),
+                          min(TW::BN, N - n0), k0 > 0);
+      k0 += kSumRows;
+    } while (left > kSumRows);
     return;
   }
   reduce<float>(s, q, x - p.dw);

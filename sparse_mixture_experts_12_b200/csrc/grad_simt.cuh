@@ -202,10 +202,10 @@ __device__ __forceinline__ void mma_tile(GemmSmem<T> &s, float (&acc)[T::TM][T::
   }
 }
 
-// c: the tile's first element
+// c: the tile's first element; `add`: to what the same thread stored there before
 template <class T, bool VEC>
 __device__ __forceinline__ void store_tile(const float (&acc)[T::TM][T::TN], float *c, size_t ldc,
-                                           int rows, int cols) {
+                                           int rows, int cols, bool add = false) {
   constexpr int TC = T::TC;
   const int tx = threadIdx.x % T::TX, ty = threadIdx.x / T::TX;
 #pragma unroll
@@ -219,17 +219,48 @@ __device__ __forceinline__ void store_tile(const float (&acc)[T::TM][T::TN], flo
       const float *v = &acc[i][g * TC];
       if constexpr (VEC) {
         if (n <= 0) continue;
-        if constexpr (TC == 4)
-          *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
-        else
-          *reinterpret_cast<float2 *>(p) = make_float2(v[0], v[1]);
+        if constexpr (TC == 4) {
+          float4 o = make_float4(v[0], v[1], v[2], v[3]);
+          if (add) {
+            const float4 q = *reinterpret_cast<const float4 *>(p);
+            o = make_float4(q.x + o.x, q.y + o.y, q.z + o.z, q.w + o.w);
+          }
+          *reinterpret_cast<float4 *>(p) = o;
+        } else {
+          float2 o = make_float2(v[0], v[1]);
+          if (add) {
+            const float2 q = *reinterpret_cast<const float2 *>(p);
+            o = make_float2(q.x + o.x, q.y + o.y);
+          }
+          *reinterpret_cast<float2 *>(p) = o;
+        }
       } else {
 #pragma unroll
         for (int j = 0; j < TC; ++j)
-          if (j < n) p[j] = v[j];
+          if (j < n) p[j] = add ? p[j] + v[j] : v[j];
       }
     }
   }
+}
+
+// Rows in one running sum of a weight's gradient: the fp32 error of a sum grows with the root
+// of its length, and a tile's read and write for each part are few beside its products' reads.
+// (65536 rows: 4.6e-6 of the result in one sum, 6.7e-7 in parts.)
+constexpr int kSumRows = 1024;
+// c = A^T B over K rows, in such parts, which the tile's threads add up in c
+template <class T, bool VEC, bool VECC>
+__device__ __forceinline__ void sum_rows(GemmSmem<T> &s, const float *a, size_t lda, int rows,
+                                         const float *b, size_t ldb, int cols, int K, float *c,
+                                         size_t ldc) {
+  int k0 = 0;
+  do {
+    float acc[T::TM][T::TN];
+    clear(acc);
+    mma_tile<T, true, VEC>(s, acc, a + (size_t)k0 * lda, lda, rows, b + (size_t)k0 * ldb, ldb, cols,
+                           min(kSumRows, K - k0));
+    store_tile<T, VECC>(acc, c, ldc, min(T::BM, rows), min(T::BN, cols), k0 > 0);
+    k0 += kSumRows;
+  } while (k0 < K);
 }
 
 }  // namespace simt

@@ -520,11 +520,11 @@ __global__ void __launch_bounds__(simt::kThreads) k_proj_tiles(RouteBwdArgs a, f
   pdl_trigger();
   const float *x = static_cast<const float *>(a.x), *w = static_cast<const float *>(a.w);
   const int nt = ceil_div(a.d, simt::BN), E = a.E, d = a.d;
-  float acc[T::TM][4];
-  simt::clear(acc);
   int b = blockIdx.x;
   if (b < dx_blocks) {
     const int m0 = b / nt * T::BM, n0 = b % nt * simt::BN;
+    float acc[T::TM][T::TN];
+    simt::clear(acc);
     simt::mma_tile<T, false, VEC>(sm, acc, a.dlogits + (size_t)m0 * E, E, a.T - m0, w + n0, d,
                                   d - n0, E);
     simt::store_tile<T, true>(acc, a.dx + (size_t)m0 * d + n0, d, min(T::BM, a.T - m0),
@@ -536,10 +536,9 @@ __global__ void __launch_bounds__(simt::kThreads) k_proj_tiles(RouteBwdArgs a, f
   b -= piece * mt * nt;
   const int m0 = b / nt * T::BM, n0 = b % nt * simt::BN;
   const int t0 = min(a.T, piece * per), n = min(a.T - t0, per);
-  simt::mma_tile<T, true, VEC>(sm, acc, a.dlogits + (size_t)t0 * E + m0, E, E - m0,
-                               x + (size_t)t0 * d + n0, d, d - n0, n);
-  simt::store_tile<T, true>(acc, dw_part + ((size_t)piece * E + m0) * d + n0, d,
-                            min(T::BM, E - m0), min(simt::BN, d - n0));
+  simt::sum_rows<T, VEC, true>(sm, a.dlogits + (size_t)t0 * E + m0, E, E - m0,
+                               x + (size_t)t0 * d + n0, d, d - n0, n,
+                               dw_part + ((size_t)piece * E + m0) * d + n0, d);
 }
 
 cudaError_t route_bwd_simt(const RouteBwdArgs &a, cudaStream_t st) {

@@ -305,3 +305,31 @@ def test_route_backward_keeps_infinities_to_their_column_and_token(E, dt):
     assert torch.equal(dz2[rows], dz[rows]) and torch.equal(dx2[rows], dx[rows])
     assert torch.isnan(dx2[9]).all()
     assert layer.last_backward_error() == (0, 0)
+
+
+# A running fp32 sum of n products of random sign is off by about U sqrt(n / 6) of its result
+# (each rounding at most U of a partial sum whose size grows with the root of its length). The
+# weights' gradients are sums of at most 1024, and of these parts.
+def _sums(n, *others):
+    return 2.0 ** -24 * (sum((m / 6) ** 0.5 for m in (min(n, 1024), n / 1024, *others)) + 8)
+
+
+def test_fp32_weight_gradients_over_many_rows():
+    n, d, F = 32768, 64, 64
+    wl, layer, x, dy, off, n = G._ffn_case(d, F, [n, 5], synth.ACT_GELU, synth.DT_F32, 1)
+    gr = layer.new_grads()
+    layer.expert_ffn_backward(x, off, dy, None, gr)
+    ref, _ = R.ffn_bwd(x, dy, off.tolist(), layer.p, wl.act, torch.float32)
+    for m in ("w1", "w2"):  # the activations behind them are sums over d
+        off_by = float((gr[m][0].double() - ref[m][0]).norm() / ref[m][0].norm())
+        assert off_by <= _sums(n, d, d), f"{m}: {off_by:.2e}"
+
+
+def test_fp32_router_gradient_over_many_tokens():
+    T, d, E, k = 65536, 4096, 20, 2
+    wl, layer, x, z, idx, counts, dg, _ = G._route_case(T, d, E, k, synth.DT_F32, 2, 3)
+    dz, gr = torch.empty_like(z), layer.new_grads()
+    layer.route_backward(x, z, idx, None, dg, None, dz, None, gr)
+    ref = dz.double().T @ x.double()
+    off_by = float((gr["w_router"].double() - ref).norm() / ref.norm())
+    assert off_by <= _sums(T // 4, 4), f"{off_by:.2e}"
