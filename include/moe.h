@@ -49,7 +49,8 @@
  *   moe_last_device_error(). A kernel that detects one skips the offending
  *   access instead of faulting.
  * - Workspace: one buffer of moe_workspace_size() bytes serves every entry point
- *   of a configuration (the gradients have one of their own). Zero it once with moe_workspace_init() before first use.
+ *   of a configuration (the gradients have one of their own). Zero it once with
+ *   moe_workspace_init() before first use.
  *   Calls that share a workspace must not overlap on the GPU.
  */
 #ifndef MOE_H_
@@ -479,7 +480,9 @@ moe_status_t moe_permute_backward(const moe_cfg_t *cfg, const void *dx_perm, con
  * NULL: the upstream gradients of aux and z_loss (counts [E], before drops, is read only
  * with it; f is held fixed). Out, each may be NULL: dlogits [T, E] fp32, dx [T, d] fp32
  * (dlogits W_r, the addend of moe_permute_backward), grads->w_router, grads->b_router
- * (grads itself may be NULL). The selection has no gradient. */
+ * (grads itself may be NULL). The selection has no gradient. bf16 layers of more than 8
+ * experts take dz as a sum of bf16 terms: an infinite entry of w_router makes its column of
+ * dx, one of x its column of the weights' gradient infinite or NaN. */
 moe_status_t moe_route_backward(const moe_cfg_t *cfg, const moe_weights_t *w, const void *x,
                                 const float *logits, const int32_t *topk_idx,
                                 const int32_t *counts, const float *dgate,
@@ -546,13 +549,14 @@ typedef struct {
 /* One AdamW step over n_tensors tensors (decoupled weight decay, bias correction):
  *   m = b1 m + (1 - b1) g;  v = b2 v + (1 - b2) g^2
  *   p = p (1 - lr wd) - lr m / (1 - b1^t) / (sqrt(v / (1 - b2^t)) + eps)
- * in fp32, every product and sum of m and v rounded by itself. state_bits 8: m = exp_avg * exp_avg_scale and sqrt(v) = exp_avg_sq *
- * exp_avg_sq_scale, the scale the block's largest magnitude / 448 (at least 2^-100 /
- * 448); the parameter's step uses the new m and v before their rounding to e4m3, and a
- * nonzero sqrt(v) keeps at least the smallest code. A gradient that is not finite
- * spoils its element (an infinite one with 8-bit states its block): found_inf is there
- * to skip such a step. `tensors` and `opt` are host memory, read before the call returns.
- * No workspace. Tensors must not overlap. */
+ * in fp32, every product and sum of m and v rounded by itself. state_bits 8:
+ * m = exp_avg * exp_avg_scale and sqrt(v) = exp_avg_sq * exp_avg_sq_scale, the scale the
+ * block's largest magnitude / 448 (at least 2^-100 / 448); the parameter's step uses the
+ * new m and v before their rounding to e4m3, and a nonzero sqrt(v) keeps at least the
+ * smallest code. A gradient that is not finite spoils its element (an infinite one with
+ * 8-bit states its block): found_inf is there to skip such a step. `tensors` and `opt` are
+ * host memory, read before the call returns. No workspace. Tensors must not overlap; one of
+ * more than 2048 (2^31 - 1) elements is MOE_ERR_UNSUPPORTED. */
 moe_status_t moe_adamw_step(const moe_adamw_tensor_t *tensors, int32_t n_tensors,
                             const moe_adamw_t *opt, moe_stream_t stream);
 

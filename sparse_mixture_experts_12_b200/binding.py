@@ -757,9 +757,10 @@ class AdamW:
         """One step from ``grads``: a list in the parameters' order, or a dict with an entry for
         each name of a dict of parameters (others are left alone).
         Device scalars, read when the kernel runs: ``grad_scale`` multiplies the gradients,
-        ``found_inf`` nonzero skips the update (the step still counts), ``step`` (int64) and
-        ``lr`` (fp32) take the place of the counter and of self.lr (a captured step needs
-        them to move)."""
+        ``found_inf`` nonzero skips the update (the step still counts: a program that counts
+        updates only passes its own ``step``), ``step`` (int64) and ``lr`` (fp32) take the place
+        of the counter and of self.lr (a captured step needs them to move, and the program's
+        count is then the one to save: self.t moves with calls, not with replays)."""
         if isinstance(grads, dict):
             if self.names is None or any(n not in grads for n in self.names):
                 raise ValueError("a dict of gradients needs the names of a dict of parameters")

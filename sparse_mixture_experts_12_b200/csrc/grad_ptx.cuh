@@ -53,8 +53,9 @@ inline bool make_map_ld(CUtensorMap *map, const void *ptr, uint64_t rows, uint64
   return r == CUDA_SUCCESS;
 }
 
-// The bf16 matrix (rows `ld` elements apart, 0: cols) as [cols / 64, rows, 64]: a box of two 64-column blocks of 64 rows
-// lands block after block (the layout of sw128_desc_mn). cols: a multiple of 64.
+// The bf16 matrix (rows `ld` elements apart, 0: cols) as [cols / 64, rows, 64]: a box of two
+// 64-column blocks of 64 rows lands block after block (the layout of sw128_desc_mn). cols: a
+// multiple of 64.
 inline bool make_mn_map(CUtensorMap *map, const void *ptr, uint64_t rows, uint64_t cols,
                         uint64_t ld = 0) {
   auto fn = encode_fn();

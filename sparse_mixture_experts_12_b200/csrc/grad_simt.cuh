@@ -177,8 +177,8 @@ struct GemmSmem {
 // columns of B inside
 template <class T, bool AT, bool VEC>
 __device__ __forceinline__ void mma_tile(GemmSmem<T> &s, float (&acc)[T::TM][T::TN],
-                                         const float *a, size_t lda, int rows, const float *b, size_t ldb, int cols,
-                                         int K) {
+                                         const float *a, size_t lda, int rows, const float *b,
+                                         size_t ldb, int cols, int K) {
   const int tx = threadIdx.x % T::TX, ty = threadIdx.x / T::TX;
   Slice<T::BM, T::BK, T::LDA, !AT, VEC> sa;
   Slice<T::BN, T::BK, T::LDB, false, VEC> sb;

@@ -607,8 +607,9 @@ cudaError_t route_bwd_tc(const RouteBwdArgs &a, cudaStream_t st) {
 
 // Whether the one pass of k_route_proj takes the products. Against the tensor cores (bf16,
 // T = 4096, d = 4096): 36 us to 39 with 8 experts, 63 to 39 with 12, 167 to 40 with 32.
-// Against the tiles on CUDA cores (fp32): 43 us to 142 with 8 and 62 to 142 with 16, but 163
-// to 156 with 32, where a thread's registers hold half the columns.
+// Against the tiles on CUDA cores (fp32): 41 us with 8 and 60 with 16, where the tiles take 130
+// (20 experts; 156 with 17, whose rows are not vectors), but 163 to 131 with 32, where a
+// thread's registers hold half the columns.
 static bool few_experts(int E, int dtype) { return E <= (dtype == MOE_DTYPE_F32 ? 16 : 8); }
 
 bool route_bwd_reads_dlogits(int E, int dtype) {

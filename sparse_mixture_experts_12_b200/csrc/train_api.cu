@@ -9,8 +9,8 @@ namespace {
 
 enum Buf {
   G_ERR, G_OFFSETS, G_MPREFIX, G_PRE256, G_POFF, G_SH, G_H, G_DG, G_DU,
-  G_COL, G_COL2, G_DLOGITS, G_ROUTE, G_X, G_DY, G_INV, G_DX, G_DX_PART, G_ROW_W, G_ROW_DOT, G_DOT_PART, G_DX_ROUTER,
-  G_DX_SHARED, G_NBUF
+  G_COL, G_COL2, G_DLOGITS, G_ROUTE, G_X, G_DY, G_INV, G_DX, G_DX_PART, G_ROW_W, G_ROW_DOT,
+  G_DOT_PART, G_DX_ROUTER, G_DX_SHARED, G_NBUF
 };
 
 struct Layout {
