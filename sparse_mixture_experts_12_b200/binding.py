@@ -743,10 +743,11 @@ class AdamW:
                                       MoeAdamWTensor.grad_dtype.offset,
                                       (ctypes.sizeof(MoeAdamWTensor),))
         self._grad_dtypes = None  # the types that _grad_types holds
-        # what the addresses above point to: the parameters' are compared at every step, the
-        # state's memory is kept by aliases of our own, whatever is done to its tensors
+        # what the addresses above point to is kept by aliases of our own, whatever is done to the
+        # tensors; the parameters' addresses are compared at every step (and no other tensor
+        # can get one of them meanwhile)
         self._addresses = [p.data_ptr() for p in self.params]
-        self._held = [x.detach() for xs in lists for x in xs if x is not None]
+        self._held = [x.detach() for xs in (self.params, *lists) for x in xs if x is not None]
         self._shapes = [p.shape for p in self.params]
         self._devices = [p.get_device() for p in self.params]
         self._index = self.params[0].get_device()

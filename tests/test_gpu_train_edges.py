@@ -45,6 +45,21 @@ def test_adamw_refuses_a_parameter_whose_storage_was_replaced():
         R.check(ps[1], rp, 2.0 ** -20 * rp.abs() + 1e-12, "p")
 
 
+def test_adamw_sees_a_replacement_of_the_freed_block():
+    """A smaller tensor that takes the old storage's block is not taken for the parameter."""
+    n = 8 << 20                                       # 32 MB: a block of its own
+    p = torch.zeros(n, device=DEV)
+    opt, g = B.AdamW([p]), torch.ones(n, device=DEV)
+    torch.cuda.synchronize()
+    p.data = torch.empty(0, device=DEV)
+    small = torch.full((6 << 20,), 7.0, device=DEV)   # the allocator gives freed blocks first
+    other = torch.full((2 << 20,), 7.0, device=DEV)
+    p.data = small
+    with pytest.raises(ValueError, match="parameter 0"):
+        opt.step([g])
+    assert (small == 7).all() and (other == 7).all()
+
+
 def test_adamw_names_a_gradient_that_is_missing():
     ps, gs, opt = _adam_case([100, 31], torch.float32, torch.float32, 32, False, 4)
     was = [p.clone() for p in ps]
