@@ -290,7 +290,8 @@ class MoELayer:
 
     ``params`` is the dict of ``synth.generate`` (CPU or CUDA tensors); they are
     moved to ``device`` once. ``forward`` runs the whole layer through
-    ``moe_forward`` on the current stream.
+    ``moe_forward`` on the current stream. The layer works on the storage that the tensors
+    of ``p`` have then: new values are written into them (``copy_``, an optimizer step).
     """
 
     def __init__(self, workload: synth.Workload, params: dict, device="cuda"):
@@ -300,6 +301,8 @@ class MoELayer:
         self.p = {k: (None if v is None else v.to(self.device).contiguous())
                   for k, v in params.items() if k != "x"}
         self.weights = MoeWeights(**{k: _ptr(self.p.get(k)) for k, _ in MoeWeights._fields_})
+        # what these addresses point to, whatever becomes of the entries of p
+        self._held = [v.detach() for v in self.p.values() if v is not None]
         self.ws = new_workspace(self.cfg, self.device)
         self.lib = load()
         self._bws = None

@@ -169,6 +169,21 @@ def test_the_gradients_workspace_is_ready_on_every_stream():
     assert layer.last_backward_error() == (0, 0)
 
 
+def test_a_layers_weights_cannot_be_pulled_from_under_it():
+    """The layer reads and differentiates the storage it was made with, whose memory stays."""
+    layer, x, taps, dy = _forward(synth.SMALL["mixtral_small"], 6)
+    y, (dx, gr) = layer.forward(x), layer.backward(x, dy, taps)
+    sizes = {n: t.numel() for n, t in layer.p.items() if t is not None}
+    layer.p["w1"].data = torch.empty(0, dtype=x.dtype, device=DEV)
+    layer.p["w2"] = layer.p["w3"] = None
+    torch.cuda.empty_cache()
+    keep = [torch.full((n,), float("nan"), dtype=x.dtype, device=DEV) for n in sizes.values()]
+    assert torch.equal(layer.forward(x), y)
+    dx2, g2 = layer.backward(x, dy, taps, grads={"w_router": torch.empty_like(gr["w_router"])})
+    assert torch.equal(dx2, dx) and torch.equal(g2["w_router"], gr["w_router"])
+    assert all(torch.isnan(t).all() for t in keep)
+
+
 @pytest.mark.parametrize("name,biases", [("switch_small", ("logit_bias",)), ("tiny", ("b_router",)),
                                          ("router_e20", ("b_router", "logit_bias")),
                                          ("mixtral_small", ())])
